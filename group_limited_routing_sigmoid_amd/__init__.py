@@ -24,6 +24,7 @@ LIB_PATH = os.environ.get("BEAM_MOE_LIB") or os.path.join(_HERE, "libbeam_moe.so
 F32, BF16, FP8_E4M3, MXFP4 = 0, 1, 2, 3
 ROUTE_LOGITS_IN, PATH_STREAM, PATH_GROUPED = 1 << 0, 1 << 1, 1 << 2
 TILE_128, TILE_256, TILE_160, TILE_64 = 1 << 3, 1 << 4, 1 << 5, 1 << 6
+ROUTE_SOFTMAX, ROUTE_UNNORMED = 1 << 7, 1 << 8
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = 0, -1, -2, -3, -4
 
 SYMBOLS = ("beam_status_string", "beam_moe_validate", "beam_moe_workspace_bytes",
@@ -32,7 +33,7 @@ SYMBOLS = ("beam_status_string", "beam_moe_validate", "beam_moe_workspace_bytes"
            "beam_moe_timer_reset", "beam_moe_timer_count", "beam_moe_timer_read",
            "beam_moe_forward_timed", "beam_moe_bias_update", "beam_moe_bias_gamma",
            "beam_moe_forward_residual", "beam_moe_quant_mxfp8",
-           "beam_moe_forward_noalloc")
+           "beam_moe_forward_noalloc", "beam_moe_route_backward")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -70,6 +71,7 @@ def lib():
         L.beam_moe_validate.argtypes = [D, i64]
         L.beam_moe_workspace_bytes.argtypes = [D, i64, ctypes.POINTER(sz)]
         L.beam_moe_route.argtypes = [D, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.beam_moe_route_backward.argtypes = [D, i64, vp, vp, vp, vp, vp]
         L.beam_moe_permute.argtypes = [D, i64, vp, vp, vp, vp, vp, vp, sz, vp]
         L.beam_moe_quant_e4m3.argtypes = [i64, i64, i32, vp, vp, vp, vp]
         L.beam_moe_quant_mxfp8.argtypes = [i64, i64, i32, vp, vp, vp, vp]
@@ -205,12 +207,51 @@ def _alloc_on(stream):
     return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
+def _arg(name: str, t: torch.Tensor, shape, *dtypes) -> int:
+    """Address of a contiguous GPU tensor of the given shape and one of the
+    given dtypes; raises ValueError otherwise."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensors passed to the HIP library must be on the GPU")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected "
+                         + " or ".join(str(d) for d in dtypes))
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors passed to the HIP library must be contiguous")
+    return t.data_ptr()
+
+
+def _run(fn, what: str, stream, tensors, *args):
+    """Call a library entry point whose last argument is the stream, on the
+    device its tensors live on.  Inputs read on a stream that is not the
+    current one are marked as used there, so torch's allocator keeps their
+    memory until the kernels are done."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: tensors on cuda:{dev} and cuda:{t.get_device()}")
+    raw = torch._C._cuda_getCurrentRawStream(dev)
+    if stream is not None and stream.cuda_stream != raw:
+        if stream.device.index != dev:
+            raise ValueError(f"{what}: a stream of {stream.device} for tensors on cuda:{dev}")
+        raw = stream.cuda_stream
+        for t in tensors:
+            t.record_stream(stream)
+    if dev == torch._C._cuda_getDevice():
+        _check(fn(*args, raw), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, raw), what)
+
+
 def route(desc: Desc, x: Optional[torch.Tensor], w_router: Optional[torch.Tensor],
           bias: Optional[torch.Tensor] = None, logits: Optional[torch.Tensor] = None,
           workspace: Optional[Workspace] = None, stream=None):
     """beam_moe_route.  Returns (topk_idx [T,K] int32, topk_w [T,K] fp32,
     logits [T,E] fp32).  With ROUTE_LOGITS_IN in desc.flags, `logits` is the
-    input and x / w_router may be None."""
+    input and x / w_router may be None.  ROUTE_SOFTMAX and ROUTE_UNNORMED choose
+    the scores and the weights."""
     lin = bool(desc.flags & ROUTE_LOGITS_IN)
     ref = logits if lin else x
     T, dev = ref.shape[0], ref.device
@@ -219,11 +260,30 @@ def route(desc: Desc, x: Optional[torch.Tensor], w_router: Optional[torch.Tensor
         w = torch.empty(T, desc.top_k, dtype=torch.float32, device=dev)
         if logits is None:
             logits = torch.empty(T, desc.n_experts, dtype=torch.float32, device=dev)
-    buf, n = _ws(desc, T, workspace, dev, stream)
+    # routing from given logits uses no scratch memory
+    buf, n = (None, 0) if lin else _ws(desc, T, workspace, dev, stream)
     _check(lib().beam_moe_route(ctypes.byref(desc), T, _p(x), _p(w_router),
                                 _p(bias), _p(logits), _p(idx), _p(w), _p(buf),
                                 n, _stream(stream, dev)), "beam_moe_route")
     return idx, w, logits
+
+
+def route_backward(desc: Desc, logits: torch.Tensor, topk_idx: torch.Tensor,
+                   d_topk_w: torch.Tensor, out: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """beam_moe_route_backward: the gradient [T,E] fp32 of the logits from that
+    of the routing weights (the selection and the bias are constants)."""
+    T, E, K = logits.shape[0], desc.n_experts, desc.top_k
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty(T, E, dtype=torch.float32, device=logits.device)
+    _run(lib().beam_moe_route_backward, "beam_moe_route_backward", stream,
+         (logits, topk_idx, d_topk_w, out), ctypes.byref(desc), T,
+         _arg("logits", logits, (T, E), torch.float32),
+         _arg("topk_idx", topk_idx, (T, K), torch.int32),
+         _arg("d_topk_w", d_topk_w, (T, K), torch.float32),
+         _arg("out", out, (T, E), torch.float32))
+    return out
 
 
 def permute(desc: Desc, topk_idx: torch.Tensor,

@@ -58,6 +58,8 @@ int make_plan(const beam_moe_desc* d, int64_t T, Plan* p) {
   p->act = d->act_dtype;
   p->wdt = d->weight_dtype;
   p->flags = d->flags;
+  p->softmax = (d->flags & BEAM_ROUTE_SOFTMAX) != 0;
+  p->normed = (d->flags & BEAM_ROUTE_UNNORMED) == 0;
   p->T = T;
   p->S = T * d->top_k;
   p->nb = ceil_div(T, kPermBlock);
@@ -203,7 +205,8 @@ const char* beam_status_string(int status) {
 int beam_moe_validate(const beam_moe_desc* d, int64_t T) {
   if (!d || T < 0) return BEAM_ERR_INVALID_ARG;
   const uint32_t tiles = BEAM_TILE_64 | BEAM_TILE_128 | BEAM_TILE_160 | BEAM_TILE_256;
-  const uint32_t known = BEAM_ROUTE_LOGITS_IN | BEAM_PATH_STREAM | BEAM_PATH_GROUPED | tiles;
+  const uint32_t known = BEAM_ROUTE_LOGITS_IN | BEAM_PATH_STREAM | BEAM_PATH_GROUPED |
+                         BEAM_ROUTE_SOFTMAX | BEAM_ROUTE_UNNORMED | tiles;
   if (d->flags & ~known) return BEAM_ERR_INVALID_ARG;
   const uint32_t tf = d->flags & tiles;
   if (tf & (tf - 1)) return BEAM_ERR_INVALID_ARG;  // at most one tile height
@@ -270,6 +273,20 @@ int beam_moe_route(const beam_moe_desc* d, int64_t T, const void* x,
                                   lin ? logits : nullptr, topk_idx, topk_w,
                                   workspace, static_cast<hipStream_t>(stream),
                                   nullptr));
+}
+
+int beam_moe_route_backward(const beam_moe_desc* d, int64_t T, const float* logits,
+                            const int32_t* topk_idx, const float* d_topk_w,
+                            float* d_logits, void* stream) {
+  Plan p;
+  int st = make_plan(d, T, &p);
+  if (st != BEAM_OK) return st;
+  if (T == 0) return BEAM_OK;
+  if (!logits || !topk_idx || !d_topk_w || !d_logits) return BEAM_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(topk_idx) || !aligned16(d_topk_w) || !aligned16(d_logits))
+    return BEAM_ERR_INVALID_ARG;
+  return hip_status(launch_route_backward(p, logits, topk_idx, d_topk_w, d_logits,
+                                          static_cast<hipStream_t>(stream)));
 }
 
 int beam_moe_permute(const beam_moe_desc* d, int64_t T, const int32_t* topk_idx,

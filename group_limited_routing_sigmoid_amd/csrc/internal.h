@@ -21,6 +21,8 @@ struct Plan {
   float scale;
   int32_t act, wdt;
   uint32_t flags;
+  bool softmax;        // scores: softmax over the logits instead of sigmoids
+  bool normed;         // weights: the chosen scores normalised to sum 1, then scaled
   int64_t T, S;        // tokens, slots (= T*K)
   int64_t nb;          // permutation blocks
   int32_t ks;          // partial logits the router selection sums
@@ -80,6 +82,9 @@ hipError_t launch_router(const Plan& p, const void* x, const float* w_router,
                          const float* bias, float* logits_out,
                          const float* logits_in, int32_t* idx, float* w,
                          void* ws, hipStream_t s, Timer* tm);
+// gradient of the weights in the logits
+hipError_t launch_route_backward(const Plan& p, const float* logits, const int32_t* idx,
+                                 const float* d_w, float* d_logits, hipStream_t s);
 // experts_grouped.hip: router logits partials by the dense tile GEMM
 hipError_t launch_router_gemm(const Plan& p, const void* x, const uint16_t* w3,
                               float* part, hipStream_t s, Timer* tm);

@@ -169,10 +169,7 @@ __global__ __launch_bounds__(256) void router_logits_valu(
 // with fused multiply-adds; coefficients are the binary64 roundings of 1/j!.
 // Every step is an IEEE-exact binary64 operation, so any conforming
 // evaluation of this sequence returns the same bits.
-__device__ __forceinline__ float sigmoid32(float l) {
-  if (l <= -104.0f) return 0.0f;
-  if (l >= 40.0f) return 1.0f;
-  const double z = -static_cast<double>(l);
+__device__ __forceinline__ double exp64(double z) {
   const double n = __builtin_rint(z * 0x1.71547652b82fep+0);
   double r = __builtin_fma(-n, 0x1.62e42feep-1, z);
   r = __builtin_fma(-n, 0x1.a39ef35793c76p-33, r);
@@ -190,9 +187,43 @@ __device__ __forceinline__ float sigmoid32(float l) {
   p = __builtin_fma(p, r, 0x1.0p-1);               // 1/2!
   p = __builtin_fma(p, r, 1.0);                    // 1/1!
   p = __builtin_fma(p, r, 1.0);                    // 1/0!
-  const double ez = __builtin_ldexp(p, static_cast<int>(n));
-  const double q = 1.0 / (1.0 + ez);
+  return __builtin_ldexp(p, static_cast<int>(n));
+}
+
+__device__ __forceinline__ float sigmoid32(float l) {
+  if (l <= -104.0f) return 0.0f;
+  if (l >= 40.0f) return 1.0f;
+  const double q = 1.0 / (1.0 + exp64(-static_cast<double>(l)));
   return static_cast<float>(q);
+}
+
+// Softmax scores of a token, one wave: s_e = e^(l_e - m) / sum_j e^(l_j - m)
+// with m the largest logit, the exponentials, their sum and the quotient in
+// binary64, rounded once to binary32 (the selection compares these values,
+// so they are held to the rounding of the exact softmax, as the sigmoids
+// are).  Exponents below -105 give 0: such a score is below half the smallest
+// binary32 value, and 1024 of them are below the sum's last bit.  A row
+// whose logits are all -infinity has m = -infinity, every comparison false
+// and the scores 0.  Needs every lane active.
+template <int EPL>
+__device__ __forceinline__ void softmax32(const float (&l)[EPL], int lane, int E, float (&s)[EPL]) {
+  float m = -__builtin_huge_valf();
+#pragma unroll
+  for (int j = 0; j < EPL; ++j)
+    if (lane * EPL + j < E) m = fmaxf(m, l[j]);
+#pragma unroll
+  for (int off = kWave / 2; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+  double ez[EPL], sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const double z = static_cast<double>(l[j]) - static_cast<double>(m);
+    ez[j] = (lane * EPL + j < E && z > -105.0) ? exp64(z) : 0.0;
+    sum += ez[j];
+  }
+#pragma unroll
+  for (int off = kWave / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) s[j] = sum > 0.0 ? static_cast<float>(ez[j] / sum) : 0.0f;
 }
 
 // Order-preserving map of a finite binary32 to uint32 (larger float, larger
@@ -251,13 +282,13 @@ __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
 // a group's experts are the L = gs/EPL lanes of one aligned power-of-two
 // segment, so group maxima are butterflies within the segment; otherwise
 // lane g scans group g's biased scores from LDS (one pad word per 32 keeps
-// the scan's lanes on distinct banks).
+// the scan's lanes on distinct banks).  SM: softmax scores.
 __device__ __forceinline__ int upad(int e) { return e + (e >> 5); }
 
-template <int EPL, int KS, bool SEG>
+template <int EPL, int KS, bool SEG, bool SM>
 __global__ __launch_bounds__(256) void router_select(
     const float* __restrict__ part, int ks, int vec4, int64_t T, int E, int G,
-    int TG, int K, int topn, float scale, const float* __restrict__ bias,
+    int TG, int K, int topn, int normed, float scale, const float* __restrict__ bias,
     float* __restrict__ logits_out, int32_t* __restrict__ idx_out,
     float* __restrict__ w_out) {
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
@@ -272,7 +303,7 @@ __global__ __launch_bounds__(256) void router_select(
   // range instead of branched on, and the clamped values are not used.
   // With vec4 (E % 4 == 0: 16-byte aligned rows) a lane's experts come four
   // to a 16-byte load.
-  float pz[EPL][KS], bz[EPL], sv[EPL], u[EPL];
+  float pz[EPL][KS], bz[EPL], lv[EPL], sv[EPL], u[EPL];
   if (EPL % 4 == 0 && vec4) {
 #pragma unroll
     for (int j = 0; j < EPL; j += 4) {
@@ -302,10 +333,13 @@ __global__ __launch_bounds__(256) void router_select(
 #pragma unroll
     for (int z = 1; z < KS; ++z)
       if (z < ks) l = l + pz[j][z];
-    sv[j] = sigmoid32(l);
-    u[j] = e < E ? sv[j] + bz[j] : ninf;
+    if (SM) lv[j] = l;
+    else sv[j] = sigmoid32(l);
     if (valid && e < E && logits_out) logits_out[t * E + e] = l;
   }
+  if constexpr (SM) softmax32<EPL>(lv, lane, E, sv);
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) u[j] = lane * EPL + j < E ? sv[j] + bz[j] : ninf;
 
   // 2. group scores: sum of the topn (1 or 2) largest biased scores (a
   // repeated value counts twice).  gsc ends in lane g for group g.
@@ -393,15 +427,161 @@ __global__ __launch_bounds__(256) void router_select(
       my_s = sk;
     }
   }
-  // 5. weights: (s / D) * scale, two binary32 roundings
+  // 5. weights: (s / D) * scale, two binary32 roundings (0 where every chosen
+  // score is 0), or s * scale
   if (lane < K) {
-    const float q = my_s / D;
+    const float q = !normed ? my_s : D == 0.0f ? 0.0f : my_s / D;
     idx_out[t * K + lane] = my_e;
     w_out[t * K + lane] = q * scale;
   }
 }
 
+// ---- gradient ---------------------------------------------------------------
+
+// 1 / (1 + e^-l) and its derivative, from t = e^-|l| so that neither loses
+// the small side: s = 1/(1+t) or t/(1+t), s (1 - s) = t / (1+t)^2.
+__device__ __forceinline__ void sigmoid_grad(float l, float& s, float& ds) {
+  const float t = expf(-fabsf(l));
+  const float r = 1.0f / (1.0f + t);
+  s = l >= 0.0f ? r : t * r;
+  ds = t * r * r;
+}
+
+// Sum over lanes 0..15, in every one of them (a wave's choices, K <= 16).
+__device__ __forceinline__ float sum16(float v) {
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+
+// One wave per token; lane l holds experts l*EPL .. l*EPL + EPL - 1 of the
+// row, lanes 0..K-1 also a choice each.  Every lane adds the choices that
+// name its experts in rank order (no scatter, so an expert named twice needs
+// no atomic and the row is written once, whole).  Bound by reading and
+// writing the logits' rows: a sigmoid row is only written, its K chosen
+// logits being gathered.
+template <int EPL, bool SM>
+__global__ __launch_bounds__(256) void route_backward(
+    const float* __restrict__ logits, const int32_t* __restrict__ idx,
+    const float* __restrict__ dw, int vec4, int64_t T, int E, int K, int normed, float scale,
+    float* __restrict__ dl) {
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kSelWaves + wave;
+  if (t >= T) return;  // wave-uniform
+  const float* row = logits + t * E;
+  float p[EPL];
+  float m = 0.0f, rs = 0.0f;
+  if constexpr (SM) {  // p = e^(l - m), rs = 1 / their sum
+    if (EPL % 4 == 0 && vec4) {
+#pragma unroll
+      for (int j = 0; j < EPL; j += 4) {
+        const u32x4 v = ld16(row + min(lane * EPL + j, E - 4));
+#pragma unroll
+        for (int q = 0; q < 4 && j + q < EPL; ++q) p[j + q] = __uint_as_float(v[q]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) p[j] = row[min(lane * EPL + j, E - 1)];
+    }
+  }
+  int e_k = -1;
+  float d_k = 0.0f, l_k = 0.0f;
+  if (lane < K) {
+    e_k = idx[t * K + lane];
+    if (e_k < 0 || e_k >= E) e_k = -1;
+    if (e_k >= 0) {
+      d_k = dw[t * K + lane];
+      l_k = row[e_k];
+    }
+  }
+  if constexpr (SM) {
+    m = -__builtin_huge_valf();
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      if (lane * EPL + j >= E) p[j] = -__builtin_huge_valf();
+      m = fmaxf(m, p[j]);
+    }
+#pragma unroll
+    for (int off = kWave / 2; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      p[j] = p[j] > -__builtin_huge_valf() ? expf(p[j] - m) : 0.0f;
+      sum += p[j];
+    }
+#pragma unroll
+    for (int off = kWave / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+    rs = sum > 0.0f ? 1.0f / sum : 0.0f;
+  }
+  // the choices: scores, then the gradient g of each choice's own logit
+  float s_k = 0.0f, ds_k = 0.0f;
+  if (e_k >= 0) {
+    if (SM) s_k = l_k > -__builtin_huge_valf() ? expf(l_k - m) * rs : 0.0f;
+    else sigmoid_grad(l_k, s_k, ds_k);
+  }
+  float D = 1.0f;
+  if (normed) {
+    D = sum16(s_k);
+    D = D > 0.0f ? D : __builtin_huge_valf();  // all scores 0: every quotient below is 0
+  }
+  // lanes 0..15 hold the sum; the dense form needs it in every lane
+  const float c = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(
+                                                __builtin_bit_cast(int, sum16(d_k * (s_k / D)))));
+  float g;
+  if (SM) g = scale * (s_k / D) * (normed ? d_k - c : d_k);
+  else g = scale * (ds_k / D) * (normed ? d_k - c : d_k);
+  const float back = (SM && !normed) ? scale * c * rs : 0.0f;
+  float out[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) out[j] = SM ? -back * p[j] : 0.0f;
+  for (int k = 0; k < K; ++k) {
+    const int e = __builtin_amdgcn_readlane(e_k, k);
+    const float gk = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, g), k));
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (lane * EPL + j == e) out[j] += gk;
+  }
+  float* o = dl + t * E;
+  if (EPL % 4 == 0 && vec4) {
+#pragma unroll
+    for (int j = 0; j < EPL; j += 4)
+      if (lane * EPL + j < E) {
+        u32x4 v;
+#pragma unroll
+        for (int q = 0; q < 4 && j + q < EPL; ++q) v[q] = __float_as_uint(out[j + q]);
+        st16(o + lane * EPL + j, v);
+      }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (lane * EPL + j < E) o[lane * EPL + j] = out[j];
+  }
+}
+
 }  // namespace
+
+hipError_t launch_route_backward(const Plan& p, const float* logits, const int32_t* idx,
+                                 const float* d_w, float* d_logits, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(ceil_div(p.T, kSelWaves)));
+  const int epl = static_cast<int>(ceil_div(p.E, kWave));
+  const int vec4 = p.E % 4 == 0;
+#define BEAM_RB(EPL)                                                                         \
+  do {                                                                                       \
+    if (p.softmax)                                                                           \
+      hipLaunchKernelGGL((route_backward<EPL, true>), grid, dim3(256), 0, s, logits, idx,    \
+                         d_w, vec4, p.T, p.E, p.K, p.normed ? 1 : 0, p.scale, d_logits);     \
+    else                                                                                     \
+      hipLaunchKernelGGL((route_backward<EPL, false>), grid, dim3(256), 0, s, logits, idx,   \
+                         d_w, vec4, p.T, p.E, p.K, p.normed ? 1 : 0, p.scale, d_logits);     \
+  } while (0)
+  if (epl <= 1) BEAM_RB(1);
+  else if (epl <= 2) BEAM_RB(2);
+  else if (epl <= 4) BEAM_RB(4);
+  else if (epl <= 8) BEAM_RB(8);
+  else BEAM_RB(16);
+#undef BEAM_RB
+  return hipGetLastError();
+}
 
 hipError_t launch_router(const Plan& p, const void* x, const float* w_router,
                          const float* bias, float* logits_out,
@@ -442,10 +622,15 @@ hipError_t launch_router(const Plan& p, const void* x, const float* w_router,
   // partials live in the workspace and given logits are 16-byte aligned
   // (checked at the boundary), so rows of E % 4 == 0 floats are too
   const int vec4 = p.E % 4 == 0;
-#define BEAM_SEL3(EPL, KS, SEG)                                                \
-  BEAM_LAUNCH(tm, "router_select", (router_select<EPL, KS, SEG>), grid, dim3(256), 0, s, part, \
-              ks, vec4, p.T, p.E, p.G, p.TG, p.K, p.topn, p.scale, bias,      \
+#define BEAM_SEL4(EPL, KS, SEG, SM)                                            \
+  BEAM_LAUNCH(tm, "router_select", (router_select<EPL, KS, SEG, SM>), grid, dim3(256), 0, s, part, \
+              ks, vec4, p.T, p.E, p.G, p.TG, p.K, p.topn, p.normed ? 1 : 0, p.scale, bias, \
               const_cast<float*>(lo), idx, w)
+#define BEAM_SEL3(EPL, KS, SEG)                                                \
+  do {                                                                         \
+    if (p.softmax) BEAM_SEL4(EPL, KS, SEG, true);                              \
+    else BEAM_SEL4(EPL, KS, SEG, false);                                       \
+  } while (0)
 #define BEAM_SEL(EPL)                                                          \
   do {                                                                         \
     if (ks == 1) {                                                             \
@@ -460,6 +645,7 @@ hipError_t launch_router(const Plan& p, const void* x, const float* w_router,
   else if (eplp == 4) BEAM_SEL(4);
   else if (eplp == 8) BEAM_SEL(8);
   else BEAM_SEL(16);
+#undef BEAM_SEL4
 #undef BEAM_SEL3
 #undef BEAM_SEL
   return hipGetLastError();

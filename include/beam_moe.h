@@ -86,6 +86,10 @@ typedef enum {
                                           FP8: the 256-row form) */
 #define BEAM_TILE_64 (1u << 6)         /* MXFP4 grouped path: force 64-slot tiles (bf16 and
                                           FP8: the 128-row form) */
+/* Router scores and weights (default: sigmoid scores, weights normalised to
+ * sum routed_scale).  Both flags work wherever a descriptor routes. */
+#define BEAM_ROUTE_SOFTMAX (1u << 7)   /* scores are the softmax over the E logits */
+#define BEAM_ROUTE_UNNORMED (1u << 8)  /* weights are score * routed_scale, not normalised */
 
 typedef struct {
   int32_t hidden;           /* H: 5120 for Beam */
@@ -135,11 +139,39 @@ int beam_moe_workspace_bytes(const beam_moe_desc* desc, int64_t T,
  *   topk_w    device [T, K] fp32: routing weights (sum to routed_scale)
  * Given identical fp32 logits the indices and weights are bitwise identical
  * to the routing specification: sigmoid rounded from a fixed binary64
- * evaluation, binary32 sums, ties broken towards the lower index. */
+ * evaluation, binary32 sums, ties broken towards the lower index.
+ * With BEAM_ROUTE_SOFTMAX the scores are s_e = exp(l_e - max l) / sum exp(l_j
+ * - max l) over all E logits, evaluated in binary64 and rounded once to
+ * binary32; a logit of -infinity gives the score 0, and a row of only those
+ * has scores 0.  With BEAM_ROUTE_UNNORMED the weights are s_k * routed_scale.
+ * Where the K chosen scores are all 0 (logits so low that binary32 holds no
+ * smaller score, or masked ones) the weights are 0.  Keeping every group
+ * (topk_groups = n_groups) is plain top-K over the experts. */
 int beam_moe_route(const beam_moe_desc* desc, int64_t T, const void* x,
                    const float* w_router, const float* bias, float* logits,
                    int32_t* topk_idx, float* topk_w, void* workspace,
                    size_t ws_bytes, void* stream);
+
+/* Gradient of the routing weights in the logits (the training step's way
+ * back through beam_moe_route).  The selection and its bias are constants;
+ * with D the sum of the K chosen scores, c = sum_k d_topk_w_k s_k:
+ *   sigmoid             d l_k = scale (dw_k - c / D) s_k (1 - s_k) / D
+ *   sigmoid, unnormed   d l_k = scale dw_k s_k (1 - s_k)
+ *   softmax             d l_k = scale (s_k / D) (dw_k - c / D)
+ *   softmax, unnormed   d l_e = scale s_e ([e chosen] dw_e - c), every expert
+ * and 0 for the experts not named (in all but the last form).  Scores are
+ * recomputed in binary32; a row whose chosen scores are all 0 has gradient 0.
+ *   logits    device [T, E] fp32: those the routing was made from
+ *   topk_idx  device [T, K] int32; an id outside [0, E) adds nothing, an id
+ *             named twice counts as two choices
+ *   d_topk_w  device [T, K] fp32: gradient of the weights
+ *   d_logits  device [T, E] fp32: output, every element written
+ * Follows desc's BEAM_ROUTE_SOFTMAX and BEAM_ROUTE_UNNORMED.  The gradients
+ * of x and w_router are the plain products d_logits W_r and d_logits^T x.
+ * No workspace. */
+int beam_moe_route_backward(const beam_moe_desc* desc, int64_t T, const float* logits,
+                            const int32_t* topk_idx, const float* d_topk_w,
+                            float* d_logits, void* stream);
 
 /* Token permutation for a given routing (the dispatch between router and
  * experts): a stable counting sort of the T*K assignments by expert.  The
