@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -33,7 +34,9 @@ SYMBOLS = ("beam_status_string", "beam_moe_validate", "beam_moe_workspace_bytes"
            "beam_moe_timer_reset", "beam_moe_timer_count", "beam_moe_timer_read",
            "beam_moe_forward_timed", "beam_moe_bias_update", "beam_moe_bias_gamma",
            "beam_moe_forward_residual", "beam_moe_quant_mxfp8",
-           "beam_moe_forward_noalloc", "beam_moe_route_backward")
+           "beam_moe_forward_noalloc", "beam_moe_route_backward",
+           "beam_moe_norm_residual", "beam_moe_norm_residual_workspace_bytes",
+           "beam_moe_norm_residual_backward")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -72,6 +75,12 @@ def lib():
         L.beam_moe_workspace_bytes.argtypes = [D, i64, ctypes.POINTER(sz)]
         L.beam_moe_route.argtypes = [D, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.beam_moe_route_backward.argtypes = [D, i64, vp, vp, vp, vp, vp]
+        f32 = ctypes.c_float
+        L.beam_moe_norm_residual.argtypes = [i64, i64, i32, vp, vp, vp, i64, vp, f32, f32, f32,
+                                             vp, vp, vp, vp, vp, vp]
+        L.beam_moe_norm_residual_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(sz)]
+        L.beam_moe_norm_residual_backward.argtypes = [i64, i64, i32, vp, vp, vp, i64, vp, f32, f32,
+                                                      f32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.beam_moe_permute.argtypes = [D, i64, vp, vp, vp, vp, vp, vp, sz, vp]
         L.beam_moe_quant_e4m3.argtypes = [i64, i64, i32, vp, vp, vp, vp]
         L.beam_moe_quant_mxfp8.argtypes = [i64, i64, i32, vp, vp, vp, vp]
@@ -192,13 +201,17 @@ class Workspace:
 _default_ws = {}
 
 
-def _ws(desc: Desc, T: int, workspace: Optional[Workspace], device, stream=None):
-    n = workspace_bytes(desc, T)
+def _scratch(n: int, workspace: Optional[Workspace], device, stream=None):
     s = _torch_stream(stream, device)
     if workspace is None:
         key = (str(device), s.cuda_stream)
         workspace = _default_ws.setdefault(key, Workspace(device))
-    return workspace.get(n, s), n
+    return workspace.get(n, s)
+
+
+def _ws(desc: Desc, T: int, workspace: Optional[Workspace], device, stream=None):
+    n = workspace_bytes(desc, T)
+    return _scratch(n, workspace, device, stream), n
 
 
 def _alloc_on(stream):
@@ -368,6 +381,158 @@ def quant_mxfp8(v: torch.Tensor, stream=None):
     _check(lib().beam_moe_quant_mxfp8(rows, cols, dt, _p(v), _p(q), _p(s),
                                       _stream(stream, v.device)), "beam_moe_quant_mxfp8")
     return q, s[:, :cols // 32]
+
+
+def residual_scale(step: int):
+    """(alpha, beta) of the depth-scaled residual stream at sublayer step k >= 1:
+    sqrt((k-1)/k) and 1/sqrt(k), as forward_residual uses them."""
+    if step < 1:
+        raise ValueError(f"step {step}: steps count from 1")
+    return math.sqrt((step - 1) / step), 1.0 / math.sqrt(step)
+
+
+def _norm_inputs(residual, o, post_weight, gate, pre_weight, dtype):
+    """Checked addresses of a step's inputs: (T, H, dtype code, dtype, o,
+    post_weight, gate, gate_cols, pre_weight, tensors)."""
+    if residual.dim() != 2:
+        raise ValueError(f"residual: shape {tuple(residual.shape)}, expected [T, H]")
+    T, H = residual.shape
+    if o is not None:
+        if dtype is not None and dtype != o.dtype:
+            raise ValueError(f"dtype {dtype} with o in {o.dtype}: o, gate and x share one dtype")
+        dtype = o.dtype
+    elif post_weight is not None or gate is not None:
+        raise ValueError("post_weight and gate belong to o")
+    elif dtype is None:
+        dtype = torch.bfloat16
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"dtype {dtype}, expected torch.bfloat16 or torch.float32")
+    ptr, tensors = [None, None, None, None], [residual]
+    cols = 0
+    if o is not None:
+        if post_weight is None:
+            raise ValueError("o needs its post_weight")
+        ptr[0] = _arg("o", o, (T, H), dtype)
+        ptr[1] = _arg("post_weight", post_weight, (H,), torch.float32)
+        tensors += [o, post_weight]
+        if gate is not None:
+            cols = H if gate.dim() == 2 and gate.shape[1] == H else 1
+            ptr[2] = _arg("gate", gate, (T, cols), dtype)
+            tensors.append(gate)
+    if pre_weight is not None:
+        ptr[3] = _arg("pre_weight", pre_weight, (H,), torch.float32)
+        tensors.append(pre_weight)
+    return (T, H, BF16 if dtype == torch.bfloat16 else F32, dtype, ptr[0], ptr[1], ptr[2], cols,
+            ptr[3], tensors)
+
+
+def _norm_residual(residual, o, post_weight, gate, pre_weight, eps, alpha, beta, dtype,
+                   residual_out, want_x, codes, stream):
+    T, H, code, dtype, po, pw, pg, cols, pp, tensors = _norm_inputs(
+        residual, o, post_weight, gate, pre_weight, dtype)
+    pr = _arg("residual", residual, (T, H), torch.float32)
+    x = q = s = None
+    with _alloc_on(stream):
+        if o is None:
+            residual_out, p_out = residual, None
+        else:
+            if residual_out is None:
+                residual_out = torch.empty_like(residual)
+            p_out = _arg("residual_out", residual_out, (T, H), torch.float32)
+            tensors.append(residual_out)
+        if pre_weight is not None and want_x:
+            x = torch.empty(T, H, dtype=dtype, device=residual.device)
+        if codes:
+            q = torch.empty(T, H, dtype=torch.uint8, device=residual.device)
+            s = torch.empty(T, H // 128, dtype=torch.float32, device=residual.device)
+    _run(lib().beam_moe_norm_residual, "beam_moe_norm_residual", stream, tensors, T, H, code, po, pw,
+         pg, cols, pp, eps, alpha, beta, pr, p_out, None if x is None else x.data_ptr(),
+         None if q is None else q.data_ptr(), None if s is None else s.data_ptr())
+    return residual_out, x, q, s
+
+
+def norm_residual(residual: torch.Tensor, o: Optional[torch.Tensor] = None,
+                  post_weight: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None,
+                  pre_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  alpha: float = 1.0, beta: float = 1.0, dtype: Optional[torch.dtype] = None,
+                  residual_out: Optional[torch.Tensor] = None, stream=None):
+    """beam_moe_norm_residual: the step between two blocks.  Returns (r', x):
+    r' = alpha residual + beta sigmoid(gate) RMSNorm(o) post_weight, fp32
+    (residual itself without o; residual_out may be residual), and x =
+    RMSNorm(r') pre_weight in o's dtype (`dtype`, bf16 by default, without o;
+    None without pre_weight).  gate is [T,H] or [T,1]."""
+    return _norm_residual(residual, o, post_weight, gate, pre_weight, eps, alpha, beta, dtype,
+                          residual_out, True, False, stream)[:2]
+
+
+def norm_residual_e4m3(residual: torch.Tensor, o: Optional[torch.Tensor] = None,
+                       post_weight: Optional[torch.Tensor] = None,
+                       gate: Optional[torch.Tensor] = None,
+                       pre_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                       alpha: float = 1.0, beta: float = 1.0,
+                       dtype: Optional[torch.dtype] = None,
+                       residual_out: Optional[torch.Tensor] = None, with_x: bool = False,
+                       stream=None):
+    """norm_residual with x as e4m3 codes [T,H] uint8 and scales [T,H/128], as
+    matmul_e4m3 takes them.  Returns (r', codes, scales), and x too with
+    with_x."""
+    if pre_weight is None:
+        raise ValueError("the codes are x's: pre_weight is needed")
+    r, x, q, s = _norm_residual(residual, o, post_weight, gate, pre_weight, eps, alpha, beta, dtype,
+                                residual_out, with_x, True, stream)
+    return (r, q, s, x) if with_x else (r, q, s)
+
+
+def norm_residual_backward(residual_out: torch.Tensor,
+                           d_residual_out: Optional[torch.Tensor] = None,
+                           d_x: Optional[torch.Tensor] = None,
+                           o: Optional[torch.Tensor] = None,
+                           post_weight: Optional[torch.Tensor] = None,
+                           gate: Optional[torch.Tensor] = None,
+                           pre_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                           alpha: float = 1.0, beta: float = 1.0,
+                           workspace: Optional[Workspace] = None, stream=None) -> dict:
+    """beam_moe_norm_residual_backward.  residual_out is the forward's r' (its
+    residual without o); d_residual_out and d_x are the gradients of r' and x
+    (None for zero, not both).  Returns a dict: d_residual [T,H] fp32; with o
+    d_o and d_post_weight, with gate d_gate, with d_x d_pre_weight."""
+    T, H, code, dtype, po, pw, pg, cols, pp, tensors = _norm_inputs(
+        residual_out, o, post_weight, gate, pre_weight,
+        d_x.dtype if o is None and d_x is not None else None)
+    if d_residual_out is None and d_x is None:
+        raise ValueError("one of d_residual_out and d_x is needed")
+    if d_x is not None and pre_weight is None:
+        raise ValueError("d_x needs the pre_weight")
+    dev = residual_out.device
+    pr = _arg("residual_out", residual_out, (T, H), torch.float32)
+    p_dr = p_dx = None
+    if d_residual_out is not None:
+        p_dr = _arg("d_residual_out", d_residual_out, (T, H), torch.float32)
+        tensors.append(d_residual_out)
+    if d_x is not None:
+        p_dx = _arg("d_x", d_x, (T, H), dtype)
+        tensors.append(d_x)
+    need = ctypes.c_size_t(0)
+    _check(lib().beam_moe_norm_residual_workspace_bytes(T, H, ctypes.byref(need)),
+           "beam_moe_norm_residual_workspace_bytes")
+    out = {}
+    with _alloc_on(stream):
+        out["d_residual"] = torch.empty(T, H, dtype=torch.float32, device=dev)
+        if o is not None:
+            out["d_o"] = torch.empty_like(o)
+            out["d_post_weight"] = torch.empty(H, dtype=torch.float32, device=dev)
+            if gate is not None:
+                out["d_gate"] = torch.empty_like(gate)
+        if d_x is not None:
+            out["d_pre_weight"] = torch.empty(H, dtype=torch.float32, device=dev)
+    buf = _scratch(need.value, workspace, dev, stream)
+    ptr = {k: v.data_ptr() for k, v in out.items()}
+    _run(lib().beam_moe_norm_residual_backward, "beam_moe_norm_residual_backward", stream, tensors,
+         T, H, code, po, pw, pg, cols, pp, eps, alpha, beta, pr, p_dr, p_dx, ptr["d_residual"],
+         ptr.get("d_o"), ptr.get("d_gate"), ptr.get("d_pre_weight"), ptr.get("d_post_weight"),
+         None if buf is None else buf.data_ptr(), need.value)
+    return out
 
 
 class Timer:

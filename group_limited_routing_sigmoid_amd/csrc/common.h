@@ -95,6 +95,13 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
       __builtin_amdgcn_cvt_pk_fp8_f32(sat448(c), sat448(d), lo, true));
 }
 
+// The e4m3 recipe's block scale: amax / 448 in binary32, or 1 where that is
+// zero (an all-zero block, or a subnormal amax whose quotient underflows).
+__device__ __forceinline__ float e4m3_scale(float amax) {
+  const float sc = amax / 448.0f;
+  return sc > 0.0f ? sc : 1.0f;
+}
+
 // silu(g) = g * sigmoid(g), the sigmoid from the hardware exponential and
 // reciprocal (each within about 1 ulp of binary32).  The bf16 paths round
 // silu(g) * u to 8 bits next, so an IEEE divide (about ten instructions more

@@ -9,13 +9,6 @@
 namespace beam {
 namespace {
 
-// The recipe's block scale: amax / 448 in binary32, or 1 where that is zero
-// (an all-zero block, or a subnormal amax whose quotient underflows).
-__device__ __forceinline__ float e4m3_scale(float amax) {
-  const float sc = amax / 448.0f;
-  return sc > 0.0f ? sc : 1.0f;
-}
-
 // 16 lanes per (row, 128-column block), 8 consecutive columns per lane (one
 // 16-byte load of bf16, two of fp32); a wave covers 4 blocks.  The block's
 // amax is reduced over its 16 lanes; scale = e4m3_scale(amax), code =

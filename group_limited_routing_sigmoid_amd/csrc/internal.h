@@ -52,6 +52,10 @@ void timer_end(Timer* t, hipStream_t s);
     timer_end(tm, stream);                                                \
   } while (0)
 
+// Checks and conversions of the C ABI's entry points.
+static inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+static inline int hip_status(hipError_t e) { return e == hipSuccess ? BEAM_OK : BEAM_ERR_HIP; }
+
 // Builds the plan; returns a beam_status.
 int make_plan(const beam_moe_desc* d, int64_t T, Plan* p);
 
@@ -125,6 +129,42 @@ struct Epilogue {
 hipError_t launch_combine(const Plan& p, const int32_t* slot_of,
                           const float* w, void* out, void* ws, hipStream_t s,
                           Timer* tm, const Epilogue* ep = nullptr);
+// norm.hip: the norms around a block, its gate and the residual stream
+struct NormArgs {
+  const void* o;          // [T, H] block output, or null: r' = residual
+  const float* post;      // [H]
+  const void* gate;       // [T, H] or [T, 1], or null
+  const float* pre;       // [H], or null: no x
+  const float* residual;  // [T, H]
+  float* residual_out;    // [T, H] (with o)
+  void* x;                // [T, H], or null
+  uint8_t* xq;            // [T, H] e4m3 codes, or null
+  float* xs;              // [T, H/128]
+  int H, gate_cols;       // gate_cols: 0 (none), 1 or H
+  float eps, alpha, beta;
+};
+struct NormGradArgs {
+  const void* o;
+  const float* post;
+  const void* gate;
+  const float* pre;
+  const float* r;      // [T, H] the forward's residual stream r'
+  const float* d_res;  // [T, H] gradient of r' from later, or null
+  const void* dx;      // [T, H] gradient of x, or null
+  float* d_residual;   // [T, H]
+  void* d_o;
+  void* d_gate;
+  float* part;         // workspace [groups][2][H]
+  int64_t T;
+  int H, gate_cols;
+  float eps, alpha, beta;
+};
+// Workgroups of the backward pass, each with its share of the weights' gradients.
+int norm_grad_groups(int64_t T);
+constexpr int kNormMaxH = 16384;  // 1024 threads of 16 columns
+hipError_t launch_norm_residual(const NormArgs& a, int64_t T, int32_t dtype, hipStream_t s);
+hipError_t launch_norm_residual_backward(const NormGradArgs& a, int32_t dtype, float* d_pre,
+                                         float* d_post, hipStream_t s);
 // fp8.hip
 hipError_t launch_quant_e4m3(int64_t rows, int64_t cols, int32_t dtype,
                              const void* v, uint8_t* q, float* scales,

@@ -300,6 +300,64 @@ int beam_moe_forward_residual(const beam_moe_desc* desc, int64_t T, const void* 
                               float* residual, void* out, void* workspace,
                               size_t ws_bytes, void* stream);
 
+/* ---- the step between two blocks -----------------------------------------
+ * The norm after a block, its gate, the scaled residual stream and the norm
+ * before the next block, per token t:
+ *   y  = o / sqrt(mean(o^2) + eps) * post_weight
+ *   r' = alpha * residual + beta * sigmoid(gate) * y
+ *   x  = r' / sqrt(mean(r'^2) + eps) * pre_weight
+ * beam_moe_forward_residual is this step's first half for the block's own
+ * output inside its combine; here o is any sublayer's output and the step
+ * ends with the next sublayer's input.  Beam's stream at step k has alpha =
+ * sqrt((k-1)/k), beta = 1/sqrt(k).
+ *   o             device [T, H] dtype, or NULL: r' = residual, post_weight,
+ *                 gate, residual_out, alpha and beta are not used
+ *   post_weight   device [H] fp32
+ *   gate          device [T, gate_cols] dtype before the sigmoid, or NULL with
+ *                 gate_cols 0; gate_cols 1 (one gate a token) or H
+ *   pre_weight    device [H] fp32, or NULL: x and its codes are not made
+ *   residual      device [T, H] fp32
+ *   residual_out  device [T, H] fp32: r'; may be residual itself
+ *   x             device [T, H] dtype, or NULL
+ *   x_codes       device [T, H] uint8, or NULL: x quantised by the recipe of
+ *                 beam_moe_quant_e4m3, from x before any rounding
+ *   x_scales      device [T, H/128] fp32, with x_codes
+ * dtype BEAM_F32 or BEAM_BF16; 1 <= H <= 16384, with x_codes H % 128 == 0
+ * (BEAM_ERR_UNSUPPORTED otherwise); eps > 0, alpha and beta finite.  A token's
+ * sums of squares must be finite in binary32.  With H % 8 == 0 the rows are
+ * read 16 bytes at a time, otherwise value by value.  No workspace. */
+int beam_moe_norm_residual(int64_t T, int64_t H, int32_t dtype, const void* o,
+                           const float* post_weight, const void* gate, int64_t gate_cols,
+                           const float* pre_weight, float eps, float alpha, float beta,
+                           const float* residual, float* residual_out, void* x,
+                           uint8_t* x_codes, float* x_scales, void* stream);
+
+/* Bytes of workspace beam_moe_norm_residual_backward needs (0 for T == 0). */
+int beam_moe_norm_residual_workspace_bytes(int64_t T, int64_t H, size_t* bytes);
+
+/* Gradients of beam_moe_norm_residual.
+ *   residual_out     device [T, H] fp32: the forward's r' (residual where o is
+ *                    NULL)
+ *   d_residual_out   device [T, H] fp32: gradient of r' from later steps, or
+ *                    NULL for zero
+ *   d_x              device [T, H] dtype: gradient of x, or NULL (pre_weight
+ *                    and d_pre_weight are then not used)
+ *   d_residual       device [T, H] fp32: output; may be d_residual_out itself
+ *   d_o              device [T, H] dtype: output, with o
+ *   d_gate           device [T, gate_cols] dtype: output, with gate
+ *   d_pre_weight, d_post_weight  device [H] fp32: outputs (sums over the
+ *                    tokens, 0 for T == 0), with d_x and with o
+ * Other arguments as in the forward.  Identical inputs give bitwise identical
+ * outputs. */
+int beam_moe_norm_residual_backward(int64_t T, int64_t H, int32_t dtype, const void* o,
+                                    const float* post_weight, const void* gate,
+                                    int64_t gate_cols, const float* pre_weight, float eps,
+                                    float alpha, float beta, const float* residual_out,
+                                    const float* d_residual_out, const void* d_x,
+                                    float* d_residual, void* d_o, void* d_gate,
+                                    float* d_pre_weight, float* d_post_weight,
+                                    void* workspace, size_t ws_bytes, void* stream);
+
 /* Auxiliary-loss-free load balancing step.  The load-balancing paragraph of
  * "Reflection AI Introduces Beam ..." says Beam builds on DeepSeek-V3's
  * bias-update balancing with a cosine decay of the update speed; the rule

@@ -71,3 +71,59 @@ def route_grad(logits, idx, dw, scale, softmax, normed):
     if softmax and not normed:
         out = -s_all * c
     return scale * out.scatter_add(1, at, torch.where(ok, g, 0.0))
+
+
+# ---- the step between two blocks -------------------------------------------
+
+def norm_step(r, o, post, gate, pre, eps, alpha, beta):
+    """(r', x, y, g): the forward in 64 bits (y the normed block output, g the
+    gate's sigmoid)."""
+    r = r.double()
+    y, g = None, torch.ones(r.shape[0], 1, dtype=F64)
+    if o is not None:
+        o = o.double()
+        y = o / torch.sqrt((o * o).mean(1, keepdim=True) + eps) * post.double()
+        if gate is not None:
+            g = torch.sigmoid(gate.double())
+        r = alpha * r + beta * g * y
+    x = None
+    if pre is not None:
+        x = r / torch.sqrt((r * r).mean(1, keepdim=True) + eps) * pre.double()
+    return r, x, y, g
+
+
+def norm_step_grad(rp, d_rp, dx, o, post, gate, pre, eps, alpha, beta, absolute=False):
+    """The gradients by their formulas, from the forward's r'.  With absolute
+    every term enters by its absolute value: the scale of the roundings."""
+    def A(v):
+        return v.abs() if absolute else v
+
+    def minus(a, b):
+        return a + b if absolute else a - b
+
+    rp = rp.double()
+    out = {}
+    d = A(d_rp.double()) if d_rp is not None else torch.zeros_like(rp)
+    if dx is not None:
+        inv = 1 / torch.sqrt((rp * rp).mean(1, keepdim=True) + eps)
+        hat, dx = A(rp * inv), A(dx.double())
+        out["d_pre_weight"] = (dx * hat).sum(0)
+        w = A(pre.double()) * dx
+        d = d + inv * minus(w, hat * (w * hat).mean(1, keepdim=True))
+    if o is None:
+        out["d_residual"] = d            # r' is the residual itself: alpha plays no part
+        return out
+    out["d_residual"] = A(torch.tensor(alpha, dtype=F64)) * d
+    d = A(torch.tensor(beta, dtype=F64)) * d
+    o = o.double()
+    inv = 1 / torch.sqrt((o * o).mean(1, keepdim=True) + eps)
+    hat, post = A(o * inv), A(post.double())
+    if gate is not None:
+        s = torch.sigmoid(gate.double())
+        dg = d * hat * post * s * torch.sigmoid(-gate.double())
+        out["d_gate"] = dg.sum(1, keepdim=True) if gate.shape[1] == 1 and hat.shape[1] != 1 else dg
+        d = d * s
+    out["d_post_weight"] = (d * hat).sum(0)
+    w = post * d
+    out["d_o"] = inv * minus(w, hat * (w * hat).mean(1, keepdim=True))
+    return out

@@ -42,3 +42,72 @@ def test_binding_checks_tensors_first():
     with pytest.raises(ValueError, match="GPU"):
         gl.route_backward(_desc(), torch.zeros(2, 256), torch.zeros(2, 8, dtype=torch.int32), torch.zeros(2, 8),
                           out=torch.zeros(2, 256))
+
+
+def _norm(**kw):
+    a = dict(T=4, H=256, dtype=gl.BF16, o=GOOD, post=GOOD, gate=GOOD, cols=256, pre=GOOD, eps=1e-6, alpha=1.0,
+             beta=1.0, res=GOOD, res_out=GOOD, x=GOOD, q=None, s=None)
+    a.update(kw)
+    return gl.lib().beam_moe_norm_residual(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), gl.ERR_INVALID_ARG), (dict(H=0), gl.ERR_INVALID_ARG), (dict(H=16385, cols=1), gl.ERR_UNSUPPORTED),
+    (dict(dtype=gl.FP8_E4M3), gl.ERR_INVALID_ARG), (dict(eps=0.0), gl.ERR_INVALID_ARG),
+    (dict(eps=-1.0), gl.ERR_INVALID_ARG), (dict(eps=float("nan")), gl.ERR_INVALID_ARG),
+    (dict(alpha=float("inf")), gl.ERR_INVALID_ARG), (dict(beta=float("nan")), gl.ERR_INVALID_ARG),
+    (dict(cols=2), gl.ERR_INVALID_ARG), (dict(cols=0), gl.ERR_INVALID_ARG),
+    (dict(gate=None), gl.ERR_INVALID_ARG), (dict(o=None), gl.ERR_INVALID_ARG),
+    (dict(post=None), gl.ERR_INVALID_ARG), (dict(res=None), gl.ERR_INVALID_ARG),
+    (dict(res_out=None), gl.ERR_INVALID_ARG), (dict(x=None), gl.ERR_INVALID_ARG),
+    (dict(pre=None), gl.ERR_INVALID_ARG), (dict(o=None, gate=None, cols=0, pre=None, x=None), gl.ERR_INVALID_ARG),
+    (dict(q=GOOD), gl.ERR_INVALID_ARG), (dict(s=GOOD), gl.ERR_INVALID_ARG),
+    (dict(H=200, cols=1, q=GOOD, s=GOOD), gl.ERR_UNSUPPORTED),
+    (dict(o=BAD), gl.ERR_INVALID_ARG), (dict(gate=BAD), gl.ERR_INVALID_ARG), (dict(res=BAD), gl.ERR_INVALID_ARG),
+    (dict(x=BAD), gl.ERR_INVALID_ARG), (dict(T=0, o=None, gate=None, res=None), gl.OK),
+])
+def test_norm_refuses(kw, status):
+    assert _norm(**kw) == status
+
+
+def _norm_grad(**kw):
+    a = dict(T=4, H=256, dtype=gl.BF16, o=GOOD, post=GOOD, gate=GOOD, cols=1, pre=GOOD, eps=1e-6, alpha=1.0,
+             beta=1.0, r=GOOD, d_r=GOOD, d_x=GOOD, d_res=GOOD, d_o=GOOD, d_gate=GOOD, d_pre=GOOD, d_post=GOOD,
+             ws=GOOD, n=1 << 30)
+    a.update(kw)
+    return gl.lib().beam_moe_norm_residual_backward(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), gl.ERR_INVALID_ARG), (dict(H=20000), gl.ERR_UNSUPPORTED), (dict(eps=0.0), gl.ERR_INVALID_ARG),
+    (dict(cols=3), gl.ERR_INVALID_ARG), (dict(r=None), gl.ERR_INVALID_ARG),
+    (dict(d_r=None, d_x=None), gl.ERR_INVALID_ARG), (dict(pre=None), gl.ERR_INVALID_ARG),
+    (dict(d_pre=None), gl.ERR_INVALID_ARG), (dict(d_o=None), gl.ERR_INVALID_ARG),
+    (dict(d_post=None), gl.ERR_INVALID_ARG), (dict(d_gate=None), gl.ERR_INVALID_ARG),
+    (dict(d_res=None), gl.ERR_INVALID_ARG), (dict(ws=None), gl.ERR_WORKSPACE), (dict(n=100), gl.ERR_WORKSPACE),
+    (dict(ws=ctypes.c_void_p(0x10010)), gl.ERR_INVALID_ARG), (dict(d_x=BAD), gl.ERR_INVALID_ARG),
+])
+def test_norm_gradient_refuses(kw, status):
+    assert _norm_grad(**kw) == status
+
+
+def test_norm_binding_checks():
+    f, r = torch.zeros(2, 8), torch.zeros(8)
+    with pytest.raises(ValueError, match="GPU"):
+        gl.norm_residual(f, pre_weight=r)
+    with pytest.raises(ValueError, match=r"\[T, H\]"):
+        gl.norm_residual(torch.zeros(8), pre_weight=r)
+    with pytest.raises(ValueError, match="belong to o"):
+        gl.norm_residual(f, post_weight=r, pre_weight=r)
+    with pytest.raises(ValueError, match="share one dtype"):
+        gl.norm_residual(f, o=f, post_weight=r, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="expected torch.bfloat16"):
+        gl.norm_residual(f, pre_weight=r, dtype=torch.float16)
+    with pytest.raises(ValueError, match="post_weight"):
+        gl.norm_residual(f, o=f)
+    with pytest.raises(ValueError, match="pre_weight is needed"):
+        gl.norm_residual_e4m3(f, o=f, post_weight=r)
+    with pytest.raises(ValueError, match="one of"):
+        gl.norm_residual_backward(f)
+    with pytest.raises(ValueError):
+        gl.residual_scale(0)
