@@ -36,7 +36,8 @@ SYMBOLS = ("beam_status_string", "beam_moe_validate", "beam_moe_workspace_bytes"
            "beam_moe_forward_residual", "beam_moe_quant_mxfp8",
            "beam_moe_forward_noalloc", "beam_moe_route_backward",
            "beam_moe_norm_residual", "beam_moe_norm_residual_workspace_bytes",
-           "beam_moe_norm_residual_backward")
+           "beam_moe_norm_residual_backward", "beam_moe_matmul_e4m3",
+           "beam_moe_quant_e4m3_2d")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -75,6 +76,8 @@ def lib():
         L.beam_moe_workspace_bytes.argtypes = [D, i64, ctypes.POINTER(sz)]
         L.beam_moe_route.argtypes = [D, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.beam_moe_route_backward.argtypes = [D, i64, vp, vp, vp, vp, vp]
+        L.beam_moe_quant_e4m3_2d.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp, vp, vp]
+        L.beam_moe_matmul_e4m3.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, i32, vp, vp]
         f32 = ctypes.c_float
         L.beam_moe_norm_residual.argtypes = [i64, i64, i32, vp, vp, vp, i64, vp, f32, f32, f32,
                                              vp, vp, vp, vp, vp, vp]
@@ -381,6 +384,59 @@ def quant_mxfp8(v: torch.Tensor, stream=None):
     _check(lib().beam_moe_quant_mxfp8(rows, cols, dt, _p(v), _p(q), _p(s),
                                       _stream(stream, v.device)), "beam_moe_quant_mxfp8")
     return q, s[:, :cols // 32]
+
+
+def quant_e4m3_2d(v: torch.Tensor, block: bool = False, straight: bool = True,
+                  transposed: bool = True, stream=None):
+    """beam_moe_quant_e4m3_2d of a 2-D fp32/bf16 tensor [R,C]: (codes [R,C'],
+    scales, transposed codes [C,R'], their scales), C' and R' the next
+    multiples of 128, the added codes zero.  A scale covers 128 values of a
+    row (of a column in the transposed codes), or with block 128 x 128 values.
+    None for an orientation that is not asked for."""
+    if v.dim() != 2:
+        raise ValueError(f"v: shape {tuple(v.shape)}, expected [rows, cols]")
+    rows, cols = v.shape
+    pv = _arg("v", v, (rows, cols), torch.bfloat16, torch.float32)
+    nr, nc, dev = (rows + 127) // 128, (cols + 127) // 128, v.device
+    q = s = qt = st = None
+    with _alloc_on(stream):
+        if straight:
+            q = torch.empty(rows, nc * 128, dtype=torch.uint8, device=dev)
+            s = torch.empty(nr if block else rows, nc, dtype=torch.float32, device=dev)
+        if transposed:
+            qt = torch.empty(cols, nr * 128, dtype=torch.uint8, device=dev)
+            st = torch.empty(nc if block else cols, nr, dtype=torch.float32, device=dev)
+    _run(lib().beam_moe_quant_e4m3_2d, "beam_moe_quant_e4m3_2d", stream, (v,), rows, cols,
+         BF16 if v.dtype == torch.bfloat16 else F32, 1 if block else 0, pv,
+         None if q is None else q.data_ptr(), None if s is None else s.data_ptr(),
+         None if qt is None else qt.data_ptr(), None if st is None else st.data_ptr())
+    return q, s, qt, st
+
+
+def matmul_e4m3(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch.Tensor,
+                dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """beam_moe_matmul_e4m3: a b^T [M,N] in `dtype` from e4m3 codes a [M,K] and
+    b [N,K] (uint8), K a multiple of 128, with scales s_a [M,K/128] and s_b
+    [ceil(N/128),K/128] (128 x 128 blocks) or [N,K/128] (rows of b)."""
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError(f"shapes {tuple(a.shape)} and {tuple(b.shape)}, expected [M, K] and [N, K]")
+    (M, K), N = a.shape, b.shape[0]
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"dtype {dtype}, expected torch.bfloat16 or torch.float32")
+    if K % 128:
+        raise ValueError(f"K = {K} is not a multiple of 128")
+    rows = s_b.dim() == 2 and s_b.shape[0] == N
+    pa, pb = _arg("a", a, (M, K), torch.uint8), _arg("b", b, (N, K), torch.uint8)
+    psa = _arg("s_a", s_a, (M, K // 128), torch.float32)
+    psb = _arg("s_b", s_b, (N if rows else (N + 127) // 128, K // 128), torch.float32)
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty(M, N, dtype=dtype, device=a.device)
+    _run(lib().beam_moe_matmul_e4m3, "beam_moe_matmul_e4m3", stream, (a, s_a, b, s_b, out), M, N, K,
+         pa, psa, pb, psb, 1 if rows else 0, BF16 if dtype == torch.bfloat16 else F32,
+         _arg("out", out, (M, N), dtype))
+    return out
 
 
 def residual_scale(step: int):

@@ -23,7 +23,8 @@ ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "router.hip", "permute.hip", "experts_grouped.hip",
            "experts_stream.hip", "experts_f32.hip", "combine.hip", "fp8.hip",
-           "mxfp4.hip", "layer.cpp", "norm.hip"]
+           "mxfp4.hip", "layer.cpp", "norm.hip",
+           "matmul_fp8.hip"]
 NO_CONTRACT = {"router.hip", "fp8.hip", "mxfp4.hip"}
 
 COMMON = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",

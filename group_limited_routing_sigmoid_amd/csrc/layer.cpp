@@ -125,4 +125,37 @@ int beam_moe_norm_residual_backward(int64_t T, int64_t H, int32_t dtype, const v
       launch_norm_residual_backward(a, dtype, dp, dq, static_cast<hipStream_t>(stream)));
 }
 
+int beam_moe_quant_e4m3_2d(int64_t rows, int64_t cols, int32_t dtype, int32_t block,
+                           const void* v, uint8_t* q, float* s, uint8_t* qt, float* st,
+                           void* stream) {
+  if (rows < 0 || cols < 0 || (dtype != BEAM_F32 && dtype != BEAM_BF16) ||
+      (block != 0 && block != 1))
+    return BEAM_ERR_INVALID_ARG;
+  if (rows > 0x7FFFFFFF || cols > 0x7FFFFFFF ||
+      ceil_div(rows, 128) * ceil_div(cols, 128) > 0x7FFFFFFF)
+    return BEAM_ERR_UNSUPPORTED;
+  if (rows == 0 || cols == 0) return BEAM_OK;
+  if (!v || (!q && !qt) || !q != !s || !qt != !st) return BEAM_ERR_INVALID_ARG;
+  if (!aligned16(v) || !aligned16(q) || !aligned16(s) || !aligned16(qt) || !aligned16(st))
+    return BEAM_ERR_INVALID_ARG;
+  return hip_status(launch_quant_2d(rows, cols, dtype, block != 0, v, q, s, qt, st,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+int beam_moe_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, const float* sa,
+                         const uint8_t* b, const float* sb, int32_t b_rows, int32_t dtype,
+                         void* y, void* stream) {
+  if (M < 0 || N < 0 || K < 0 || (dtype != BEAM_F32 && dtype != BEAM_BF16) ||
+      (b_rows != 0 && b_rows != 1))
+    return BEAM_ERR_INVALID_ARG;
+  if (K % 128 || K > kMatmulMaxK || M > kMatmulMaxRows || N > kMatmulMaxRows)
+    return BEAM_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return BEAM_OK;
+  if (!y || (K > 0 && (!a || !sa || !b || !sb))) return BEAM_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(sa) || !aligned16(b) || !aligned16(sb) || !aligned16(y))
+    return BEAM_ERR_INVALID_ARG;
+  return hip_status(launch_matmul_e4m3(M, N, K, a, sa, b, sb, b_rows != 0, dtype, y,
+                                       static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

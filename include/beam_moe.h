@@ -300,6 +300,47 @@ int beam_moe_forward_residual(const beam_moe_desc* desc, int64_t T, const void* 
                               float* residual, void* out, void* workspace,
                               size_t ws_bytes, void* stream);
 
+/* ---- dense e4m3 products ---------------------------------------------------
+ * y[m,n] = sum_kb sa[m,kb] * sb[.,kb] * sum_{k in block kb} a[m,k] * b[n,k],
+ * blocks of 128 along k: the product of beam_moe_quant_e4m3's codes (or
+ * beam_moe_norm_residual's) with weights of the FP8 form, for the dense layers
+ * around the expert block.  Block sums on the matrix cores, one binary32
+ * multiply-add a block with its scales, one rounding to dtype.  With BEAM_F32
+ * products and sums are binary32 throughout; with BEAM_BF16 the e4m3 matrix
+ * instructions sum, which cut products at 2^-13 of the largest of eight
+ * neighbours (1.5e-5 of a result of normal data, against bf16's 2e-3).
+ *   a   device [M, K] uint8 e4m3fn codes   sa  device [M, K/128] fp32
+ *   b   device [N, K] uint8 e4m3fn codes (weights out x in)
+ *   sb  device fp32: [ceil(N/128), K/128] with b_rows 0 (a scale for each
+ *       128 x 128 block), [N, K/128] with b_rows 1 (for each row of b)
+ *   y   device [M, N] dtype (BEAM_F32 or BEAM_BF16)
+ * K % 128 == 0, K <= 2^22, M, N < 2^23 - 127 (BEAM_ERR_UNSUPPORTED otherwise).
+ * K == 0 gives zeros.  NaN codes (0x7F, 0xFF) are outside the contract.
+ * A linear layer's training step is three of them on what
+ * beam_moe_quant_e4m3_2d makes of x [M,K], dy [M,N] and w [N,K]:
+ *   y = x w^T    rows of x, blocks of w (straight)
+ *   dx = dy w    rows of dy, blocks of w (transposed)
+ *   dw = dy^T x  columns of dy, columns of x (both transposed, b_rows 1) */
+int beam_moe_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, const float* sa,
+                         const uint8_t* b, const float* sb, int32_t b_rows, int32_t dtype,
+                         void* y, void* stream);
+
+/* e4m3 quantisation of a matrix for products along its columns and along its
+ * rows, in one reading of it (scale = amax / 448 in binary32, 1 where that is
+ * 0; code = e4m3(v / scale), as beam_moe_quant_e4m3).  With R = 128
+ * ceil(rows/128) and C = 128 ceil(cols/128), and zeros past the end of v:
+ *   v   device [rows, cols] dtype (BEAM_F32 or BEAM_BF16)
+ *   q   device [rows, C] uint8 codes, or NULL
+ *   s   device fp32, with q: [rows, C/128] with block 0 (a scale for 128
+ *       columns of a row), [R/128, C/128] with block 1 (for 128 x 128 values)
+ *   qt  device [cols, R] uint8 codes of v transposed, or NULL (not both)
+ *   st  device fp32, with qt: [cols, R/128] with block 0 (a scale for 128 rows
+ *       of a column), [C/128, R/128] with block 1
+ * No workspace. */
+int beam_moe_quant_e4m3_2d(int64_t rows, int64_t cols, int32_t dtype, int32_t block,
+                           const void* v, uint8_t* q, float* s, uint8_t* qt, float* st,
+                           void* stream);
+
 /* ---- the step between two blocks -----------------------------------------
  * The norm after a block, its gate, the scaled residual stream and the norm
  * before the next block, per token t:

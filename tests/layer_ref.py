@@ -127,3 +127,38 @@ def norm_step_grad(rp, d_rp, dx, o, post, gate, pre, eps, alpha, beta, absolute=
     w = post * d
     out["d_o"] = inv * minus(w, hat * (w * hat).mean(1, keepdim=True))
     return out
+
+
+# ---- e4m3 products ----------------------------------------------------------
+
+def expand(s, n, k, rows):
+    """Block scales [ceil(n/128) or n, k/128] as one value per element."""
+    s = s.double()
+    if not rows:
+        s = s.repeat_interleave(128, 0)[:n]
+    return s.repeat_interleave(128, 1)
+
+
+def codes(q):
+    return q.view(torch.float8_e4m3fn).to(F64)
+
+
+def product(a, sa, b, sb, rows):
+    """(y, size): the scaled product in 64 bits and the sum of its terms'
+    absolute values."""
+    x = codes(a) * expand(sa, a.shape[0], a.shape[1], True)
+    w = codes(b) * expand(sb, b.shape[0], b.shape[1], rows)
+    return x @ w.t().contiguous(), x.abs() @ w.abs().t().contiguous()
+
+
+def quantise(v, block_rows, block_cols):
+    """(codes as values, scales) of v by blocks, the scale and the quotient
+    rounded to binary32 as the recipe has them; v padded with zeros."""
+    r, c = v.shape
+    p = torch.nn.functional.pad(v.double(), (0, -c % block_cols, 0, -r % block_rows))
+    R, C = p.shape[0] // block_rows, p.shape[1] // block_cols
+    p = p.view(R, block_rows, C, block_cols)
+    s = (p.abs().amax((1, 3)) / 448.0).float()
+    s = torch.where(s > 0, s, torch.ones_like(s))
+    q = (p / s.double()[:, None, :, None]).float().clamp(-448, 448).to(torch.float8_e4m3fn)
+    return q.view(R * block_rows, C * block_cols).view(torch.uint8), s

@@ -111,3 +111,53 @@ def test_norm_binding_checks():
         gl.norm_residual_backward(f)
     with pytest.raises(ValueError):
         gl.residual_scale(0)
+
+
+def _mm(**kw):
+    a = dict(M=4, N=8, K=256, a=GOOD, sa=GOOD, b=GOOD, sb=GOOD, rows=0, dtype=gl.BF16, y=GOOD)
+    a.update(kw)
+    return gl.lib().beam_moe_matmul_e4m3(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), gl.ERR_INVALID_ARG), (dict(N=-1), gl.ERR_INVALID_ARG), (dict(K=-128), gl.ERR_INVALID_ARG),
+    (dict(K=100), gl.ERR_UNSUPPORTED), (dict(K=1 << 23), gl.ERR_UNSUPPORTED), (dict(M=1 << 23), gl.ERR_UNSUPPORTED),
+    (dict(N=1 << 40), gl.ERR_UNSUPPORTED), (dict(rows=2), gl.ERR_INVALID_ARG),
+    (dict(dtype=gl.FP8_E4M3), gl.ERR_INVALID_ARG), (dict(a=None), gl.ERR_INVALID_ARG),
+    (dict(sa=None), gl.ERR_INVALID_ARG), (dict(b=None), gl.ERR_INVALID_ARG), (dict(sb=None), gl.ERR_INVALID_ARG),
+    (dict(y=None), gl.ERR_INVALID_ARG), (dict(a=BAD), gl.ERR_INVALID_ARG), (dict(sb=BAD), gl.ERR_INVALID_ARG),
+    (dict(y=BAD), gl.ERR_INVALID_ARG), (dict(M=0, a=None, sa=None, y=None), gl.OK), (dict(N=0, b=None), gl.OK),
+])
+def test_matmul_refuses(kw, status):
+    assert _mm(**kw) == status
+
+
+def _q2(**kw):
+    a = dict(rows=4, cols=8, dtype=gl.BF16, block=0, v=GOOD, q=GOOD, s=GOOD, qt=GOOD, st=GOOD)
+    a.update(kw)
+    return gl.lib().beam_moe_quant_e4m3_2d(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), gl.ERR_INVALID_ARG), (dict(cols=-1), gl.ERR_INVALID_ARG), (dict(dtype=7), gl.ERR_INVALID_ARG),
+    (dict(block=3), gl.ERR_INVALID_ARG), (dict(rows=1 << 40), gl.ERR_UNSUPPORTED), (dict(v=None), gl.ERR_INVALID_ARG),
+    (dict(q=None), gl.ERR_INVALID_ARG), (dict(st=None), gl.ERR_INVALID_ARG),
+    (dict(q=None, s=None, qt=None, st=None), gl.ERR_INVALID_ARG), (dict(qt=BAD), gl.ERR_INVALID_ARG),
+    (dict(rows=0, v=None), gl.OK), (dict(cols=0, v=None), gl.OK),
+])
+def test_quant_2d_refuses(kw, status):
+    assert _q2(**kw) == status
+
+
+def test_matmul_binding_checks():
+    a, s = torch.zeros(2, 128, dtype=torch.uint8), torch.ones(2, 1)
+    with pytest.raises(ValueError, match="GPU"):
+        gl.matmul_e4m3(a, s, a, s)
+    with pytest.raises(ValueError, match="multiple of 128"):
+        gl.matmul_e4m3(a[:, :100], s, a[:, :100], s)
+    with pytest.raises(ValueError, match="expected torch.bfloat16"):
+        gl.matmul_e4m3(a, s, a, s, dtype=torch.float16)
+    with pytest.raises(ValueError, match=r"\[M, K\]"):
+        gl.matmul_e4m3(a[0], s, a, s)
+    with pytest.raises(ValueError, match="GPU"):
+        gl.quant_e4m3_2d(torch.zeros(2, 3))
