@@ -168,9 +168,9 @@ hipError_t launch_norm_residual_backward(const NormGradArgs& a, int32_t dtype, f
 // matmul_fp8.hip: dense e4m3 products and their operands' quantisation
 hipError_t launch_quant_2d(int64_t rows, int64_t cols, int32_t dtype, bool block, const void* v,
                            uint8_t* q, float* s, uint8_t* qt, float* st, hipStream_t stream);
-// Byte offsets inside a tile of 256 rows are 32-bit; a grid has 2^16 rows of
-// 128-row tiles.
+// Byte offsets inside a tile of 256 rows are 32-bit; tiles are counted in 31.
 constexpr int64_t kMatmulMaxK = 1 << 22, kMatmulMaxRows = (1 << 23) - 128;
+constexpr int64_t kMatmulMaxOut = int64_t{1} << 38;
 hipError_t launch_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, const float* sa,
                               const uint8_t* b, const float* sb, bool rows, int32_t dtype,
                               void* y, hipStream_t s);

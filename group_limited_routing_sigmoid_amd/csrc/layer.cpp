@@ -148,7 +148,8 @@ int beam_moe_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, cons
   if (M < 0 || N < 0 || K < 0 || (dtype != BEAM_F32 && dtype != BEAM_BF16) ||
       (b_rows != 0 && b_rows != 1))
     return BEAM_ERR_INVALID_ARG;
-  if (K % 128 || K > kMatmulMaxK || M > kMatmulMaxRows || N > kMatmulMaxRows)
+  if (K % 128 || K > kMatmulMaxK || M > kMatmulMaxRows || N > kMatmulMaxRows ||
+      M * N > kMatmulMaxOut)
     return BEAM_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return BEAM_OK;
   if (!y || (K > 0 && (!a || !sa || !b || !sb))) return BEAM_ERR_INVALID_ARG;

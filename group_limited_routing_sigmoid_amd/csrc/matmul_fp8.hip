@@ -16,22 +16,21 @@
 // (2.07 against 4.04 PFLOP/s measured), which hold every product and sum
 // binary32: an e4m3 value is a bf16 value, and one conversion instruction
 // expands two codes.
+#include <algorithm>
 #include <type_traits>
 
-#include "common.h"
-#include "internal.h"
+#include "grouped_tile.h"
 
 namespace beam {
 namespace {
 
 constexpr int kRow = 128;  // bytes of a tile row: one block of 128 codes
 
-// D = A(32x64) * B(64x32) + C on e4m3 codes (format 0, unit E8M0 scales).
-// Lane l supplies row (l % 32) of A and column (l % 32) of B, codes
-// 32*(l/32) .. +32 of the 64-deep slice; element r of lane l is
-// C[8*(r/4) + 4*(l/32) + r%4][l % 32].
-__device__ __forceinline__ f32x16 mfma_e4m3(i32x8 a, i32x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
+// D = A(16x128) * B(128x16) + C on e4m3 codes (format 0, unit E8M0 scales).
+// Lane l supplies row (l % 16) of A and column (l % 16) of B, codes
+// 32*(l/16) .. +32; element r of lane l is C[4*(l/16) + r][l % 16].
+__device__ __forceinline__ f32x4 mfma_e4m3(i32x8 a, i32x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
 }
 
 // The lane's 32 codes as four bf16 fragments of 8 (both operands take the
@@ -55,21 +54,22 @@ __device__ __forceinline__ Wide widen(i32x8 q) {
     }
   return w;
 }
-__device__ __forceinline__ f32x16 mfma_wide(const Wide& a, const Wide& b, f32x16 c) {
+__device__ __forceinline__ f32x4 mfma_wide(const Wide& a, const Wide& b, f32x4 c) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) c = mfma32x32x16(a.f[j], b.f[j], c);
+  for (int j = 0; j < 4; ++j) c = mfma16x16x32(a.f[j], b.f[j], c);
   return c;
 }
 
-// Swizzle of a tile row's eight 16-byte chunks: the chunks of any 8
-// consecutive rows, and of the even or odd rows of any 16, lie on distinct
-// bank groups.
-__device__ __forceinline__ int key(int row) { return (row ^ (row >> 3)) & 7; }
+// Swizzle of a tile row's eight 16-byte chunks: the same chunk of any 16
+// consecutive rows lies in 16 different places of the LDS banks' 256 bytes
+// (rows 2i and 2i + 1 in its two halves), and the key repeats every 16 rows,
+// so one lane offset serves every fragment.
+__device__ __forceinline__ int key(int row) { return (row >> 1) & 7; }
 
-// Codes of half h (64 deep) of the lane's row of a 32-row fragment starting
-// at tile row `row0`.
-__device__ __forceinline__ i32x8 frag(const unsigned char* tile, int row0, int lane, int h) {
-  const int row = row0 + lane % 32, c = 4 * h + 2 * (lane / 32);
+// The lane's codes of a 16-row fragment starting at tile row `row0`: its row
+// l % 16, the 32 codes from 32 (l / 16) of the block.
+__device__ __forceinline__ i32x8 frag(const unsigned char* tile, int row0, int lane) {
+  const int row = row0 + lane % 16, c = 2 * (lane / 16);
   const unsigned char* p = tile + row * kRow;
   const u32x4 lo = *reinterpret_cast<const u32x4*>(p + ((c ^ key(row)) << 4));
   const u32x4 hi = *reinterpret_cast<const u32x4*>(p + (((c + 1) ^ key(row)) << 4));
@@ -80,48 +80,144 @@ __device__ __forceinline__ i32x8 frag(const unsigned char* tile, int row0, int l
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = f32_to_bf16_bits(v); }
 
-// A BM x BN tile of y by WM x WN waves of (BM/WM) x (BN/WN).  The b matrix is
-// the matrix cores' row operand, so a lane holds outputs of one row of y:
-// the row's scale is one register, and the columns' scales are uniform over a
-// wave (sb for 128 x 128 blocks) or lie in LDS (ROWS: sb for each row of b).
-// Tiles and scale words are copied straight to LDS, two stages of one block
-// each: stage kb + 1 is on its way while stage kb is multiplied.
-template <int BM, int BN, int WM, int WN, bool ROWS, typename OUT>
-__global__ __launch_bounds__(64 * WM * WN) void matmul_tile(
+// As dma16, from a buffer at byte offset voff + soff (soff uniform).
+__device__ __forceinline__ void buf_dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, void* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff,
+                                           0, 0);
+}
+
+// Four neighbouring values of a row to LDS.
+__device__ __forceinline__ void put4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{a, b, c, d};
+}
+__device__ __forceinline__ void put4(uint16_t* p, float a, float b, float c, float d) {
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(f32_to_bf16_bits(a) | static_cast<uint32_t>(f32_to_bf16_bits(b)) << 16,
+                 f32_to_bf16_bits(c) | static_cast<uint32_t>(f32_to_bf16_bits(d)) << 16);
+}
+
+// Orders a wave's LDS writes before its other lanes' reads (a wave's LDS
+// operations complete in order; this holds the compiler to it).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// A wave's fragments to y, 32 rows at a time through its own room in LDS, so
+// that they leave as whole runs of y's rows (a lane's own values lie in one
+// row, a column apart from its neighbour's: stored directly they took a third
+// of the time of a large product).  The wave's part starts at row rw, column
+// cw of the tile at (m0, n0), whose last row and column are mr and nr.
+template <int FM, int FN, int TN, typename OUT>
+__device__ __forceinline__ void store_tile(OUT* room, int lane, const f32x4 (&acc)[FN][FM], OUT* y,
+                                           int64_t m0, int rw, int mr, int64_t N, int64_t n0, int cw,
+                                           int nr) {
+  constexpr int kVec = 16 / static_cast<int>(sizeof(OUT)), kPitch = TN + kVec, kChunks = TN / kVec;
+  constexpr int kRows = FM == 1 ? 16 : 32;
+  const bool vec = N % kVec == 0;  // every row of y then starts 16-byte aligned
+#pragma unroll
+  for (int m = 0; m < FM; m += 2) {
+#pragma unroll
+    for (int i = 0; i < kRows / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+        put4(room + (16 * i + lane % 16) * kPitch + 16 * n + 4 * (lane / 16), acc[n][m + i][0],
+             acc[n][m + i][1], acc[n][m + i][2], acc[n][m + i][3]);
+    wave_sync();
+    const int row0 = rw + 16 * m;
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < kRows * kChunks / kWave; ++i) {
+        const int r = (i * kWave + lane) / kChunks, c = (i * kWave + lane) % kChunks * kVec;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(room + r * kPitch + c);
+        // N % kVec == 0: a chunk that starts inside the row ends inside it
+        if (row0 + r <= mr && cw + c <= nr) st16(y + (m0 + row0 + r) * N + n0 + cw + c, v);
+      }
+    } else {
+      for (int i = 0; i < kRows * TN / kWave; ++i) {
+        const int r = (i * kWave + lane) / TN, c = (i * kWave + lane) % TN;
+        const OUT v = room[r * kPitch + c];
+        if (row0 + r <= mr && cw + c <= nr) y[(m0 + row0 + r) * N + n0 + cw + c] = v;
+      }
+    }
+    wave_sync();
+  }
+}
+
+// A BM x BN tile of y.  The workgroup's waves form KS groups of WM x WN, each
+// wave with a (BM/WM) x (BN/WN) part of the tile; group g takes the blocks g,
+// g + KS, ... along k, so that small tiles still have many waves and long
+// copies (the groups' sums meet in LDS at the end, added in group order).
+// The b matrix is the matrix cores' row operand, so a lane holds outputs of
+// one row of y: the row's scale is one register, and the columns' scales are
+// uniform over a wave (sb for 128 x 128 blocks) or lie in LDS (ROWS: sb for
+// each row of b).  Tiles and scale words are copied straight to LDS through a
+// ring of ST stages of KS blocks, ST - 1 of them in flight while one is
+// multiplied.  Each group copies its own block; a wave issues the same number
+// of copies for every block, so "a stage has landed" is a count of
+// outstanding copies.
+template <int BM, int BN, int KS, int WM, int WN, int ST, bool ROWS, typename OUT>
+__global__ __launch_bounds__(64 * KS * WM * WN) void matmul_tile(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ b,
     const float* __restrict__ sb, OUT* __restrict__ y, int64_t M, int64_t N, int64_t K) {
-  constexpr int W = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
-  constexpr int kScales = (BM + BN) * kRow, kStage = kScales + (BM + BN) * 4;
-  __shared__ __attribute__((aligned(16))) unsigned char lds[2][kStage];
+  constexpr int G = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  constexpr int kScales = (BM + BN) * kRow;                    // scale words after the tiles
+  constexpr int kWords = ((BM + BN + 63) / 64) * 64;           // copied 64 at a time
+  constexpr int kBlock = kScales + kWords * 4, kStage = KS * kBlock;
+  constexpr int kPart = FN * FM * 4 * kWave * G * 4;          // a group's sums
+  constexpr int kRoom = 32 * (TN * static_cast<int>(sizeof(OUT)) + 16);  // a wave's, to store from
+  constexpr int kLds = std::max({ST * kStage, (KS - 1) * kPart, G * kRoom});
+  static_assert(TM % 32 == 0 && TN % 16 == 0 && TN <= 128, "tile shape");
+  __shared__ __attribute__((aligned(16))) unsigned char lds[kLds];
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int wm = wave / WN, wn = wave % WN;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * BM, n0 = static_cast<int64_t>(blockIdx.x) * BN;
+  const int g = wave / G, wg = wave % G, wm = wg / WN, wn = wg % WN;
+  const uint32_t nt = static_cast<uint32_t>((N + BN - 1) / BN);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x / nt) * BM, n0 = static_cast<int64_t>(blockIdx.x % nt) * BN;
   const int nkb = static_cast<int>(K / 128);
 
-  // rows past the matrices' ends repeat the last one; nothing of them is stored
+  // rows past the matrices' ends repeat the last one (whole 8-row regions of
+  // a past it are not copied); nothing of them is stored
   const int mr = static_cast<int>(min(M - m0, static_cast<int64_t>(BM))) - 1;
   const int nr = static_cast<int>(min(N - n0, static_cast<int64_t>(BN))) - 1;
+  constexpr int NA = (BM / 8 + G - 1) / G, NB = (BN / 8 + G - 1) / G, NS = (kWords / 64 + G - 1) / G;
+  const uint8_t* at0 = a + m0 * K;
+  const uint8_t* bt0 = b + n0 * K;
+  uint32_t aoff[NA], boff[NB];
+  const float* soff[NS];
+  int copies = 0;
+#pragma unroll
+  for (int i = 0; i < NA; ++i) {
+    const int row = 8 * (wg + i * G) + lane / 8;
+    aoff[i] = static_cast<uint32_t>(min(row, mr)) * static_cast<uint32_t>(K) + (((lane % 8) ^ key(row)) << 4);
+    copies += (8 * (wg + i * G) <= mr) ? 1 : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int row = 8 * (wg + i * G) + lane / 8;
+    boff[i] = static_cast<uint32_t>(min(row, nr)) * static_cast<uint32_t>(K) + (((lane % 8) ^ key(row)) << 4);
+    copies += (8 * (wg + i * G) < BN) ? 1 : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const int w = 64 * (wg + i * G) + lane;  // tile rows of a, then of b
+    const int64_t r = w < BM ? m0 + min(w, mr) : n0 + min(w - BM, nr);
+    soff[i] = w < BM ? sa + r * nkb : sb + (ROWS ? r : r / 128) * nkb;
+    copies += (64 * (wg + i * G) < kWords) ? 1 : 0;
+  }
   auto copy = [&](int st, int kb) {
+    unsigned char* at = lds + st * kStage + g * kBlock;
+    unsigned char* bt = at + BM * kRow;
 #pragma unroll
-    for (int i = wave; i < BM / 8; i += W) {
-      const int row = 8 * i + lane / 8;
-      dma16(a + (m0 + min(row, mr)) * K + kb * 128 + (((lane % 8) ^ key(row)) << 4),
-            &lds[st][i * 1024]);
-    }
+    for (int i = 0; i < NB; ++i)
+      if (8 * (wg + i * G) < BN) dma16(bt0 + (boff[i] + kb * 128), bt + (wg + i * G) * 1024);
 #pragma unroll
-    for (int i = wave; i < BN / 8; i += W) {
-      const int row = 8 * i + lane / 8;
-      dma16(b + (n0 + min(row, nr)) * K + kb * 128 + (((lane % 8) ^ key(row)) << 4),
-            &lds[st][BM * kRow + i * 1024]);
-    }
+    for (int i = 0; i < NA; ++i)
+      if (8 * (wg + i * G) <= mr) dma16(at0 + (aoff[i] + kb * 128), at + (wg + i * G) * 1024);
 #pragma unroll
-    for (int i = wave; i < (BM + BN) / 64; i += W) {
-      const int row = 64 * i + lane;
-      const int64_t r = i < BM / 64 ? m0 + min(row, mr) : n0 + min(row - BM, nr);
-      const float* s = i < BM / 64 ? sa + r * nkb : sb + (ROWS ? r : r / 128) * nkb;
-      dma4(s + kb, &lds[st][kScales + 256 * i]);
-    }
+    for (int i = 0; i < NS; ++i)
+      if (64 * (wg + i * G) < kWords) dma4(soff[i] + kb, at + kScales + (wg + i * G) * 256);
   };
 
   constexpr bool kWide = sizeof(OUT) == 4;  // binary32 results: binary32 sums
@@ -130,60 +226,285 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_tile(
     if constexpr (kWide) return widen(q);
     else return q;
   };
-  auto product = [](const Frag& x, const Frag& w, f32x16 c) {
-    if constexpr (kWide) return mfma_wide(x, w, c);
-    else return mfma_e4m3(x, w, c);
+  auto product = [](const Frag& x, const Frag& w) {
+    if constexpr (kWide) return mfma_wide(x, w, f32x4{});
+    else return mfma_e4m3(x, w, f32x4{});
   };
-  f32x16 acc[FN][FM];
+  f32x4 acc[FN][FM];
 #pragma unroll
   for (int n = 0; n < FN; ++n)
 #pragma unroll
-    for (int m = 0; m < FM; ++m) acc[n][m] = f32x16{};
-  if (nkb > 0) copy(0, 0);
-  __syncthreads();
-  for (int kb = 0; kb < nkb; ++kb) {
-    const unsigned char* at = lds[kb & 1];
-    const unsigned char* bt = at + BM * kRow;
-    const float* sat = reinterpret_cast<const float*>(at + kScales) + wm * TM;
-    const float* sbt = reinterpret_cast<const float*>(at + kScales) + BM + wn * TN;
-    if (kb + 1 < nkb) copy((kb + 1) & 1, kb + 1);
-    Frag bf[FN][2];
+    for (int m = 0; m < FM; ++m) acc[n][m] = f32x4{};
+
+  const int stages = (nkb + KS - 1) / KS;
+  // copies of this wave's block of stage s (none where the last stage has no block for it)
+  auto issued = [&](int s) { return s < stages && s * KS + g < nkb ? copies : 0; };
 #pragma unroll
-    for (int n = 0; n < FN; ++n)
+  for (int s = 0; s < ST - 1; ++s)
+    if (s * KS + g < nkb) copy(s, s * KS + g);
+  {
+    int later = 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) bf[n][h] = operand(frag(bt, wn * TN + 32 * n, lane, h));
+    for (int s = 1; s < ST - 1; ++s) later += issued(s);
+    tile::ring_barrier(later);
+  }
+  int st = 0;
+  for (int s = 0; s < stages; ++s) {
+    const int kn = (s + ST - 1) * KS + g;
+    if (kn < nkb) copy(st == 0 ? ST - 1 : st - 1, kn);  // the stage multiplied last time
+    if (s * KS + g < nkb) {
+      const unsigned char* at = lds + st * kStage + g * kBlock;
+      const unsigned char* bt = at + BM * kRow;
+      const float* sat = reinterpret_cast<const float*>(at + kScales) + wm * TM;
+      const float* sbt = reinterpret_cast<const float*>(at + kScales) + BM + wn * TN;
+      Frag bf[FN];
 #pragma unroll
-    for (int m = 0; m < FM; ++m) {
-      const Frag a0 = operand(frag(at, wm * TM + 32 * m, lane, 0));
-      const Frag a1 = operand(frag(at, wm * TM + 32 * m, lane, 1));
-      const float s = sat[32 * m + lane % 32] * (ROWS ? 1.0f : sbt[0]);
+      for (int n = 0; n < FN; ++n) bf[n] = operand(frag(bt, wn * TN + 16 * n, lane));
+      // Products of row fragment m beside the multiply-adds of fragment m - 1
+      // (one product, then four of those), its successor's codes on their way.
+      f32x4 p[2][FN];
+      float sc[2];
+      auto add = [&](int m, int n) {
 #pragma unroll
-      for (int n = 0; n < FN; ++n) {
-        f32x16 p = product(bf[n][0], a0, f32x16{});
-        p = product(bf[n][1], a1, p);
+        for (int r = 0; r < 4; ++r) {
+          const float sr = ROWS ? sc[m & 1] * sbt[16 * n + 4 * (lane / 16) + r] : sc[m & 1];
+          acc[n][m][r] = __builtin_fmaf(p[m & 1][n][r], sr, acc[n][m][r]);
+        }
+      };
+      i32x8 next = frag(at, wm * TM, lane);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float sr = ROWS ? s * sbt[32 * n + 8 * (r / 4) + 4 * (lane / 32) + r % 4] : s;
-          acc[n][m][r] = __builtin_fmaf(p[r], sr, acc[n][m][r]);
+      for (int m = 0; m < FM; ++m) {
+        const Frag af = operand(next);
+        if (m + 1 < FM) next = frag(at, wm * TM + 16 * (m + 1), lane);
+        sc[m & 1] = sat[16 * m + lane % 16] * (ROWS ? 1.0f : sbt[0]);
+#pragma unroll
+        for (int n = 0; n < FN; ++n) {
+          p[m & 1][n] = product(bf[n], af);
+          if (m > 0) add(m - 1, n);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
+#pragma unroll
+      for (int n = 0; n < FN; ++n) add(FM - 1, n);
     }
-    __syncthreads();  // waits for this wave's copies, then for every wave
+    int later = 0;
+#pragma unroll
+    for (int i = 2; i < ST; ++i) later += issued(s + i);
+    tile::ring_barrier(later);  // stage s + 1 has landed, stage s is read
+    st = (st == ST - 1) ? 0 : st + 1;
   }
 
+  if constexpr (KS > 1) {
+    f32x4* part = reinterpret_cast<f32x4*>(lds);
+    if (g > 0) {
 #pragma unroll
-  for (int m = 0; m < FM; ++m) {
-    const int row = wm * TM + 32 * m + lane % 32;
-    if (row > mr) continue;
-    OUT* yr = y + (m0 + row) * N + n0;
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+          part[((((g - 1) * G + wg) * FN + n) * FM + m) * kWave + lane] = acc[n][m];
+    }
+    __syncthreads();
+    if (g == 0)
+#pragma unroll
+      for (int o = 0; o < KS - 1; ++o)
+#pragma unroll
+        for (int n = 0; n < FN; ++n)
+#pragma unroll
+          for (int m = 0; m < FM; ++m)
+            acc[n][m] += part[(((o * G + wg) * FN + n) * FM + m) * kWave + lane];
+    __syncthreads();
+    if (g > 0) return;
+  }
+  store_tile<FM, FN, TN>(reinterpret_cast<OUT*>(lds + wg * kRoom), lane, acc, y, m0, wm * TM, mr, N, n0,
+                         wn * TN, nr);
+}
+
+// ---- many rows -------------------------------------------------------------
+// 256-column tiles of BM rows (256; 128 for binary32 results, whose widened
+// fragments take twice the registers), eight waves of BM/2 x 64, one
+// workgroup per compute unit, two stages of one block.  The next stage's
+// copies are spread over the products (nine instructions a wave: issued
+// together they fill the unit's texture path and hold up every wave's LDS
+// reads).
+//
+// Order of the tiles: workgroups are dealt round-robin to the 8 XCDs, each
+// with its own L2, so workgroup b takes the (b / 8) % 32-th tile of chunk
+// b % 8 of its round of 256 (one tile per compute unit), a chunk being about
+// 4 tiles along m by 8 along n that share their operands in one L2.  The last
+// round's tiles, when they are at most a half or a quarter of the compute
+// units, are cut into halves or quarters along m, so that every unit has a
+// piece of it.
+struct TileGrid {
+  int full;     // workgroups of whole rounds of 256 tiles
+  int rest;     // tiles of the last round
+  int split;    // pieces each is cut into: 1, 2 or 4
+  int nt, mt;   // tiles along n and m
+};
+
+template <int BM, bool ROWS, typename OUT>
+struct Many {
+  static constexpr bool kWide = sizeof(OUT) == 4;
+  static constexpr int BN = 256, TN = 64, FN = TN / 16, W = 8;
+  static constexpr int kScales = (BM + BN) * kRow, kStage = kScales + (BM + BN) * 4;
+  static constexpr int kRoom = 32 * (TN * static_cast<int>(sizeof(OUT)) + 16);
+  static constexpr int kLds = std::max(2 * kStage, W * kRoom);
+  using Frag = std::conditional_t<kWide, Wide, i32x8>;
+
+  // FM: 16-row fragments of a wave (its share of 2 * 16 FM rows).
+  template <int FM>
+  static __device__ __forceinline__ void run(unsigned char* lds, const uint8_t* a, const float* sa,
+                                             const uint8_t* b, const float* sb, OUT* y, int64_t M,
+                                             int64_t N, int64_t K, int64_t m0, int64_t n0) {
+    constexpr int R = 32 * FM, TM = 16 * FM;  // rows of the piece, of a wave
+    constexpr int NA = (R + 63) / 64, NB = BN / 64;  // copies of 8 rows a wave
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave / 4, wn = wave % 4;
+    const int nkb = static_cast<int>(K / 128);
+    // rows past the matrices' ends repeat the last one; nothing of them is stored
+    const int mr = static_cast<int>(min(M - m0, static_cast<int64_t>(R))) - 1;
+    const int nr = static_cast<int>(min(N - n0, static_cast<int64_t>(BN))) - 1;
+    // One lane offset serves every copy of an operand: copy c's rows are 64 c
+    // further, a scalar offset, and the buffer's extent ends with the last
+    // row (what stands in LDS beyond it is not stored).  The extent is
+    // compared with the lane's offset after subtracting the scalar one, so a
+    // copy of only missing rows repeats the first instead.
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a + m0 * K, static_cast<uint32_t>(mr + 1) * static_cast<uint32_t>(K));
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(b + n0 * K, static_cast<uint32_t>(nr + 1) * static_cast<uint32_t>(K));
+    const int crow = 8 * wave + lane / 8;
+    const uint32_t coff = static_cast<uint32_t>(crow) * static_cast<uint32_t>(K) + (((lane % 8) ^ key(crow)) << 4);
+    uint32_t astep[NA], bstep[NB];
+#pragma unroll
+    for (int i = 0; i < NA; ++i) astep[i] = 64 * i <= mr ? 64u * i * static_cast<uint32_t>(K) : 0u;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) bstep[i] = 64 * i <= nr ? 64u * i * static_cast<uint32_t>(K) : 0u;
+    // scale words: waves 0-3 of the b rows, the others of the a rows (where
+    // there are fewer, two waves copy the same)
+    const int sw = wave < 4 ? wave : (wave - 4) % (BM / 64), srow = 64 * sw + lane;
+    const float* soff;
+    if (wave < 4) {
+      const int64_t r = n0 + min(srow, nr);
+      soff = sb + (ROWS ? r : r / 128) * nkb;
+    } else {
+      soff = sa + (m0 + min(srow, mr)) * nkb;
+    }
+    const int sdst = kScales + (wave < 4 ? BM * 4 : 0) + sw * 256;
+    auto copy = [&](int st, int kb, int c) {
+      unsigned char* t = lds + st * kStage;
+      if (c < NB) buf_dma16(rb, coff, bstep[c < NB ? c : 0] + kb * 128, t + BM * kRow + (wave + W * c) * 1024);
+      else if (c < NB + NA) buf_dma16(ra, coff, astep[c < NB ? 0 : c - NB < NA ? c - NB : 0] + kb * 128, t + (wave + W * (c - NB)) * 1024);
+      else dma4(soff + kb, t + sdst);
+    };
+    auto operand = [](i32x8 q) {
+      if constexpr (kWide) return widen(q);
+      else return q;
+    };
+    auto product = [](const Frag& x, const Frag& w) {
+      if constexpr (kWide) return mfma_wide(x, w, f32x4{});
+      else return mfma_e4m3(x, w, f32x4{});
+    };
+    f32x4 acc[FN][FM];
 #pragma unroll
     for (int n = 0; n < FN; ++n)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int col = wn * TN + 32 * n + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
-        if (col <= nr) put(yr + col, acc[n][m][r]);
+      for (int m = 0; m < FM; ++m) acc[n][m] = f32x4{};
+    constexpr int kCopies = NA + NB + 1, kEach = (kCopies + FM * FN - 1) / (FM * FN);
+    constexpr int kLag = 3;  // products between a product and its multiply-adds
+    if (nkb > 0)
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) copy(0, 0, c);
+    __syncthreads();
+    // the lane's place in its fragments: chunks 2 (l / 16) and the next one
+    const int f0 = (lane % 16) * kRow + ((2 * (lane / 16) ^ key(lane % 16)) << 4);
+    auto codes = [&](const unsigned char* t) {
+      const u32x4 lo = *reinterpret_cast<const u32x4*>(t + f0);
+      const u32x4 hi = *reinterpret_cast<const u32x4*>(t + (f0 ^ 16));
+      return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                   (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    };
+    for (int kb = 0; kb < nkb; ++kb) {
+      const unsigned char* at = lds + (kb & 1) * kStage + wm * TM * kRow;
+      const unsigned char* bt = lds + (kb & 1) * kStage + (BM + wn * TN) * kRow;
+      const float* sat = reinterpret_cast<const float*>(lds + (kb & 1) * kStage + kScales) + wm * TM + lane % 16;
+      const float* sbt = reinterpret_cast<const float*>(lds + (kb & 1) * kStage + kScales) + BM + wn * TN;
+      const int kn = min(kb + 1, nkb - 1);  // the last stage's copies are not used
+      Frag bf[FN];
+      f32x4 sr[ROWS ? FN : 1];
+      float sc[2];
+      i32x8 next = codes(at);
+      sc[0] = sat[0] * (ROWS ? 1.0f : sbt[0]);
+#pragma unroll
+      for (int n = 0; n < FN; ++n) bf[n] = operand(codes(bt + 16 * n * kRow));
+      if (ROWS) {
+#pragma unroll
+        for (int n = 0; n < FN; ++n)
+          sr[ROWS ? n : 0] = *reinterpret_cast<const f32x4*>(sbt + 16 * n + 4 * (lane / 16));
       }
+      // Beside each product the multiply-adds of the third one before it
+      // (whose sums are ready by then), the next row fragment's codes and the
+      // next stage's copies on their way.
+      f32x4 p[kLag + 1];
+      auto add = [&](int i) {  // the block's sums of product i into the result's
+        const int m = i / FN, n = i % FN;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[n][m][r] = __builtin_fmaf(p[i % (kLag + 1)][r],
+                                        ROWS ? sc[m & 1] * sr[ROWS ? n : 0][r] : sc[m & 1], acc[n][m][r]);
+      };
+#pragma unroll
+      for (int m = 0; m < FM; ++m) {
+        const Frag af = operand(next);
+        float scn = 0.0f;
+#pragma unroll
+        for (int n = 0; n < FN; ++n) {
+          const int i = m * FN + n;
+          p[i % (kLag + 1)] = product(bf[n], af);
+          __builtin_amdgcn_sched_barrier(0);
+          if (n == 0 && m + 1 < FM) {
+            next = codes(at + 16 * (m + 1) * kRow);
+            scn = sat[16 * (m + 1)];
+          }
+          if (i >= kLag) add(i - kLag);
+#pragma unroll
+          for (int c = i * kEach; c < (i + 1) * kEach && c < kCopies; ++c) copy((kb + 1) & 1, kn, c);
+          if (n == FN - 1 && m + 1 < FM) sc[(m + 1) & 1] = scn * (ROWS ? 1.0f : sbt[0]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int i = FM * FN - kLag; i < FM * FN; ++i) add(i);
+      __syncthreads();  // waits for this wave's copies, then for every wave
+    }
+    store_tile<FM, FN, TN>(reinterpret_cast<OUT*>(lds + wave * kRoom), lane, acc, y, m0, wm * TM, mr, N,
+                           n0, wn * TN, nr);
   }
+};
+
+template <int BM, bool ROWS, typename OUT>
+__global__ __launch_bounds__(512, 2) void matmul_many(
+    const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ b,
+    const float* __restrict__ sb, OUT* __restrict__ y, int64_t M, int64_t N, int64_t K, TileGrid t) {
+  using T = Many<BM, ROWS, OUT>;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[T::kLds];
+  int L = blockIdx.x, piece = 0, split = 1;
+  if (L < t.full) {
+    L = (L / 256 * 8 + L % 8) * 32 + L / 8 % 32;
+  } else {
+    const int u = L - t.full, per = (t.rest * t.split + 7) / 8;  // an XCD's pieces
+    const int i = u % 8 * per + u / 8;
+    if (u / 8 >= per || i >= t.rest * t.split) return;
+    split = t.split;
+    L = t.full + i / split;
+    piece = i % split;
+  }
+  const int band = L / (4 * t.nt), gm = min(4, t.mt - 4 * band), j = L - band * 4 * t.nt;
+  const int quad = j / (gm * 8), rem = j - quad * gm * 8;
+  const int64_t n0 = static_cast<int64_t>(quad * 8 + rem / gm) * T::BN;
+  const int64_t m0 = static_cast<int64_t>(4 * band + rem % gm) * BM + piece * (BM / split);
+  if (m0 >= M) return;
+  if (split == 1) T::template run<BM / 32>(lds, a, sa, b, sb, y, M, N, K, m0, n0);
+  else if (split == 2) T::template run<BM / 64>(lds, a, sa, b, sb, y, M, N, K, m0, n0);
+  else T::template run<BM / 128>(lds, a, sa, b, sb, y, M, N, K, m0, n0);
 }
 
 // ---- quantisation in both orientations --------------------------------------
@@ -310,6 +631,83 @@ __global__ __launch_bounds__(256) void quant_2d(const IO* __restrict__ v, int64_
   }
 }
 
+// The form of a product: the one whose tiles are estimated to take least time,
+// rounds of 256 tiles (one per compute unit) times the time of a tile's
+// 128-deep block.  Microseconds a block, measured at K = 5120 with 160 tiles:
+//   32 x 16 0.09, 32 x 32 0.14, 64 x 16 0.16, 64 x 32 0.24, 64 x 64 0.34,
+//   128 x 64 0.52, 128 x 128 0.85; 256 x 256 1.73, its halves 1.27 and
+//   quarters 1.0 (whole products of 5120 x 5120 by N = 5120: 1 row 8.5 us, 64
+//   rows 12.4, 128 rows 16.7, 256 rows 23.8, 512 rows 37, 1024 rows 54).
+struct Shape {
+  int bm, bn;
+  float us;
+};
+constexpr Shape kShapes[] = {{32, 16, 0.09f},  {32, 32, 0.14f},  {64, 16, 0.16f},  {64, 32, 0.24f},
+                             {64, 64, 0.34f},  {128, 64, 0.52f}, {128, 128, 0.85f}};
+constexpr int kShapeMany = 7;
+
+TileGrid tile_grid(int64_t M, int64_t N, int bm) {
+  TileGrid t;
+  t.nt = static_cast<int>(ceil_div(N, 256));
+  t.mt = static_cast<int>(ceil_div(M, bm));
+  const int64_t tiles = static_cast<int64_t>(t.nt) * t.mt;
+  t.full = static_cast<int>(tiles / 256 * 256);
+  t.rest = static_cast<int>(tiles - t.full);
+  t.split = 1;
+  while (t.split < 4 && t.rest * t.split * 2 <= 256) t.split *= 2;
+  return t;
+}
+
+int choose_shape(int64_t M, int64_t N) {
+  int best = 0;
+  float least = 0.0f;
+  for (int i = 0; i <= kShapeMany; ++i) {
+    float us;
+    if (i < kShapeMany) {
+      const Shape& s = kShapes[i];
+      us = static_cast<float>(ceil_div(ceil_div(M, s.bm) * ceil_div(N, s.bn), 256)) * s.us;
+    } else {
+      const TileGrid t = tile_grid(M, N, 256);
+      us = static_cast<float>(t.full / 256) * 1.73f;
+      if (t.rest) us += t.split == 1 ? 1.73f : t.split == 2 ? 1.27f : 1.0f;
+    }
+    if (i == 0 || us < least) {
+      least = us;
+      best = i;
+    }
+  }
+  return best;
+}
+
+template <bool ROWS, typename OUT>
+void launch_product(int64_t M, int64_t N, int64_t K, const uint8_t* a, const float* sa,
+                    const uint8_t* b, const float* sb, void* y, hipStream_t s) {
+  OUT* out = static_cast<OUT*>(y);
+  const int shape = choose_shape(M, N);
+  if (shape == kShapeMany) {
+    constexpr int BM = sizeof(OUT) == 4 ? 128 : 256;
+    const TileGrid t = tile_grid(M, N, BM);
+    const int grid = t.full + static_cast<int>(ceil_div(t.rest * t.split, 8)) * 8;
+    hipLaunchKernelGGL((matmul_many<BM, ROWS, OUT>), dim3(grid), dim3(512), 0, s, a, sa, b, sb, out,
+                       M, N, K, t);
+    return;
+  }
+#define BEAM_TILE(BM, BN, KS, WM, WN, ST)                                                       \
+  hipLaunchKernelGGL((matmul_tile<BM, BN, KS, WM, WN, ST, ROWS, OUT>),                          \
+                     dim3(static_cast<unsigned>(ceil_div(N, BN) * ceil_div(M, BM))),            \
+                     dim3(64 * KS * WM * WN), 0, s, a, sa, b, sb, out, M, N, K)
+  switch (shape) {
+    case 0: BEAM_TILE(32, 16, 8, 1, 1, 3); break;
+    case 1: BEAM_TILE(32, 32, 4, 1, 1, 3); break;
+    case 2: BEAM_TILE(64, 16, 4, 2, 1, 3); break;
+    case 3: BEAM_TILE(64, 32, 4, 2, 2, 3); break;
+    case 4: BEAM_TILE(64, 64, 2, 2, 2, 3); break;
+    case 5: BEAM_TILE(128, 64, 2, 4, 1, 3); break;
+    default: BEAM_TILE(128, 128, 1, 2, 4, 3); break;
+  }
+#undef BEAM_TILE
+}
+
 }  // namespace
 
 hipError_t launch_quant_2d(int64_t rows, int64_t cols, int32_t dtype, bool block, const void* v,
@@ -341,19 +739,13 @@ hipError_t launch_quant_2d(int64_t rows, int64_t cols, int32_t dtype, bool block
 hipError_t launch_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, const float* sa,
                               const uint8_t* b, const float* sb, bool rows, int32_t dtype,
                               void* y, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(N, 128)), static_cast<unsigned>(ceil_div(M, 128)));
-#define BEAM_MM2(R, OUT)                                                                      \
-  hipLaunchKernelGGL((matmul_tile<128, 128, 2, 2, R, OUT>), grid, dim3(256), 0, s, a, sa, b,  \
-                     sb, static_cast<OUT*>(y), M, N, K)
-#define BEAM_MM1(OUT)             \
-  do {                            \
-    if (rows) BEAM_MM2(true, OUT); \
-    else BEAM_MM2(false, OUT);    \
-  } while (0)
-  if (dtype == BEAM_BF16) BEAM_MM1(uint16_t);
-  else BEAM_MM1(float);
-#undef BEAM_MM1
-#undef BEAM_MM2
+  if (dtype == BEAM_BF16) {
+    if (rows) launch_product<true, uint16_t>(M, N, K, a, sa, b, sb, y, s);
+    else launch_product<false, uint16_t>(M, N, K, a, sa, b, sb, y, s);
+  } else {
+    if (rows) launch_product<true, float>(M, N, K, a, sa, b, sb, y, s);
+    else launch_product<false, float>(M, N, K, a, sa, b, sb, y, s);
+  }
   return hipGetLastError();
 }
 

@@ -314,7 +314,8 @@ int beam_moe_forward_residual(const beam_moe_desc* desc, int64_t T, const void* 
  *   sb  device fp32: [ceil(N/128), K/128] with b_rows 0 (a scale for each
  *       128 x 128 block), [N, K/128] with b_rows 1 (for each row of b)
  *   y   device [M, N] dtype (BEAM_F32 or BEAM_BF16)
- * K % 128 == 0, K <= 2^22, M, N < 2^23 - 127 (BEAM_ERR_UNSUPPORTED otherwise).
+ * K % 128 == 0, K <= 2^22, M, N < 2^23 - 127, M * N <= 2^38
+ * (BEAM_ERR_UNSUPPORTED otherwise).
  * K == 0 gives zeros.  NaN codes (0x7F, 0xFF) are outside the contract.
  * A linear layer's training step is three of them on what
  * beam_moe_quant_e4m3_2d makes of x [M,K], dy [M,N] and w [N,K]:

@@ -139,6 +139,15 @@ def test_offsets_past_32_bits():
     assert (y[-1000:-3] == 0).all()
 
 
+def test_tall_and_narrow():
+    # more row tiles than a grid's second dimension holds
+    dev = device()
+    for M, N in ((3000001, 1), (1, 3000001)):
+        a, sa = operand(M, 128, 1, 1, dev)
+        b, sb = operand(N, 128, 128, 2, dev)
+        check(gl.matmul_e4m3(a, sa, b, sb), a, sa, b, sb, False)
+
+
 def test_captured_and_on_another_stream():
     dev = device()
     for M in (1, 64, 600):

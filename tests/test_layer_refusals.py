@@ -122,7 +122,7 @@ def _mm(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(M=-1), gl.ERR_INVALID_ARG), (dict(N=-1), gl.ERR_INVALID_ARG), (dict(K=-128), gl.ERR_INVALID_ARG),
     (dict(K=100), gl.ERR_UNSUPPORTED), (dict(K=1 << 23), gl.ERR_UNSUPPORTED), (dict(M=1 << 23), gl.ERR_UNSUPPORTED),
-    (dict(N=1 << 40), gl.ERR_UNSUPPORTED), (dict(rows=2), gl.ERR_INVALID_ARG),
+    (dict(N=1 << 40), gl.ERR_UNSUPPORTED), (dict(M=1 << 22, N=1 << 17), gl.ERR_UNSUPPORTED), (dict(rows=2), gl.ERR_INVALID_ARG),
     (dict(dtype=gl.FP8_E4M3), gl.ERR_INVALID_ARG), (dict(a=None), gl.ERR_INVALID_ARG),
     (dict(sa=None), gl.ERR_INVALID_ARG), (dict(b=None), gl.ERR_INVALID_ARG), (dict(sb=None), gl.ERR_INVALID_ARG),
     (dict(y=None), gl.ERR_INVALID_ARG), (dict(a=BAD), gl.ERR_INVALID_ARG), (dict(sb=BAD), gl.ERR_INVALID_ARG),
