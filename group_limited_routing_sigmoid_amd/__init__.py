@@ -167,7 +167,11 @@ def _torch_stream(stream, device):
 
 
 def _stream(stream=None, device=None):
-    return ctypes.c_void_p(_torch_stream(stream, device).cuda_stream)
+    if stream is None:  # the current stream's handle without a Stream object
+        i = device.index if device is not None else None
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(
+            torch.cuda.current_device() if i is None else i))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 class Workspace:
@@ -223,42 +227,51 @@ def _alloc_on(stream):
     return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
-def _arg(name: str, t: torch.Tensor, shape, *dtypes) -> int:
-    """Address of a contiguous GPU tensor of the given shape and one of the
-    given dtypes; raises ValueError otherwise."""
+def _arg(name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple) -> int:
+    """Address of a contiguous tensor on GPU `dev` of the given dtype and
+    shape; raises ValueError otherwise."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name}: tensors passed to the HIP library must be on the GPU")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected "
-                         + " or ".join(str(d) for d in dtypes))
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: tensors passed to the HIP library must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, the other tensors on cuda:{dev}")
+    raise ValueError(f"{name}: tensors passed to the HIP library must be contiguous")
 
 
-def _run(fn, what: str, stream, tensors, *args):
-    """Call a library entry point whose last argument is the stream, on the
-    device its tensors live on.  Inputs read on a stream that is not the
-    current one are marked as used there, so torch's allocator keeps their
-    memory until the kernels are done."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError(f"{what}: tensors on cuda:{dev} and cuda:{t.get_device()}")
+def _empty(stream, device, dtype: torch.dtype, *shape) -> torch.Tensor:
+    """An output, allocated on the call's stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _run(fn, what: str, stream, dev: int, tensors, *args):
+    """Call a library entry point whose last argument is the stream on GPU
+    `dev`, whichever is current.  Tensors read or written on a stream that is
+    not the current one are marked as used there, so torch's allocator keeps
+    their memory until the kernels are done."""
     raw = torch._C._cuda_getCurrentRawStream(dev)
     if stream is not None and stream.cuda_stream != raw:
         if stream.device.index != dev:
             raise ValueError(f"{what}: a stream of {stream.device} for tensors on cuda:{dev}")
         raw = stream.cuda_stream
         for t in tensors:
-            t.record_stream(stream)
-    if dev == torch._C._cuda_getDevice():
-        _check(fn(*args, raw), what)
+            if t is not None:
+                t.record_stream(stream)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, raw), what)
+            status = fn(*args, raw)
+    if status != OK:
+        raise BeamError(status, what)
 
 
 def route(desc: Desc, x: Optional[torch.Tensor], w_router: Optional[torch.Tensor],
@@ -271,11 +284,10 @@ def route(desc: Desc, x: Optional[torch.Tensor], w_router: Optional[torch.Tensor
     lin = bool(desc.flags & ROUTE_LOGITS_IN)
     ref = logits if lin else x
     T, dev = ref.shape[0], ref.device
-    with _alloc_on(stream):
-        idx = torch.empty(T, desc.top_k, dtype=torch.int32, device=dev)
-        w = torch.empty(T, desc.top_k, dtype=torch.float32, device=dev)
-        if logits is None:
-            logits = torch.empty(T, desc.n_experts, dtype=torch.float32, device=dev)
+    idx = _empty(stream, dev, torch.int32, T, desc.top_k)
+    w = _empty(stream, dev, torch.float32, T, desc.top_k)
+    if logits is None:
+        logits = _empty(stream, dev, torch.float32, T, desc.n_experts)
     # routing from given logits uses no scratch memory
     buf, n = (None, 0) if lin else _ws(desc, T, workspace, dev, stream)
     _check(lib().beam_moe_route(ctypes.byref(desc), T, _p(x), _p(w_router),
@@ -289,16 +301,15 @@ def route_backward(desc: Desc, logits: torch.Tensor, topk_idx: torch.Tensor,
                    stream=None) -> torch.Tensor:
     """beam_moe_route_backward: the gradient [T,E] fp32 of the logits from that
     of the routing weights (the selection and the bias are constants)."""
-    T, E, K = logits.shape[0], desc.n_experts, desc.top_k
+    T, E, K, dev = logits.shape[0], desc.n_experts, desc.top_k, logits.get_device()
+    pl = _arg("logits", logits, dev, torch.float32, (T, E))
+    pi = _arg("topk_idx", topk_idx, dev, torch.int32, (T, K))
+    pw = _arg("d_topk_w", d_topk_w, dev, torch.float32, (T, K))
     if out is None:
-        with _alloc_on(stream):
-            out = torch.empty(T, E, dtype=torch.float32, device=logits.device)
-    _run(lib().beam_moe_route_backward, "beam_moe_route_backward", stream,
-         (logits, topk_idx, d_topk_w, out), ctypes.byref(desc), T,
-         _arg("logits", logits, (T, E), torch.float32),
-         _arg("topk_idx", topk_idx, (T, K), torch.int32),
-         _arg("d_topk_w", d_topk_w, (T, K), torch.float32),
-         _arg("out", out, (T, E), torch.float32))
+        out = _empty(stream, logits.device, torch.float32, T, E)
+    _run(lib().beam_moe_route_backward, "beam_moe_route_backward", stream, dev,
+         (logits, topk_idx, d_topk_w, out), ctypes.byref(desc), T, pl, pi, pw,
+         _arg("out", out, dev, torch.float32, (T, E)))
     return out
 
 
@@ -395,21 +406,22 @@ def quant_e4m3_2d(v: torch.Tensor, block: bool = False, straight: bool = True,
     None for an orientation that is not asked for."""
     if v.dim() != 2:
         raise ValueError(f"v: shape {tuple(v.shape)}, expected [rows, cols]")
+    if v.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"v: dtype {v.dtype}, expected torch.bfloat16 or torch.float32")
     rows, cols = v.shape
-    pv = _arg("v", v, (rows, cols), torch.bfloat16, torch.float32)
-    nr, nc, dev = (rows + 127) // 128, (cols + 127) // 128, v.device
+    dev, device = v.get_device(), v.device
+    pv = _arg("v", v, dev, v.dtype, (rows, cols))
+    nr, nc = (rows + 127) // 128, (cols + 127) // 128
     q = s = qt = st = None
-    with _alloc_on(stream):
-        if straight:
-            q = torch.empty(rows, nc * 128, dtype=torch.uint8, device=dev)
-            s = torch.empty(nr if block else rows, nc, dtype=torch.float32, device=dev)
-        if transposed:
-            qt = torch.empty(cols, nr * 128, dtype=torch.uint8, device=dev)
-            st = torch.empty(nc if block else cols, nr, dtype=torch.float32, device=dev)
-    _run(lib().beam_moe_quant_e4m3_2d, "beam_moe_quant_e4m3_2d", stream, (v,), rows, cols,
-         BF16 if v.dtype == torch.bfloat16 else F32, 1 if block else 0, pv,
-         None if q is None else q.data_ptr(), None if s is None else s.data_ptr(),
-         None if qt is None else qt.data_ptr(), None if st is None else st.data_ptr())
+    if straight:
+        q = _empty(stream, device, torch.uint8, rows, nc * 128)
+        s = _empty(stream, device, torch.float32, nr if block else rows, nc)
+    if transposed:
+        qt = _empty(stream, device, torch.uint8, cols, nr * 128)
+        st = _empty(stream, device, torch.float32, nc if block else cols, nr)
+    _run(lib().beam_moe_quant_e4m3_2d, "beam_moe_quant_e4m3_2d", stream, dev, (v, q, s, qt, st),
+         rows, cols, BF16 if v.dtype is torch.bfloat16 else F32, 1 if block else 0, pv,
+         *(None if t is None else t.data_ptr() for t in (q, s, qt, st)))
     return q, s, qt, st
 
 
@@ -427,15 +439,15 @@ def matmul_e4m3(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch.
     if K % 128:
         raise ValueError(f"K = {K} is not a multiple of 128")
     rows = s_b.dim() == 2 and s_b.shape[0] == N
-    pa, pb = _arg("a", a, (M, K), torch.uint8), _arg("b", b, (N, K), torch.uint8)
-    psa = _arg("s_a", s_a, (M, K // 128), torch.float32)
-    psb = _arg("s_b", s_b, (N if rows else (N + 127) // 128, K // 128), torch.float32)
+    dev = a.get_device()
+    pa, pb = _arg("a", a, dev, torch.uint8, (M, K)), _arg("b", b, dev, torch.uint8, (N, K))
+    psa = _arg("s_a", s_a, dev, torch.float32, (M, K // 128))
+    psb = _arg("s_b", s_b, dev, torch.float32, (N if rows else (N + 127) // 128, K // 128))
     if out is None:
-        with _alloc_on(stream):
-            out = torch.empty(M, N, dtype=dtype, device=a.device)
-    _run(lib().beam_moe_matmul_e4m3, "beam_moe_matmul_e4m3", stream, (a, s_a, b, s_b, out), M, N, K,
-         pa, psa, pb, psb, 1 if rows else 0, BF16 if dtype == torch.bfloat16 else F32,
-         _arg("out", out, (M, N), dtype))
+        out = _empty(stream, a.device, dtype, M, N)
+    _run(lib().beam_moe_matmul_e4m3, "beam_moe_matmul_e4m3", stream, dev, (a, s_a, b, s_b, out),
+         M, N, K, pa, psa, pb, psb, 1 if rows else 0, BF16 if dtype is torch.bfloat16 else F32,
+         _arg("out", out, dev, dtype, (M, N)))
     return out
 
 
@@ -448,62 +460,62 @@ def residual_scale(step: int):
 
 
 def _norm_inputs(residual, o, post_weight, gate, pre_weight, dtype):
-    """Checked addresses of a step's inputs: (T, H, dtype code, dtype, o,
-    post_weight, gate, gate_cols, pre_weight, tensors)."""
+    """Checked arguments of a step: (T, H, device index, dtype, addresses of o,
+    post_weight and gate, gate_cols, address of pre_weight)."""
     if residual.dim() != 2:
         raise ValueError(f"residual: shape {tuple(residual.shape)}, expected [T, H]")
     T, H = residual.shape
-    if o is not None:
-        if dtype is not None and dtype != o.dtype:
+    dev = residual.get_device()
+    if o is None:
+        if post_weight is not None or gate is not None:
+            raise ValueError("post_weight and gate belong to o")
+        if dtype is None:
+            dtype = torch.bfloat16
+    else:
+        if dtype is not None and dtype is not o.dtype:
             raise ValueError(f"dtype {dtype} with o in {o.dtype}: o, gate and x share one dtype")
         dtype = o.dtype
-    elif post_weight is not None or gate is not None:
-        raise ValueError("post_weight and gate belong to o")
-    elif dtype is None:
-        dtype = torch.bfloat16
-    if dtype not in (torch.bfloat16, torch.float32):
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError(f"dtype {dtype}, expected torch.bfloat16 or torch.float32")
-    ptr, tensors = [None, None, None, None], [residual]
+    po = pw = pg = pp = None
     cols = 0
     if o is not None:
         if post_weight is None:
             raise ValueError("o needs its post_weight")
-        ptr[0] = _arg("o", o, (T, H), dtype)
-        ptr[1] = _arg("post_weight", post_weight, (H,), torch.float32)
-        tensors += [o, post_weight]
+        po = _arg("o", o, dev, dtype, (T, H))
+        pw = _arg("post_weight", post_weight, dev, torch.float32, (H,))
         if gate is not None:
             cols = H if gate.dim() == 2 and gate.shape[1] == H else 1
-            ptr[2] = _arg("gate", gate, (T, cols), dtype)
-            tensors.append(gate)
+            pg = _arg("gate", gate, dev, dtype, (T, cols))
     if pre_weight is not None:
-        ptr[3] = _arg("pre_weight", pre_weight, (H,), torch.float32)
-        tensors.append(pre_weight)
-    return (T, H, BF16 if dtype == torch.bfloat16 else F32, dtype, ptr[0], ptr[1], ptr[2], cols,
-            ptr[3], tensors)
+        pp = _arg("pre_weight", pre_weight, dev, torch.float32, (H,))
+    return T, H, dev, dtype, po, pw, pg, cols, pp
 
 
 def _norm_residual(residual, o, post_weight, gate, pre_weight, eps, alpha, beta, dtype,
                    residual_out, want_x, codes, stream):
-    T, H, code, dtype, po, pw, pg, cols, pp, tensors = _norm_inputs(
+    T, H, dev, dtype, po, pw, pg, cols, pp = _norm_inputs(
         residual, o, post_weight, gate, pre_weight, dtype)
-    pr = _arg("residual", residual, (T, H), torch.float32)
-    x = q = s = None
-    with _alloc_on(stream):
-        if o is None:
-            residual_out, p_out = residual, None
-        else:
-            if residual_out is None:
-                residual_out = torch.empty_like(residual)
-            p_out = _arg("residual_out", residual_out, (T, H), torch.float32)
-            tensors.append(residual_out)
-        if pre_weight is not None and want_x:
-            x = torch.empty(T, H, dtype=dtype, device=residual.device)
-        if codes:
-            q = torch.empty(T, H, dtype=torch.uint8, device=residual.device)
-            s = torch.empty(T, H // 128, dtype=torch.float32, device=residual.device)
-    _run(lib().beam_moe_norm_residual, "beam_moe_norm_residual", stream, tensors, T, H, code, po, pw,
-         pg, cols, pp, eps, alpha, beta, pr, p_out, None if x is None else x.data_ptr(),
-         None if q is None else q.data_ptr(), None if s is None else s.data_ptr())
+    pr = _arg("residual", residual, dev, torch.float32, (T, H))
+    device = residual.device
+    x = q = s = p_out = px = pq = ps = None
+    if o is None:
+        residual_out = residual
+    else:
+        if residual_out is None:
+            residual_out = _empty(stream, device, torch.float32, T, H)
+        p_out = _arg("residual_out", residual_out, dev, torch.float32, (T, H))
+    if pp is not None and want_x:
+        x = _empty(stream, device, dtype, T, H)
+        px = x.data_ptr()
+    if codes:
+        q = _empty(stream, device, torch.uint8, T, H)
+        s = _empty(stream, device, torch.float32, T, H // 128)
+        pq, ps = q.data_ptr(), s.data_ptr()
+    _run(lib().beam_moe_norm_residual, "beam_moe_norm_residual", stream, dev,
+         (residual, o, post_weight, gate, pre_weight, residual_out, x, q, s), T, H,
+         BF16 if dtype is torch.bfloat16 else F32, po, pw, pg, cols, pp, eps, alpha, beta, pr, p_out,
+         px, pq, ps)
     return residual_out, x, q, s
 
 
@@ -553,41 +565,35 @@ def norm_residual_backward(residual_out: torch.Tensor,
     residual without o); d_residual_out and d_x are the gradients of r' and x
     (None for zero, not both).  Returns a dict: d_residual [T,H] fp32; with o
     d_o and d_post_weight, with gate d_gate, with d_x d_pre_weight."""
-    T, H, code, dtype, po, pw, pg, cols, pp, tensors = _norm_inputs(
+    T, H, dev, dtype, po, pw, pg, cols, pp = _norm_inputs(
         residual_out, o, post_weight, gate, pre_weight,
         d_x.dtype if o is None and d_x is not None else None)
     if d_residual_out is None and d_x is None:
         raise ValueError("one of d_residual_out and d_x is needed")
     if d_x is not None and pre_weight is None:
         raise ValueError("d_x needs the pre_weight")
-    dev = residual_out.device
-    pr = _arg("residual_out", residual_out, (T, H), torch.float32)
-    p_dr = p_dx = None
-    if d_residual_out is not None:
-        p_dr = _arg("d_residual_out", d_residual_out, (T, H), torch.float32)
-        tensors.append(d_residual_out)
-    if d_x is not None:
-        p_dx = _arg("d_x", d_x, (T, H), dtype)
-        tensors.append(d_x)
+    device, f32 = residual_out.device, torch.float32
+    pr = _arg("residual_out", residual_out, dev, f32, (T, H))
+    p_dr = None if d_residual_out is None else _arg("d_residual_out", d_residual_out, dev, f32, (T, H))
+    p_dx = None if d_x is None else _arg("d_x", d_x, dev, dtype, (T, H))
     need = ctypes.c_size_t(0)
     _check(lib().beam_moe_norm_residual_workspace_bytes(T, H, ctypes.byref(need)),
            "beam_moe_norm_residual_workspace_bytes")
-    out = {}
-    with _alloc_on(stream):
-        out["d_residual"] = torch.empty(T, H, dtype=torch.float32, device=dev)
-        if o is not None:
-            out["d_o"] = torch.empty_like(o)
-            out["d_post_weight"] = torch.empty(H, dtype=torch.float32, device=dev)
-            if gate is not None:
-                out["d_gate"] = torch.empty_like(gate)
-        if d_x is not None:
-            out["d_pre_weight"] = torch.empty(H, dtype=torch.float32, device=dev)
-    buf = _scratch(need.value, workspace, dev, stream)
+    out = {"d_residual": _empty(stream, device, f32, T, H)}
+    if o is not None:
+        out["d_o"] = _empty(stream, device, dtype, T, H)
+        out["d_post_weight"] = _empty(stream, device, f32, H)
+        if gate is not None:
+            out["d_gate"] = _empty(stream, device, dtype, T, cols)
+    if d_x is not None:
+        out["d_pre_weight"] = _empty(stream, device, f32, H)
+    buf = _scratch(need.value, workspace, device, stream)
     ptr = {k: v.data_ptr() for k, v in out.items()}
-    _run(lib().beam_moe_norm_residual_backward, "beam_moe_norm_residual_backward", stream, tensors,
-         T, H, code, po, pw, pg, cols, pp, eps, alpha, beta, pr, p_dr, p_dx, ptr["d_residual"],
-         ptr.get("d_o"), ptr.get("d_gate"), ptr.get("d_pre_weight"), ptr.get("d_post_weight"),
-         None if buf is None else buf.data_ptr(), need.value)
+    _run(lib().beam_moe_norm_residual_backward, "beam_moe_norm_residual_backward", stream, dev,
+         (residual_out, d_residual_out, d_x, o, post_weight, gate, pre_weight, *out.values()),
+         T, H, BF16 if dtype is torch.bfloat16 else F32, po, pw, pg, cols, pp, eps, alpha, beta, pr,
+         p_dr, p_dx, ptr["d_residual"], ptr.get("d_o"), ptr.get("d_gate"), ptr.get("d_pre_weight"),
+         ptr.get("d_post_weight"), None if buf is None else buf.data_ptr(), need.value)
     return out
 
 

@@ -25,6 +25,8 @@
 //                    reproducible from the fp32 logits.
 //
 // This translation unit is compiled with -ffp-contract=off.
+#include <type_traits>
+
 #include "common.h"
 #include "internal.h"
 
@@ -197,9 +199,79 @@ __device__ __forceinline__ float sigmoid32(float l) {
   return static_cast<float>(q);
 }
 
+// Order-preserving map of a finite binary32 to uint32 (larger float, larger
+// key); +0 and -0 map to the same key after canonicalisation.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+constexpr int kSelWaves = 4;
+constexpr int kMaxE = 1024;
+constexpr int kMaxKs = 16;   // the plan splits the router's reduction at most 16 ways
+constexpr int kMaxG = 64;
+
+// ---- wave-wide helpers --------------------------------------------------
+// Reductions over the wave in data-parallel moves: swap neighbours, swap
+// pairs (quad permutations), mirror the half rows, mirror the row; every lane
+// then holds its row of 16's result, and the rows meet in the last lane or
+// are read out lane by lane.  All need every lane active.
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, false));
+}
+
+// Maximum over the wave, returned uniform.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max(v, dpp<0xB1>(v));   // quad_perm(1, 0, 3, 2)
+  v = max(v, dpp<0x4E>(v));   // quad_perm(2, 3, 0, 1)
+  v = max(v, dpp<0x141>(v));  // row_half_mirror
+  v = max(v, dpp<0x140>(v));  // row_mirror
+  v = max(v, dpp<0x142>(v));  // row_bcast:15, the row before's
+  v = max(v, dpp<0x143>(v));  // row_bcast:31, the first two rows'
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+
+__device__ __forceinline__ float readlane_f(float v, int l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+
+__device__ __forceinline__ float wave_max_f32(float v) {
+  auto step = [&](uint32_t o) { v = fmaxf(v, __uint_as_float(o)); };
+  step(dpp<0xB1>(__float_as_uint(v)));
+  step(dpp<0x4E>(__float_as_uint(v)));
+  step(dpp<0x141>(__float_as_uint(v)));
+  step(dpp<0x140>(__float_as_uint(v)));
+  return fmaxf(fmaxf(readlane_f(v, 0), readlane_f(v, 16)),
+               fmaxf(readlane_f(v, 32), readlane_f(v, 48)));
+}
+
+__device__ __forceinline__ double wave_sum_f64(double v) {
+  auto move = [&](auto ctrl) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = dpp<decltype(ctrl)::value>(static_cast<uint32_t>(b));
+    const uint64_t hi = dpp<decltype(ctrl)::value>(static_cast<uint32_t>(b >> 32));
+    v += __builtin_bit_cast(double, lo | (hi << 32));
+  };
+  move(std::integral_constant<int, 0xB1>{});
+  move(std::integral_constant<int, 0x4E>{});
+  move(std::integral_constant<int, 0x141>{});
+  move(std::integral_constant<int, 0x140>{});
+  auto row = [&](int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), l);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), l);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32));
+  };
+  return (row(0) + row(16)) + (row(32) + row(48));
+}
+
 // Softmax scores of a token, one wave: s_e = e^(l_e - m) / sum_j e^(l_j - m)
-// with m the largest logit, the exponentials, their sum and the quotient in
-// binary64, rounded once to binary32 (the selection compares these values,
+// with m the largest logit, the exponentials, their sum and its reciprocal
+// (one division a token: by itself a third of the scores' time) in binary64,
+// rounded once to binary32 (the selection compares these values,
 // so they are held to the rounding of the exact softmax, as the sigmoids
 // are).  Exponents below -105 give 0: such a score is below half the smallest
 // binary32 value, and 1024 of them are below the sum's last bit.  A row
@@ -211,8 +283,7 @@ __device__ __forceinline__ void softmax32(const float (&l)[EPL], int lane, int E
 #pragma unroll
   for (int j = 0; j < EPL; ++j)
     if (lane * EPL + j < E) m = fmaxf(m, l[j]);
-#pragma unroll
-  for (int off = kWave / 2; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+  m = wave_max_f32(m);
   double ez[EPL], sum = 0.0;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
@@ -220,60 +291,10 @@ __device__ __forceinline__ void softmax32(const float (&l)[EPL], int lane, int E
     ez[j] = (lane * EPL + j < E && z > -105.0) ? exp64(z) : 0.0;
     sum += ez[j];
   }
+  sum = wave_sum_f64(sum);
+  const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
 #pragma unroll
-  for (int off = kWave / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) s[j] = sum > 0.0 ? static_cast<float>(ez[j] / sum) : 0.0f;
-}
-
-// Order-preserving map of a finite binary32 to uint32 (larger float, larger
-// key); +0 and -0 map to the same key after canonicalisation.
-__device__ __forceinline__ uint32_t ordered(float v) {
-  const uint32_t b = __float_as_uint(v + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-
-// Rank key: larger value first, then lower expert id.  0 means "not a
-// candidate" and is below every real key.
-__device__ __forceinline__ uint64_t rank_key(float u, int e) {
-  return (static_cast<uint64_t>(ordered(u)) << 32) |
-         static_cast<uint64_t>(0xFFFFFFFFu - static_cast<uint32_t>(e));
-}
-
-constexpr int kSelWaves = 4;
-constexpr int kMaxE = 1024;
-constexpr int kMaxKs = 16;   // the plan splits the router's reduction at most 16 ways
-constexpr int kMaxG = 64;
-
-// ---- wave-wide helpers for the selection --------------------------------
-
-// 64-bit DPP move (both halves with the same lane pattern)
-template <int CTRL>
-__device__ __forceinline__ uint64_t dpp64(uint64_t v) {
-  const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, false);
-  const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), CTRL, 0xF, 0xF, false);
-  return (static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32) | static_cast<uint32_t>(lo);
-}
-
-__device__ __forceinline__ uint64_t readlane64(uint64_t v, int l) {
-  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), l);
-  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), l);
-  return (static_cast<uint64_t>(hi) << 32) | lo;
-}
-
-__device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
-
-// Maximum over the wave, returned uniform.  Within each row of 16 lanes:
-// swap neighbours, swap pairs (quad permutations), mirror the half rows,
-// mirror the row; every lane then holds its row's maximum, and the four
-// rows' maxima are read out lane by lane.  Needs every lane active.
-__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
-  v = max64(v, dpp64<0xB1>(v));   // quad_perm(1, 0, 3, 2)
-  v = max64(v, dpp64<0x4E>(v));   // quad_perm(2, 3, 0, 1)
-  v = max64(v, dpp64<0x141>(v));  // row_half_mirror
-  v = max64(v, dpp64<0x140>(v));  // row_mirror
-  return max64(max64(readlane64(v, 0), readlane64(v, 16)),
-               max64(readlane64(v, 32), readlane64(v, 48)));
+  for (int j = 0; j < EPL; ++j) s[j] = static_cast<float>(ez[j] * inv);
 }
 
 // grid ceil(T/4), block 256: wave w routes token 4*blockIdx.x + w, holding
@@ -391,42 +412,49 @@ __global__ __launch_bounds__(256) void router_select(
   // 3. keep the TG best groups (ties: lower group id): bit g of `keep`
   int rank = 0;
   for (int g = 0; g < G; ++g) {
-    const float o = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, gsc), g));
+    const float o = readlane_f(gsc, g);
     rank += (o > gsc) || (o == gsc && g < lane);
   }
   const uint64_t keep = __ballot(lane < G && rank < TG);
 
-  // 4. top-K of the eligible experts by biased score, rank order
-  uint64_t key[EPL];
+  // 4. top-K of the eligible experts by biased score, rank order: the largest
+  // key (0: not a candidate) over the wave, then the lowest lane holding it
+  // and the lowest of its experts, as lanes hold consecutive experts.
+  // (On 64-bit keys of score and index every step of the maximum took six
+  // instructions for one: 96 us for 52,001 tokens of 256 experts.)
+  uint32_t key[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = lane * EPL + j;
-    key[j] = (e < E && ((keep >> (e / gs)) & 1)) ? rank_key(u[j], e) : 0;
+    key[j] = (e < E && ((keep >> (e / gs)) & 1)) ? ordered(u[j]) : 0;
   }
-  float D = 0.0f, my_s = 0.0f;
   int my_e = 0;
   for (int k = 0; k < K; ++k) {
-    uint64_t best = 0;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) best = max64(best, key[j]);
-    best = wave_max64(best);
-    // K <= TG*E/G eligible experts always remain, so best != 0; the clamp
-    // only keeps the lane index below in range.
-    int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
-    e = e < 0 ? 0 : (e >= E ? E - 1 : e);
-    float se = sv[0];
+    for (int j = 1; j < EPL; ++j) best = max(best, key[j]);
+    const uint32_t top = wave_max_u32(best);
+    const int owner = __builtin_ctzll(__ballot(best == top));
+    int at = 0;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      if (lane * EPL + j == e) key[j] = 0;
-      if (j == e % EPL) se = sv[j];
-    }
-    const float sk = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, se), e / EPL));
-    D = (k == 0) ? sk : D + sk;
-    if (lane == k) {
-      my_e = e;
-      my_s = sk;
-    }
+    for (int j = EPL - 1; j >= 0; --j) at = key[j] == top ? j : at;
+    at = lane == owner ? at : -1;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = at == j ? 0 : key[j];
+    // K <= TG*E/G eligible experts always remain, so top != 0; the clamp
+    // only keeps the index in range.
+    const int e = min(owner * EPL + __builtin_amdgcn_readlane(at, owner), E - 1);
+    my_e = lane == k ? e : my_e;
   }
+  // the chosen scores and, in rank order, their sum
+  float my_s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const float v = __shfl(sv[j], my_e / EPL);
+    my_s = my_e % EPL == j ? v : my_s;
+  }
+  float D = readlane_f(my_s, 0);
+  for (int k = 1; k < K; ++k) D = D + readlane_f(my_s, k);
   // 5. weights: (s / D) * scale, two binary32 roundings (0 where every chosen
   // score is 0), or s * scale
   if (lane < K) {
@@ -501,8 +529,7 @@ __global__ __launch_bounds__(256) void route_backward(
       if (lane * EPL + j >= E) p[j] = -__builtin_huge_valf();
       m = fmaxf(m, p[j]);
     }
-#pragma unroll
-    for (int off = kWave / 2; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+    m = wave_max_f32(m);
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
