@@ -287,8 +287,10 @@ __device__ __forceinline__ void softmax32(const float (&l)[EPL], int lane, int E
   double ez[EPL], sum = 0.0;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
+    // no branch, so that the exponentials of a lane overlap
     const double z = static_cast<double>(l[j]) - static_cast<double>(m);
-    ez[j] = (lane * EPL + j < E && z > -105.0) ? exp64(z) : 0.0;
+    const double v = exp64(__builtin_fmax(z, -105.0));
+    ez[j] = (lane * EPL + j < E && z > -105.0) ? v : 0.0;
     sum += ez[j];
   }
   sum = wave_sum_f64(sum);
@@ -300,8 +302,8 @@ __device__ __forceinline__ void softmax32(const float (&l)[EPL], int lane, int E
 // grid ceil(T/4), block 256: wave w routes token 4*blockIdx.x + w, holding
 // EPL experts per lane in registers (lane l: experts l*EPL .. l*EPL+EPL-1).
 // KS is 1 (one partial per logit) or kMaxKs (ks <= kMaxKs partials).  SEG:
-// a group's experts are the L = gs/EPL lanes of one aligned power-of-two
-// segment, so group maxima are butterflies within the segment; otherwise
+// a group's experts are the 2^lg = gs/EPL lanes of one aligned segment, so
+// group maxima are butterflies within the segment; otherwise
 // lane g scans group g's biased scores from LDS (one pad word per 32 keeps
 // the scan's lanes on distinct banks).  SM: softmax scores.
 __device__ __forceinline__ int upad(int e) { return e + (e >> 5); }
@@ -309,7 +311,7 @@ __device__ __forceinline__ int upad(int e) { return e + (e >> 5); }
 template <int EPL, int KS, bool SEG, bool SM>
 __global__ __launch_bounds__(256) void router_select(
     const float* __restrict__ part, int ks, int vec4, int64_t T, int E, int G,
-    int TG, int K, int topn, int normed, float scale, const float* __restrict__ bias,
+    int TG, int K, int topn, int lg, int normed, float scale, const float* __restrict__ bias,
     float* __restrict__ logits_out, int32_t* __restrict__ idx_out,
     float* __restrict__ w_out) {
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
@@ -346,7 +348,20 @@ __global__ __launch_bounds__(256) void router_select(
     }
   }
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) bz[j] = bias ? bias[min(lane * EPL + j, E - 1)] : 0.0f;
+  for (int j = 0; j < EPL; ++j) bz[j] = 0.0f;
+  if (bias) {
+    if (EPL % 4 == 0 && vec4) {
+#pragma unroll
+      for (int j = 0; j < EPL; j += 4) {
+        const u32x4 v = ld16(bias + min(lane * EPL + j, E - 4));
+#pragma unroll
+        for (int q = 0; q < 4 && j + q < EPL; ++q) bz[j + q] = __uint_as_float(v[q]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) bz[j] = bias[min(lane * EPL + j, E - 1)];
+    }
+  }
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = lane * EPL + j;
@@ -363,9 +378,12 @@ __global__ __launch_bounds__(256) void router_select(
   for (int j = 0; j < EPL; ++j) u[j] = lane * EPL + j < E ? sv[j] + bz[j] : ninf;
 
   // 2. group scores: sum of the topn (1 or 2) largest biased scores (a
-  // repeated value counts twice).  gsc ends in lane g for group g.
+  // repeated value counts twice).  gsc ends in lane g for group g.  Not
+  // needed where every group is kept.
   float gsc = ninf;
-  if constexpr (SEG) {
+  uint64_t keep = ~uint64_t{0};
+  const bool limited = TG < G;
+  if (SEG && limited) {
     float t1 = ninf, t2 = ninf;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
@@ -376,16 +394,23 @@ __global__ __launch_bounds__(256) void router_select(
         t2 = u[j];
       }
     }
-    const int L = gs / EPL;
-    for (int off = 1; off < L; off <<= 1) {
-      const float o1 = __shfl_xor(t1, off), o2 = __shfl_xor(t2, off);
+    auto meet = [&](float o1, float o2) {
       const float n2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
       t1 = fmaxf(t1, o1);
       t2 = n2;
-    }
+    };
+    auto move = [&](auto ctrl) {
+      constexpr int c = decltype(ctrl)::value;
+      meet(__uint_as_float(dpp<c>(__float_as_uint(t1))), __uint_as_float(dpp<c>(__float_as_uint(t2))));
+    };
+    if (lg > 0) move(std::integral_constant<int, 0xB1>{});
+    if (lg > 1) move(std::integral_constant<int, 0x4E>{});
+    if (lg > 2) move(std::integral_constant<int, 0x141>{});
+    if (lg > 3) move(std::integral_constant<int, 0x140>{});
+    for (int off = 16; off < (1 << lg); off <<= 1) meet(__shfl_xor(t1, off), __shfl_xor(t2, off));
     const float mine = (topn == 1) ? t1 : t1 + t2;
-    gsc = __shfl(mine, min(lane, G - 1) * L);
-  } else {
+    gsc = __shfl(mine, min(lane, G - 1) << lg);
+  } else if (limited) {
     __shared__ float u_sh[kSelWaves][kMaxE + kMaxE / 32];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
@@ -410,12 +435,14 @@ __global__ __launch_bounds__(256) void router_select(
   if (!valid) return;
 
   // 3. keep the TG best groups (ties: lower group id): bit g of `keep`
-  int rank = 0;
-  for (int g = 0; g < G; ++g) {
-    const float o = readlane_f(gsc, g);
-    rank += (o > gsc) || (o == gsc && g < lane);
+  if (limited) {
+    int rank = 0;
+    for (int g = 0; g < G; ++g) {
+      const float o = readlane_f(gsc, g);
+      rank += (o > gsc) || (o == gsc && g < lane);
+    }
+    keep = __ballot(lane < G && rank < TG);
   }
-  const uint64_t keep = __ballot(lane < G && rank < TG);
 
   // 4. top-K of the eligible experts by biased score, rank order: the largest
   // key (0: not a candidate) over the wave, then the lowest lane holding it
@@ -426,21 +453,54 @@ __global__ __launch_bounds__(256) void router_select(
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = lane * EPL + j;
-    key[j] = (e < E && ((keep >> (e / gs)) & 1)) ? ordered(u[j]) : 0;
+    const int g = SEG ? lane >> lg : e / gs;
+    key[j] = (e < E && ((keep >> g) & 1)) ? ordered(u[j]) : 0;
+  }
+  // Up to four experts a lane are first sorted (larger key first, then lower
+  // index: stable), so that a choice only looks at and shifts the heads.
+  constexpr bool kSorted = EPL <= 4;
+  uint32_t order = 0x03020100u;  // byte i: which expert of the lane is i-th
+  if constexpr (kSorted && EPL > 1) {
+    auto swap = [&](int a, int b) {  // a < b: keeps equal keys in place
+      const bool s = key[b] > key[a];
+      const uint32_t lo = s ? key[a] : key[b];
+      key[a] = s ? key[b] : key[a];
+      key[b] = lo;
+      const uint32_t pa = (order >> (8 * a)) & 0xFF, pb = (order >> (8 * b)) & 0xFF;
+      const uint32_t x = s ? pa ^ pb : 0;
+      order ^= (x << (8 * a)) | (x << (8 * b));
+    };
+    // neighbours only, so that the sort is stable
+    if constexpr (EPL == 2) {
+      swap(0, 1);
+    } else {
+      swap(0, 1), swap(2, 3), swap(1, 2), swap(0, 1), swap(2, 3), swap(1, 2);
+    }
   }
   int my_e = 0;
   for (int k = 0; k < K; ++k) {
     uint32_t best = key[0];
+    if constexpr (!kSorted) {
 #pragma unroll
-    for (int j = 1; j < EPL; ++j) best = max(best, key[j]);
+      for (int j = 1; j < EPL; ++j) best = max(best, key[j]);
+    }
     const uint32_t top = wave_max_u32(best);
     const int owner = __builtin_ctzll(__ballot(best == top));
-    int at = 0;
+    int at;
+    if constexpr (kSorted) {
+      at = order & 0xFF;
+      const bool mine = lane == owner;
 #pragma unroll
-    for (int j = EPL - 1; j >= 0; --j) at = key[j] == top ? j : at;
-    at = lane == owner ? at : -1;
+      for (int j = 0; j < EPL; ++j) key[j] = mine ? (j + 1 < EPL ? key[j + 1] : 0) : key[j];
+      order = mine ? order >> 8 : order;
+    } else {
+      at = 0;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) key[j] = at == j ? 0 : key[j];
+      for (int j = EPL - 1; j >= 0; --j) at = key[j] == top ? j : at;
+      const int gone = lane == owner ? at : -1;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) key[j] = gone == j ? 0 : key[j];
+    }
     // K <= TG*E/G eligible experts always remain, so top != 0; the clamp
     // only keeps the index in range.
     const int e = min(owner * EPL + __builtin_amdgcn_readlane(at, owner), E - 1);
@@ -646,12 +706,13 @@ hipError_t launch_router(const Plan& p, const void* x, const float* w_router,
   const int eplp = epl <= 1 ? 1 : epl <= 2 ? 2 : epl <= 4 ? 4 : epl <= 8 ? 8 : 16;
   const int gs = p.E / p.G, seg_l = gs / eplp;
   const bool seg = gs % eplp == 0 && (seg_l & (seg_l - 1)) == 0;
+  const int lg = seg ? __builtin_ctz(static_cast<unsigned>(seg_l)) : 0;
   // partials live in the workspace and given logits are 16-byte aligned
   // (checked at the boundary), so rows of E % 4 == 0 floats are too
   const int vec4 = p.E % 4 == 0;
 #define BEAM_SEL4(EPL, KS, SEG, SM)                                            \
   BEAM_LAUNCH(tm, "router_select", (router_select<EPL, KS, SEG, SM>), grid, dim3(256), 0, s, part, \
-              ks, vec4, p.T, p.E, p.G, p.TG, p.K, p.topn, p.normed ? 1 : 0, p.scale, bias, \
+              ks, vec4, p.T, p.E, p.G, p.TG, p.K, p.topn, lg, p.normed ? 1 : 0, p.scale, bias, \
               const_cast<float*>(lo), idx, w)
 #define BEAM_SEL3(EPL, KS, SEG)                                                \
   do {                                                                         \
