@@ -14,6 +14,8 @@
 // and every output written once: both directions are bound by those bytes.
 // Sums of squares and dot products are binary32, reduced lane by lane, then
 // wave by wave in a fixed order.
+#include <type_traits>
+
 #include "common.h"
 #include "internal.h"
 
@@ -44,6 +46,41 @@ __device__ __forceinline__ void load_vec(const IO* p, float (&v)[VEC]) {
   }
 }
 
+// VEC values as they lie in memory (bf16 ones two to a register).
+template <typename IO, int VEC>
+struct Raw {
+  static constexpr int kWords = VEC == 1 ? 1 : VEC * static_cast<int>(sizeof(IO)) / 16;
+  using Word = std::conditional_t<VEC == 1, IO, u32x4>;
+  Word w[kWords];
+  __device__ __forceinline__ void load(const IO* p) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = *reinterpret_cast<const Word*>(p + i * (VEC / kWords));
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = Word{};
+  }
+  // Makes the compiler forget values it has unpacked (it would rather keep
+  // them, in twice the registers, than unpack again).
+  __device__ __forceinline__ void repack() {
+    if constexpr (VEC > 1) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[i]));
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (VEC == 1) {
+      if constexpr (sizeof(IO) == 2) return bf16_bits_to_f32(w[0]);
+      else return w[0];
+    } else if constexpr (sizeof(IO) == 2) {
+      const uint32_t v = w[0][j / 2];
+      return __uint_as_float(j % 2 ? v & 0xFFFF0000u : v << 16);
+    } else {
+      return __uint_as_float(w[j / 4][j % 4]);
+    }
+  }
+};
+
 template <typename IO, int VEC>
 __device__ __forceinline__ void store_vec(IO* p, const float (&v)[VEC]) {
   if constexpr (VEC == 1) {
@@ -64,6 +101,15 @@ __device__ __forceinline__ void store_vec(IO* p, const float (&v)[VEC]) {
   }
 }
 
+// Adds another lane's value in one data-parallel move: CTRL swaps neighbours
+// or pairs, mirrors half rows or rows of 16, or hands a row's last lane to
+// the next rows (which then hold the sum so far; the last lane ends with all).
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+                 0, static_cast<int>(__float_as_uint(v)), CTRL, 0xF, 0xF, false)));
+}
+
 // Sums over the workgroup of N values a thread, the same bits in every
 // thread; sh [N][kMaxWaves] must not be in use by an earlier sum that a wave
 // may still be reading.
@@ -71,10 +117,18 @@ template <int N>
 __device__ __forceinline__ void block_sum(float (&v)[N], float (*sh)[kMaxWaves]) {
   const int wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
 #pragma unroll
-  for (int off = kWave / 2; off >= 1; off >>= 1)
+  for (int i = 0; i < N; ++i) v[i] = dpp_add<0xB1>(v[i]);   // quad_perm(1, 0, 3, 2)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], off);
-  if (threadIdx.x % kWave == 0)
+  for (int i = 0; i < N; ++i) v[i] = dpp_add<0x4E>(v[i]);   // quad_perm(2, 3, 0, 1)
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_add<0x141>(v[i]);  // row_half_mirror
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_add<0x140>(v[i]);  // row_mirror
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_add<0x142>(v[i]);  // row_bcast:15
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_add<0x143>(v[i]);  // row_bcast:31
+  if (threadIdx.x % kWave == kWave - 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) sh[i][wave] = v[i];
   __syncthreads();
@@ -200,106 +254,151 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
 // walks over tokens blockIdx.x, blockIdx.x + gridDim.x, ... and holds its
 // share of the weights' gradients in registers; the shares of all
 // workgroups go to the workspace and are added in a fixed order by
-// norm_weight_grad (no atomics).
-template <typename IO, int VEC, int NC>
-__global__ __launch_bounds__(1024) void norm_residual_backward(NormGradArgs a) {
+// norm_weight_grad (no atomics).  The weights lie in LDS and the inputs stay
+// packed as they lie in memory, so that two workgroups of a 5,120-column row
+// share a compute unit and one's loads run beside the other's sums: 8,191
+// tokens, bf16, one gate a token, 160 us, 4.7 TB/s (everything unpacked in
+// registers, one workgroup a unit: 181 us; the next token's loads issued
+// ahead instead: 165 us; half the threads with twice the columns: 186 us).
+// O: there is a block output; DX: there is a gradient of x; CG: a gate for
+// each channel (or none, or one a token, in the other form).
+template <typename IO, int VEC, int NC, bool O, bool DX, bool CG>
+__global__ __launch_bounds__(1024, VEC == 8 && NC == 1 && !CG ? 5 : 4) void norm_residual_backward(NormGradArgs a) {
   __shared__ float sh[2][3][kMaxWaves], sh2[1][kMaxWaves];
+  __shared__ __attribute__((aligned(16))) float wts[2][1024 * NC * VEC];  // w_pre, w_post
   const int H = a.H;
   const float rh = 1.0f / static_cast<float>(H);
-  float w_pre[NC][VEC], w_post[NC][VEC], g_pre[NC][VEC], g_post[NC][VEC];
+  float g_pre[NC][VEC], g_post[NC][VEC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
+    // a thread reads only what it wrote
     const int c = (threadIdx.x + i * blockDim.x) * VEC;
+    float w[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) w_pre[i][j] = w_post[i][j] = g_pre[i][j] = g_post[i][j] = 0.0f;
-    if (c < H) {
-      if (a.dx) load_vec<float, VEC>(a.pre + c, w_pre[i]);
-      if (a.o) load_vec<float, VEC>(a.post + c, w_post[i]);
+    for (int j = 0; j < VEC; ++j) g_pre[i][j] = g_post[i][j] = w[j] = 0.0f;
+    if (DX) {
+      if (c < H) load_vec<float, VEC>(a.pre + c, w);
+      store_vec<float, VEC>(wts[0] + c, w);
+    }
+    if (O) {
+      if (c < H) load_vec<float, VEC>(a.post + c, w);
+      store_vec<float, VEC>(wts[1] + c, w);
     }
   }
-  int par = 0;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
-    const int64_t base = t * H;
-    float r[NC][VEC], dx[NC][VEC], dr[NC][VEC], o[NC][VEC], gv[NC][VEC];
+  struct Row {
+    Raw<float, VEC> r[NC], dr[NC];
+    Raw<IO, VEC> dx[NC], o[NC], gv[NC];
+  };
+  auto load = [&](Row& x, int64_t t) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * VEC;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) r[i][j] = dx[i][j] = dr[i][j] = o[i][j] = gv[i][j] = 0.0f;
+      const int64_t at = t * H + c;
       if (c < H) {
-        if (a.dx) {
-          load_vec<float, VEC>(a.r + base + c, r[i]);
-          load_vec<IO, VEC>(static_cast<const IO*>(a.dx) + base + c, dx[i]);
-        }
-        if (a.d_res) load_vec<float, VEC>(a.d_res + base + c, dr[i]);
-        if (a.o) load_vec<IO, VEC>(static_cast<const IO*>(a.o) + base + c, o[i]);
-        if (a.gate_cols > 1)
-          load_vec<IO, VEC>(static_cast<const IO*>(a.gate) + base + c, gv[i]);
+        if (DX) x.r[i].load(a.r + at), x.dx[i].load(static_cast<const IO*>(a.dx) + at);
+        if (O) x.o[i].load(static_cast<const IO*>(a.o) + at);
+        if (a.d_res) x.dr[i].load(a.d_res + at);
+        if (CG) x.gv[i].load(static_cast<const IO*>(a.gate) + at);
       }
     }
+  };
+  Row x;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) x.r[i].zero(), x.dr[i].zero(), x.dx[i].zero(), x.o[i].zero(), x.gv[i].zero();
+  int par = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
+    const int64_t base = t * H;
+    load(x, t);
     float tg = 1.0f, tdg = 0.0f;  // a token gate's sigmoid and derivative
-    if (a.gate_cols == 1) {
+    if (O && !CG && a.gate_cols == 1) {
       float g[1];
       load_vec<IO, 1>(static_cast<const IO*>(a.gate) + t, g);
       tg = sigmoid_fast(g[0], tdg);
     }
     float s[3] = {0.0f, 0.0f, 0.0f};  // sum r'^2, sum w_pre dx r', sum o^2
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < NC; ++i) {
+      const int c = (threadIdx.x + i * blockDim.x) * VEC;
+      float w[VEC];
+      if (DX) load_vec<float, VEC>(wts[0] + c, w);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        s[0] = __builtin_fmaf(r[i][j], r[i][j], s[0]);
-        s[1] = __builtin_fmaf(w_pre[i][j] * dx[i][j], r[i][j], s[1]);
-        s[2] = __builtin_fmaf(o[i][j], o[i][j], s[2]);
+        const float rv = x.r[i].get(j), ov = x.o[i].get(j);
+        if (DX) {
+          s[0] = __builtin_fmaf(rv, rv, s[0]);
+          s[1] = __builtin_fmaf(w[j] * x.dx[i].get(j), rv, s[1]);
+        }
+        if (O) s[2] = __builtin_fmaf(ov, ov, s[2]);
       }
+    }
     block_sum<3>(s, sh[par]);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) x.r[i].repack(), x.dx[i].repack(), x.o[i].repack();
     const float inv_r = 1.0f / sqrtf(s[0] * rh + a.eps);
     const float inv_o = 1.0f / sqrtf(s[2] * rh + a.eps);
-    const float k_r = a.dx ? (s[1] * inv_r * rh) * inv_r * inv_r : 0.0f;
+    const float k_r = (s[1] * inv_r * rh) * inv_r * inv_r;
     float u[1] = {0.0f};  // sum w_post dn o (without a token gate's sigmoid)
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * VEC;
-      float out[VEC], dgate[VEC];
+      float out[VEC], dgate[VEC], wp[VEC], wq[VEC];
+      if (DX) load_vec<float, VEC>(wts[0] + c, wp);
+      if (O) load_vec<float, VEC>(wts[1] + c, wq);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        g_pre[i][j] = __builtin_fmaf(dx[i][j], r[i][j] * inv_r, g_pre[i][j]);
-        float d = dr[i][j] + inv_r * (w_pre[i][j] * dx[i][j]) - r[i][j] * k_r;
-        out[j] = a.alpha * d;
-        d *= a.beta;
-        if (a.gate_cols > 1) {
-          float dg;
-          const float g = sigmoid_fast(gv[i][j], dg);
-          dgate[j] = d * (o[i][j] * inv_o * w_post[i][j]) * dg;
-          d *= g;
+        float d = x.dr[i].get(j);
+        if (DX) {
+          const float rv = x.r[i].get(j), xv = x.dx[i].get(j);
+          g_pre[i][j] = __builtin_fmaf(xv, rv * inv_r, g_pre[i][j]);
+          d = d + inv_r * (wp[j] * xv) - rv * k_r;
         }
-        dr[i][j] = d;  // gradient of y but for a token gate's sigmoid
-        u[0] = __builtin_fmaf(w_post[i][j] * d, o[i][j], u[0]);
+        out[j] = a.alpha * d;
+        if (O) {
+          const float ov = x.o[i].get(j);
+          d *= a.beta;
+          if (CG) {
+            float dg;
+            const float g = sigmoid_fast(x.gv[i].get(j), dg);
+            dgate[j] = d * (ov * inv_o * wq[j]) * dg;
+            d *= g;
+          }
+          // gradient of y but for a token gate's sigmoid, in dr's place
+          if constexpr (VEC == 1) x.dr[i].w[0] = d;
+          else x.dr[i].w[j / 4][j % 4] = __float_as_uint(d);
+          u[0] = __builtin_fmaf(wq[j] * d, ov, u[0]);
+        }
       }
       if (c < H) {
         store_vec<float, VEC>(a.d_residual + base + c, out);
-        if (a.gate_cols > 1) store_vec<IO, VEC>(static_cast<IO*>(a.d_gate) + base + c, dgate);
+        if (CG) store_vec<IO, VEC>(static_cast<IO*>(a.d_gate) + base + c, dgate);
       }
     }
-    if (a.o) {
+    if (O) {
       block_sum<1>(u, sh2);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) x.o[i].repack();
       const float k_o = (u[0] * tg * inv_o * rh) * inv_o * inv_o;
-      if (a.gate_cols == 1 && threadIdx.x == 0) {
+      if (!CG && a.gate_cols == 1 && threadIdx.x == 0) {
         const float dg[1] = {u[0] * inv_o * tdg};
         store_vec<IO, 1>(static_cast<IO*>(a.d_gate) + t, dg);
       }
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * VEC;
-        float out[VEC];
+        float out[VEC], wq[VEC];
+        load_vec<float, VEC>(wts[1] + c, wq);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const float dn = tg * dr[i][j];
-          g_post[i][j] = __builtin_fmaf(dn, o[i][j] * inv_o, g_post[i][j]);
-          out[j] = inv_o * (w_post[i][j] * dn) - o[i][j] * k_o;
+          const float dn = tg * x.dr[i].get(j), ov = x.o[i].get(j);
+          g_post[i][j] = __builtin_fmaf(dn, ov * inv_o, g_post[i][j]);
+          out[j] = inv_o * (wq[j] * dn) - ov * k_o;
         }
         if (c < H) store_vec<IO, VEC>(static_cast<IO*>(a.d_o) + base + c, out);
       }
+    }
+    if (!a.d_res) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) x.dr[i].zero();
     }
   }
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * H;
@@ -307,41 +406,49 @@ __global__ __launch_bounds__(1024) void norm_residual_backward(NormGradArgs a) {
   for (int i = 0; i < NC; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * VEC;
     if (c >= H) continue;
-    if (a.dx) store_vec<float, VEC>(part + c, g_pre[i]);
-    if (a.o) store_vec<float, VEC>(part + H + c, g_post[i]);
+    if (DX) store_vec<float, VEC>(part + c, g_pre[i]);
+    if (O) store_vec<float, VEC>(part + H + c, g_post[i]);
   }
 }
 
-// d_w[c] = sum over the n workgroups' shares, 64 columns a workgroup: four
-// waves each add every fourth share, then meet in LDS in wave order.
-__global__ __launch_bounds__(256) void norm_weight_grad(const float* __restrict__ part, int n,
-                                                        int H, float* __restrict__ d_pre,
-                                                        float* __restrict__ d_post) {
-  __shared__ float sh[4][kWave];
+// d_w[c] = sum over the n workgroups' shares, 64 columns a workgroup: sixteen
+// waves each add every sixteenth share, then meet in LDS in wave order.
+__global__ __launch_bounds__(1024) void norm_weight_grad(const float* __restrict__ part, int n,
+                                                         int H, float* __restrict__ d_pre,
+                                                         float* __restrict__ d_post) {
+  __shared__ float sh[16][kWave];
   float* out = blockIdx.y == 0 ? d_pre : d_post;
   if (!out) return;
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   const int c = blockIdx.x * kWave + lane;
   float s = 0.0f;
   if (c < H)
-    for (int i = wave; i < n; i += 4)
+#pragma unroll 8
+    for (int i = wave; i < n; i += 16)
       s += part[(static_cast<int64_t>(i) * 2 + blockIdx.y) * H + c];
   sh[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && c < H) out[c] = ((sh[0][lane] + sh[1][lane]) + sh[2][lane]) + sh[3][lane];
+  if (wave == 0 && c < H) {
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += sh[w][lane];
+    out[c] = s;
+  }
 }
 
 // Threads of a row: rows of a multiple of 8 columns take 8 consecutive
 // columns a thread (16-byte accesses; every such row starts 16-byte aligned),
 // others single ones.
+// `pairs`: two chunks of 8 a thread also where one would do (rows of more
+// than 2,048 columns; the forward of many tokens: 16,384 gated tokens of 5,120
+// 211 against 215 us, while one token is faster spread over more threads).
 struct RowShape {
   int vec, nc, threads;
 };
-RowShape row_shape(int H) {
+RowShape row_shape(int H, bool pairs) {
   RowShape s;
   s.vec = H % 8 == 0 ? 8 : 1;
   const int chunks = H / s.vec;
-  s.nc = s.vec == 8 ? (chunks <= 1024 ? 1 : 2) : (chunks <= 4096 ? 4 : 16);
+  s.nc = s.vec == 8 ? (chunks <= (pairs ? 256 : 1024) ? 1 : 2) : (chunks <= 4096 ? 4 : 16);
   s.threads = static_cast<int>(ceil_div(ceil_div(chunks, s.nc), kWave)) * kWave;
   return s;
 }
@@ -357,7 +464,7 @@ int norm_grad_groups(int64_t T) { return static_cast<int>(T < 512 ? T : 512); }
   else RUN(1, 16)
 
 hipError_t launch_norm_residual(const NormArgs& a, int64_t T, int32_t dtype, hipStream_t s) {
-  const RowShape rs = row_shape(a.H);
+  const RowShape rs = row_shape(a.H, T >= 1024);
   const dim3 grid(static_cast<unsigned>(T)), block(rs.threads);
 #define BEAM_NORM(V, N)                                                                       \
   do {                                                                                        \
@@ -373,25 +480,35 @@ hipError_t launch_norm_residual(const NormArgs& a, int64_t T, int32_t dtype, hip
 
 hipError_t launch_norm_residual_backward(const NormGradArgs& a, int32_t dtype, float* d_pre,
                                          float* d_post, hipStream_t s) {
-  const RowShape rs = row_shape(a.H);
+  const RowShape rs = row_shape(a.H, false);
   const int n = norm_grad_groups(a.T);
   const dim3 grid(n), block(rs.threads);
   if (n > 0) {
 #define BEAM_NORM(V, N)                                                                       \
   do {                                                                                        \
-    if (dtype == BEAM_BF16)                                                                   \
-      hipLaunchKernelGGL((norm_residual_backward<uint16_t, V, N>), grid, block, 0, s, a);     \
-    else                                                                                      \
-      hipLaunchKernelGGL((norm_residual_backward<float, V, N>), grid, block, 0, s, a);        \
+    if (dtype == BEAM_BF16) BEAM_NORM2(uint16_t, V, N);                                       \
+    else BEAM_NORM2(float, V, N);                                                             \
   } while (0)
+#define BEAM_NORM2(IO, V, N)                                                                  \
+  do {                                                                                        \
+    if (!a.o) BEAM_NORM3(IO, V, N, false, true, false);                                       \
+    else if (a.gate_cols > 1 && a.dx) BEAM_NORM3(IO, V, N, true, true, true);                 \
+    else if (a.gate_cols > 1) BEAM_NORM3(IO, V, N, true, false, true);                        \
+    else if (a.dx) BEAM_NORM3(IO, V, N, true, true, false);                                   \
+    else BEAM_NORM3(IO, V, N, true, false, false);                                            \
+  } while (0)
+#define BEAM_NORM3(IO, V, N, O, DX, CG)                                                       \
+  hipLaunchKernelGGL((norm_residual_backward<IO, V, N, O, DX, CG>), grid, block, 0, s, a)
     BEAM_NORM_SHAPES(BEAM_NORM);
+#undef BEAM_NORM3
+#undef BEAM_NORM2
 #undef BEAM_NORM
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (d_pre || d_post)
     hipLaunchKernelGGL(norm_weight_grad, dim3(static_cast<unsigned>(ceil_div(a.H, kWave)), 2),
-                       dim3(256), 0, s, a.part, n, a.H, d_pre, d_post);
+                       dim3(1024), 0, s, a.part, n, a.H, d_pre, d_post);
   return hipGetLastError();
 }
 
