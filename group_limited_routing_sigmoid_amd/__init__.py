@@ -77,7 +77,8 @@ def lib():
         L.beam_moe_route.argtypes = [D, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.beam_moe_route_backward.argtypes = [D, i64, vp, vp, vp, vp, vp]
         L.beam_moe_quant_e4m3_2d.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp, vp, vp]
-        L.beam_moe_matmul_e4m3.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, i32, vp, vp]
+        L.beam_moe_matmul_e4m3.argtypes = [i64, i64, i64, vp, vp, i64, i64, vp, vp, i64, i64, i32,
+                                           i32, vp, vp]
         f32 = ctypes.c_float
         L.beam_moe_norm_residual.argtypes = [i64, i64, i32, vp, vp, vp, i64, vp, f32, f32, f32,
                                              vp, vp, vp, vp, vp, vp]
@@ -227,11 +228,12 @@ def _alloc_on(stream):
     return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
-def _arg(name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple) -> int:
-    """Address of a contiguous tensor on GPU `dev` of the given dtype and
-    shape; raises ValueError otherwise."""
+def _arg(name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple,
+         strided: bool = False) -> int:
+    """Address of a contiguous (or strided, where a call takes strides) tensor
+    on GPU `dev` of the given dtype and shape; raises ValueError otherwise."""
     if (t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0
-            and t.is_contiguous()):
+            and (strided or t.is_contiguous())):
         return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name}: tensors passed to the HIP library must be on the GPU")
@@ -402,8 +404,10 @@ def quant_e4m3_2d(v: torch.Tensor, block: bool = False, straight: bool = True,
     """beam_moe_quant_e4m3_2d of a 2-D fp32/bf16 tensor [R,C]: (codes [R,C'],
     scales, transposed codes [C,R'], their scales), C' and R' the next
     multiples of 128, the added codes zero.  A scale covers 128 values of a
-    row (of a column in the transposed codes), or with block 128 x 128 values.
-    None for an orientation that is not asked for."""
+    row (of a column in the transposed codes): [R,C'/128] and [C,R'/128],
+    stored block-major (views of transposed tensors); or with block 128 x 128
+    values: [R'/128,C'/128] and its transpose.  None for an orientation that
+    is not asked for."""
     if v.dim() != 2:
         raise ValueError(f"v: shape {tuple(v.shape)}, expected [rows, cols]")
     if v.dtype not in (torch.bfloat16, torch.float32):
@@ -415,10 +419,12 @@ def quant_e4m3_2d(v: torch.Tensor, block: bool = False, straight: bool = True,
     q = s = qt = st = None
     if straight:
         q = _empty(stream, device, torch.uint8, rows, nc * 128)
-        s = _empty(stream, device, torch.float32, nr if block else rows, nc)
+        s = (_empty(stream, device, torch.float32, nr, nc) if block else
+             _empty(stream, device, torch.float32, nc, rows).t())
     if transposed:
         qt = _empty(stream, device, torch.uint8, cols, nr * 128)
-        st = _empty(stream, device, torch.float32, nc if block else cols, nr)
+        st = (_empty(stream, device, torch.float32, nc, nr) if block else
+              _empty(stream, device, torch.float32, nr, cols).t())
     _run(lib().beam_moe_quant_e4m3_2d, "beam_moe_quant_e4m3_2d", stream, dev, (v, q, s, qt, st),
          rows, cols, BF16 if v.dtype is torch.bfloat16 else F32, 1 if block else 0, pv,
          *(None if t is None else t.data_ptr() for t in (q, s, qt, st)))
@@ -430,7 +436,8 @@ def matmul_e4m3(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch.
                 stream=None) -> torch.Tensor:
     """beam_moe_matmul_e4m3: a b^T [M,N] in `dtype` from e4m3 codes a [M,K] and
     b [N,K] (uint8), K a multiple of 128, with scales s_a [M,K/128] and s_b
-    [ceil(N/128),K/128] (128 x 128 blocks) or [N,K/128] (rows of b)."""
+    [ceil(N/128),K/128] (128 x 128 blocks) or [N,K/128] (rows of b), which may
+    have any strides."""
     if a.dim() != 2 or b.dim() != 2:
         raise ValueError(f"shapes {tuple(a.shape)} and {tuple(b.shape)}, expected [M, K] and [N, K]")
     (M, K), N = a.shape, b.shape[0]
@@ -441,12 +448,12 @@ def matmul_e4m3(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch.
     rows = s_b.dim() == 2 and s_b.shape[0] == N
     dev = a.get_device()
     pa, pb = _arg("a", a, dev, torch.uint8, (M, K)), _arg("b", b, dev, torch.uint8, (N, K))
-    psa = _arg("s_a", s_a, dev, torch.float32, (M, K // 128))
-    psb = _arg("s_b", s_b, dev, torch.float32, (N if rows else (N + 127) // 128, K // 128))
+    psa = _arg("s_a", s_a, dev, torch.float32, (M, K // 128), True)
+    psb = _arg("s_b", s_b, dev, torch.float32, (N if rows else (N + 127) // 128, K // 128), True)
     if out is None:
         out = _empty(stream, a.device, dtype, M, N)
     _run(lib().beam_moe_matmul_e4m3, "beam_moe_matmul_e4m3", stream, dev, (a, s_a, b, s_b, out),
-         M, N, K, pa, psa, pb, psb, 1 if rows else 0, BF16 if dtype is torch.bfloat16 else F32,
+         M, N, K, pa, psa, *s_a.stride(), pb, psb, *s_b.stride(), 1 if rows else 0, BF16 if dtype is torch.bfloat16 else F32,
          _arg("out", out, dev, dtype, (M, N)))
     return out
 

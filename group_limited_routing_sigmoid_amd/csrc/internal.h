@@ -172,8 +172,9 @@ hipError_t launch_quant_2d(int64_t rows, int64_t cols, int32_t dtype, bool block
 constexpr int64_t kMatmulMaxK = 1 << 22, kMatmulMaxRows = (1 << 23) - 128;
 constexpr int64_t kMatmulMaxOut = int64_t{1} << 38;
 hipError_t launch_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, const float* sa,
-                              const uint8_t* b, const float* sb, bool rows, int32_t dtype,
-                              void* y, hipStream_t s);
+                              const int64_t* sa_stride, const uint8_t* b, const float* sb,
+                              const int64_t* sb_stride, bool rows, int32_t dtype, void* y,
+                              hipStream_t s);
 // fp8.hip
 hipError_t launch_quant_e4m3(int64_t rows, int64_t cols, int32_t dtype,
                              const void* v, uint8_t* q, float* scales,

@@ -143,8 +143,9 @@ int beam_moe_quant_e4m3_2d(int64_t rows, int64_t cols, int32_t dtype, int32_t bl
 }
 
 int beam_moe_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, const float* sa,
-                         const uint8_t* b, const float* sb, int32_t b_rows, int32_t dtype,
-                         void* y, void* stream) {
+                         int64_t sa_row, int64_t sa_block, const uint8_t* b, const float* sb,
+                         int64_t sb_row, int64_t sb_block, int32_t b_rows, int32_t dtype, void* y,
+                         void* stream) {
   if (M < 0 || N < 0 || K < 0 || (dtype != BEAM_F32 && dtype != BEAM_BF16) ||
       (b_rows != 0 && b_rows != 1))
     return BEAM_ERR_INVALID_ARG;
@@ -153,9 +154,11 @@ int beam_moe_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, cons
     return BEAM_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return BEAM_OK;
   if (!y || (K > 0 && (!a || !sa || !b || !sb))) return BEAM_ERR_INVALID_ARG;
+  if (sa_row < 0 || sa_block < 0 || sb_row < 0 || sb_block < 0) return BEAM_ERR_INVALID_ARG;
   if (!aligned16(a) || !aligned16(sa) || !aligned16(b) || !aligned16(sb) || !aligned16(y))
     return BEAM_ERR_INVALID_ARG;
-  return hip_status(launch_matmul_e4m3(M, N, K, a, sa, b, sb, b_rows != 0, dtype, y,
+  const int64_t za[2] = {sa_row, sa_block}, zb[2] = {sb_row, sb_block};
+  return hip_status(launch_matmul_e4m3(M, N, K, a, sa, za, b, sb, zb, b_rows != 0, dtype, y,
                                        static_cast<hipStream_t>(stream)));
 }
 

@@ -86,6 +86,12 @@ __device__ __forceinline__ void buf_dma16(__amdgpu_buffer_rsrc_t r, uint32_t vof
                                            0, 0);
 }
 
+// Scale words with any layout: word (row, block) at p[row * r + block * k].
+struct Scales {
+  const float* p;
+  int64_t r, k;
+};
+
 // Four neighbouring values of a row to LDS.
 __device__ __forceinline__ void put4(float* p, float a, float b, float c, float d) {
   *reinterpret_cast<f32x4*>(p) = f32x4{a, b, c, d};
@@ -114,12 +120,12 @@ __device__ __forceinline__ void store_tile(OUT* room, int lane, const f32x4 (&ac
                                            int64_t m0, int rw, int mr, int64_t N, int64_t n0, int cw,
                                            int nr) {
   constexpr int kVec = 16 / static_cast<int>(sizeof(OUT)), kPitch = TN + kVec, kChunks = TN / kVec;
-  constexpr int kRows = FM == 1 ? 16 : 32;
   const bool vec = N % kVec == 0;  // every row of y then starts 16-byte aligned
 #pragma unroll
   for (int m = 0; m < FM; m += 2) {
+    const int rows = m + 1 < FM ? 32 : 16;  // known once unrolled
 #pragma unroll
-    for (int i = 0; i < kRows / 16; ++i)
+    for (int i = 0; i < rows / 16; ++i)
 #pragma unroll
       for (int n = 0; n < FN; ++n)
         put4(room + (16 * i + lane % 16) * kPitch + 16 * n + 4 * (lane / 16), acc[n][m + i][0],
@@ -128,14 +134,14 @@ __device__ __forceinline__ void store_tile(OUT* room, int lane, const f32x4 (&ac
     const int row0 = rw + 16 * m;
     if (vec) {
 #pragma unroll
-      for (int i = 0; i < kRows * kChunks / kWave; ++i) {
+      for (int i = 0; i < rows * kChunks / kWave; ++i) {
         const int r = (i * kWave + lane) / kChunks, c = (i * kWave + lane) % kChunks * kVec;
         const u32x4 v = *reinterpret_cast<const u32x4*>(room + r * kPitch + c);
         // N % kVec == 0: a chunk that starts inside the row ends inside it
         if (row0 + r <= mr && cw + c <= nr) st16(y + (m0 + row0 + r) * N + n0 + cw + c, v);
       }
     } else {
-      for (int i = 0; i < kRows * TN / kWave; ++i) {
+      for (int i = 0; i < rows * TN / kWave; ++i) {
         const int r = (i * kWave + lane) / TN, c = (i * kWave + lane) % TN;
         const OUT v = room[r * kPitch + c];
         if (row0 + r <= mr && cw + c <= nr) y[(m0 + row0 + r) * N + n0 + cw + c] = v;
@@ -159,8 +165,8 @@ __device__ __forceinline__ void store_tile(OUT* room, int lane, const f32x4 (&ac
 // outstanding copies.
 template <int BM, int BN, int KS, int WM, int WN, int ST, bool ROWS, typename OUT>
 __global__ __launch_bounds__(64 * KS * WM * WN) void matmul_tile(
-    const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ b,
-    const float* __restrict__ sb, OUT* __restrict__ y, int64_t M, int64_t N, int64_t K) {
+    const uint8_t* __restrict__ a, Scales sa, const uint8_t* __restrict__ b, Scales sb,
+    OUT* __restrict__ y, int64_t M, int64_t N, int64_t K) {
   constexpr int G = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr int kScales = (BM + BN) * kRow;                    // scale words after the tiles
   constexpr int kWords = ((BM + BN + 63) / 64) * 64;           // copied 64 at a time
@@ -186,6 +192,7 @@ __global__ __launch_bounds__(64 * KS * WM * WN) void matmul_tile(
   const uint8_t* bt0 = b + n0 * K;
   uint32_t aoff[NA], boff[NB];
   const float* soff[NS];
+  int64_t sstep[NS];
   int copies = 0;
 #pragma unroll
   for (int i = 0; i < NA; ++i) {
@@ -203,7 +210,8 @@ __global__ __launch_bounds__(64 * KS * WM * WN) void matmul_tile(
   for (int i = 0; i < NS; ++i) {
     const int w = 64 * (wg + i * G) + lane;  // tile rows of a, then of b
     const int64_t r = w < BM ? m0 + min(w, mr) : n0 + min(w - BM, nr);
-    soff[i] = w < BM ? sa + r * nkb : sb + (ROWS ? r : r / 128) * nkb;
+    soff[i] = w < BM ? sa.p + r * sa.r + g * sa.k : sb.p + (ROWS ? r : r / 128) * sb.r + g * sb.k;
+    sstep[i] = (w < BM ? sa.k : sb.k) * KS;  // from one of the group's blocks to its next
     copies += (64 * (wg + i * G) < kWords) ? 1 : 0;
   }
   auto copy = [&](int st, int kb) {
@@ -217,7 +225,10 @@ __global__ __launch_bounds__(64 * KS * WM * WN) void matmul_tile(
       if (8 * (wg + i * G) <= mr) dma16(at0 + (aoff[i] + kb * 128), at + (wg + i * G) * 1024);
 #pragma unroll
     for (int i = 0; i < NS; ++i)
-      if (64 * (wg + i * G) < kWords) dma4(soff[i] + kb, at + kScales + (wg + i * G) * 256);
+      if (64 * (wg + i * G) < kWords) {
+        dma4(soff[i], at + kScales + (wg + i * G) * 256);
+        soff[i] += sstep[i];  // the blocks are copied in order
+      }
   };
 
   constexpr bool kWide = sizeof(OUT) == 4;  // binary32 results: binary32 sums
@@ -320,8 +331,7 @@ __global__ __launch_bounds__(64 * KS * WM * WN) void matmul_tile(
 }
 
 // ---- many rows -------------------------------------------------------------
-// 256-column tiles of BM rows (256; 128 for binary32 results, whose widened
-// fragments take twice the registers), eight waves of BM/2 x 64, one
+// 256-column tiles of BM rows, eight waves of BM/2 x 64, one
 // workgroup per compute unit, two stages of one block.  The next stage's
 // copies are spread over the products (nine instructions a wave: issued
 // together they fill the unit's texture path and hold up every wave's LDS
@@ -345,15 +355,16 @@ template <int BM, bool ROWS, typename OUT>
 struct Many {
   static constexpr bool kWide = sizeof(OUT) == 4;
   static constexpr int BN = 256, TN = 64, FN = TN / 16, W = 8;
-  static constexpr int kScales = (BM + BN) * kRow, kStage = kScales + (BM + BN) * 4;
+  static constexpr int AR = (BM + 63) / 64 * 64;  // rows of room for a's part: copies are of 64
+  static constexpr int kScales = (AR + BN) * kRow, kStage = kScales + (AR + BN) * 4;
   static constexpr int kRoom = 32 * (TN * static_cast<int>(sizeof(OUT)) + 16);
   static constexpr int kLds = std::max(2 * kStage, W * kRoom);
   using Frag = std::conditional_t<kWide, Wide, i32x8>;
 
   // FM: 16-row fragments of a wave (its share of 2 * 16 FM rows).
   template <int FM>
-  static __device__ __forceinline__ void run(unsigned char* lds, const uint8_t* a, const float* sa,
-                                             const uint8_t* b, const float* sb, OUT* y, int64_t M,
+  static __device__ __forceinline__ void run(unsigned char* lds, const uint8_t* a, Scales sa,
+                                             const uint8_t* b, Scales sb, OUT* y, int64_t M,
                                              int64_t N, int64_t K, int64_t m0, int64_t n0) {
     constexpr int R = 32 * FM, TM = 16 * FM;  // rows of the piece, of a wave
     constexpr int NA = (R + 63) / 64, NB = BN / 64;  // copies of 8 rows a wave
@@ -380,28 +391,25 @@ struct Many {
     for (int i = 0; i < NB; ++i) bstep[i] = 64 * i <= nr ? 64u * i * static_cast<uint32_t>(K) : 0u;
     // scale words: waves 0-3 of the b rows, the others of the a rows (where
     // there are fewer, two waves copy the same)
-    const int sw = wave < 4 ? wave : (wave - 4) % (BM / 64), srow = 64 * sw + lane;
+    const int sw = wave < 4 ? wave : (wave - 4) % (AR / 64), srow = 64 * sw + lane;
     const float* soff;
     if (wave < 4) {
       const int64_t r = n0 + min(srow, nr);
-      soff = sb + (ROWS ? r : r / 128) * nkb;
+      soff = sb.p + (ROWS ? r : r / 128) * sb.r;
     } else {
-      soff = sa + (m0 + min(srow, mr)) * nkb;
+      soff = sa.p + (m0 + min(srow, mr)) * sa.r;
     }
-    const int sdst = kScales + (wave < 4 ? BM * 4 : 0) + sw * 256;
+    const int64_t sstep = wave < 4 ? sb.k : sa.k;
+    const int sdst = kScales + (wave < 4 ? AR * 4 : 0) + sw * 256;
     auto copy = [&](int st, int kb, int c) {
       unsigned char* t = lds + st * kStage;
-      if (c < NB) buf_dma16(rb, coff, bstep[c < NB ? c : 0] + kb * 128, t + BM * kRow + (wave + W * c) * 1024);
+      if (c < NB) buf_dma16(rb, coff, bstep[c < NB ? c : 0] + kb * 128, t + AR * kRow + (wave + W * c) * 1024);
       else if (c < NB + NA) buf_dma16(ra, coff, astep[c < NB ? 0 : c - NB < NA ? c - NB : 0] + kb * 128, t + (wave + W * (c - NB)) * 1024);
-      else dma4(soff + kb, t + sdst);
+      else dma4(soff + kb * sstep, t + sdst);
     };
     auto operand = [](i32x8 q) {
       if constexpr (kWide) return widen(q);
       else return q;
-    };
-    auto product = [](const Frag& x, const Frag& w) {
-      if constexpr (kWide) return mfma_wide(x, w, f32x4{});
-      else return mfma_e4m3(x, w, f32x4{});
     };
     f32x4 acc[FN][FM];
 #pragma unroll
@@ -424,9 +432,9 @@ struct Many {
     };
     for (int kb = 0; kb < nkb; ++kb) {
       const unsigned char* at = lds + (kb & 1) * kStage + wm * TM * kRow;
-      const unsigned char* bt = lds + (kb & 1) * kStage + (BM + wn * TN) * kRow;
+      const unsigned char* bt = lds + (kb & 1) * kStage + (AR + wn * TN) * kRow;
       const float* sat = reinterpret_cast<const float*>(lds + (kb & 1) * kStage + kScales) + wm * TM + lane % 16;
-      const float* sbt = reinterpret_cast<const float*>(lds + (kb & 1) * kStage + kScales) + BM + wn * TN;
+      const float* sbt = reinterpret_cast<const float*>(lds + (kb & 1) * kStage + kScales) + AR + wn * TN;
       const int kn = min(kb + 1, nkb - 1);  // the last stage's copies are not used
       Frag bf[FN];
       f32x4 sr[ROWS ? FN : 1];
@@ -440,39 +448,73 @@ struct Many {
         for (int n = 0; n < FN; ++n)
           sr[ROWS ? n : 0] = *reinterpret_cast<const f32x4*>(sbt + 16 * n + 4 * (lane / 16));
       }
-      // Beside each product the multiply-adds of the third one before it
-      // (whose sums are ready by then), the next row fragment's codes and the
-      // next stage's copies on their way.
-      f32x4 p[kLag + 1];
+      constexpr bool kBeside = kWide && FM <= 4;  // registers for two fragments' sums
+      constexpr int kHeld = kWide ? (kBeside ? 2 * FN : FN) : kLag + 1;
+      f32x4 p[kHeld];
       auto add = [&](int i) {  // the block's sums of product i into the result's
         const int m = i / FN, n = i % FN;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          acc[n][m][r] = __builtin_fmaf(p[i % (kLag + 1)][r],
+          acc[n][m][r] = __builtin_fmaf(p[i % kHeld][r],
                                         ROWS ? sc[m & 1] * sr[ROWS ? n : 0][r] : sc[m & 1], acc[n][m][r]);
       };
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
         const Frag af = operand(next);
         float scn = 0.0f;
+        if constexpr (kWide) {
+          // A product is four dependent instructions: those of the row
+          // fragment's FN products take turns.  Their multiply-adds go beside
+          // the next fragment's or, where there are no registers for two
+          // fragments' sums, wait for them: the unit's other wave has the
+          // matrix cores then.
+          static_assert(FN == 4, "one product's multiply-adds beside each turn");
 #pragma unroll
-        for (int n = 0; n < FN; ++n) {
-          const int i = m * FN + n;
-          p[i % (kLag + 1)] = product(bf[n], af);
-          __builtin_amdgcn_sched_barrier(0);
-          if (n == 0 && m + 1 < FM) {
-            next = codes(at + 16 * (m + 1) * kRow);
-            scn = sat[16 * (m + 1)];
+          for (int j = 0; j < 4; ++j) {
+            const int i = m * 4 + j;
+#pragma unroll
+            for (int n = 0; n < FN; ++n)
+              p[(m * FN + n) % kHeld] =
+                  mfma16x16x32(bf[n].f[j], af.f[j], j ? p[(m * FN + n) % kHeld] : f32x4{});
+            __builtin_amdgcn_sched_barrier(0);
+            if (kBeside && m > 0) add(i - FN);
+            if (j == 0 && m + 1 < FM) {
+              next = codes(at + 16 * (m + 1) * kRow);
+              scn = sat[16 * (m + 1)];
+            }
+#pragma unroll
+            for (int c = i * kEach; c < (i + 1) * kEach && c < kCopies; ++c) copy((kb + 1) & 1, kn, c);
+            __builtin_amdgcn_sched_barrier(0);
           }
-          if (i >= kLag) add(i - kLag);
+          if (!kBeside || m == FM - 1)
 #pragma unroll
-          for (int c = i * kEach; c < (i + 1) * kEach && c < kCopies; ++c) copy((kb + 1) & 1, kn, c);
-          if (n == FN - 1 && m + 1 < FM) sc[(m + 1) & 1] = scn * (ROWS ? 1.0f : sbt[0]);
+            for (int n = 0; n < FN; ++n) add(m * FN + n);
+          if (m + 1 < FM) sc[(m + 1) & 1] = scn * (ROWS ? 1.0f : sbt[0]);
           __builtin_amdgcn_sched_barrier(0);
+        } else {
+          // Beside each product the multiply-adds of the third one before it
+          // (whose sums are ready by then), the next row fragment's codes and
+          // the next stage's copies on their way.
+#pragma unroll
+          for (int n = 0; n < FN; ++n) {
+            const int i = m * FN + n;
+            p[i % kHeld] = mfma_e4m3(bf[n], af, f32x4{});
+            __builtin_amdgcn_sched_barrier(0);
+            if (n == 0 && m + 1 < FM) {
+              next = codes(at + 16 * (m + 1) * kRow);
+              scn = sat[16 * (m + 1)];
+            }
+            if (i >= kLag) add(i - kLag);
+#pragma unroll
+            for (int c = i * kEach; c < (i + 1) * kEach && c < kCopies; ++c) copy((kb + 1) & 1, kn, c);
+            if (n == FN - 1 && m + 1 < FM) sc[(m + 1) & 1] = scn * (ROWS ? 1.0f : sbt[0]);
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
       }
+      if (!kWide)
 #pragma unroll
-      for (int i = FM * FN - kLag; i < FM * FN; ++i) add(i);
+        for (int i = FM * FN - kLag; i < FM * FN; ++i) add(i);
       __syncthreads();  // waits for this wave's copies, then for every wave
     }
     store_tile<FM, FN, TN>(reinterpret_cast<OUT*>(lds + wave * kRoom), lane, acc, y, m0, wm * TM, mr, N,
@@ -482,8 +524,8 @@ struct Many {
 
 template <int BM, bool ROWS, typename OUT>
 __global__ __launch_bounds__(512, 2) void matmul_many(
-    const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ b,
-    const float* __restrict__ sb, OUT* __restrict__ y, int64_t M, int64_t N, int64_t K, TileGrid t) {
+    const uint8_t* __restrict__ a, Scales sa, const uint8_t* __restrict__ b, Scales sb,
+    OUT* __restrict__ y, int64_t M, int64_t N, int64_t K, TileGrid t) {
   using T = Many<BM, ROWS, OUT>;
   __shared__ __attribute__((aligned(16))) unsigned char lds[T::kLds];
   int L = blockIdx.x, piece = 0, split = 1;
@@ -502,174 +544,209 @@ __global__ __launch_bounds__(512, 2) void matmul_many(
   const int64_t n0 = static_cast<int64_t>(quad * 8 + rem / gm) * T::BN;
   const int64_t m0 = static_cast<int64_t>(4 * band + rem % gm) * BM + piece * (BM / split);
   if (m0 >= M) return;
-  if (split == 1) T::template run<BM / 32>(lds, a, sa, b, sb, y, M, N, K, m0, n0);
-  else if (split == 2) T::template run<BM / 64>(lds, a, sa, b, sb, y, M, N, K, m0, n0);
-  else T::template run<BM / 128>(lds, a, sa, b, sb, y, M, N, K, m0, n0);
+  constexpr int FM = BM / 32;
+  if (split == 1) T::template run<FM>(lds, a, sa, b, sb, y, M, N, K, m0, n0);
+  if constexpr (FM % 2 == 0)
+    if (split == 2) T::template run<FM / 2>(lds, a, sa, b, sb, y, M, N, K, m0, n0);
+  if constexpr (FM % 4 == 0)
+    if (split == 4) T::template run<FM / 4>(lds, a, sa, b, sb, y, M, N, K, m0, n0);
+}
+
+// Maximum over a row of 16 lanes, in each of them, by data-parallel moves.
+__device__ __forceinline__ float row_max(float v) {
+  auto step = [&](int o) { v = fmaxf(v, __builtin_bit_cast(float, o)); };
+  step(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, false));   // neighbours
+  step(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x4E, 0xF, 0xF, false));   // pairs
+  step(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x141, 0xF, 0xF, false));  // half rows
+  step(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x140, 0xF, 0xF, false));  // the row
+  return v;
 }
 
 // ---- quantisation in both orientations --------------------------------------
-// One workgroup per 128 x 128 tile of v; thread (rg, cg) holds rows 8 rg .. +8
-// and columns 8 cg .. +8.  A scale covers 128 columns of a row and, for the
-// transposed codes, 128 rows of a column (BLOCK: the whole tile, both ways).
-// The transposed codes cross the tile through LDS, so v is read once and both
-// codes leave in whole lines.  Rows and columns past v's end count as zeros.
+// One workgroup per 128 x 128 tile of v; thread (rg, cg) holds rows 4 rg .. +4
+// and columns 8 cg .. +8, packed as they lie in memory.  A scale covers 128
+// columns of a row and, for the transposed codes, 128 rows of a column (BLOCK:
+// the whole tile, both ways).  The transposed codes cross the tile through
+// LDS, so v is read once and both codes leave in whole lines.  Rows and
+// columns past v's end count as zeros.  The scales of rows and columns leave
+// block-major, 128 consecutive words a tile, as the products' copies read
+// them.  4,099 x 5,120 bf16 both ways, 84 MB: 22.5 us (27 with the columns'
+// maxima of the eight waves read by every thread, 38 with the plain division
+// and half the threads).
 template <typename IO, bool BLOCK, bool VEC>
-__global__ __launch_bounds__(256) void quant_2d(const IO* __restrict__ v, int64_t rows,
+__global__ __launch_bounds__(512) void quant_2d(const IO* __restrict__ v, int64_t rows,
                                                 int64_t cols, int64_t ncb, uint8_t* __restrict__ q,
                                                 float* __restrict__ s, uint8_t* __restrict__ qt,
                                                 float* __restrict__ st) {
-  __shared__ __attribute__((aligned(16))) uint2 tile[128][16];
-  __shared__ float sh[4][128];
+  constexpr int P = 4, kWaves = 8;
+  __shared__ __attribute__((aligned(16))) uint32_t tile[128][32];
+  __shared__ __attribute__((aligned(16))) uint32_t top[128];  // columns' maxima (bits of floats >= 0)
+  __shared__ float sh[kWaves];
   const int tid = threadIdx.x, cg = tid % 16, rg = tid / 16, wave = tid / kWave;
+  if (!BLOCK) {
+    if (tid < 128) top[tid] = 0;
+    __syncthreads();
+  }
   const int64_t rb = blockIdx.x / ncb, cb = blockIdx.x % ncb;
   const int64_t nrb = (rows + 127) / 128;
-  const int64_t r0 = rb * 128 + 8 * rg, c0 = cb * 128 + 8 * cg;
-  float x[8][8];
+  const int64_t r0 = rb * 128 + P * rg, c0 = cb * 128 + 8 * cg;
+  constexpr int kWords = sizeof(IO) == 2 ? 1 : 2;
+  u32x4 raw[P][kWords];
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
+  for (int p = 0; p < P; ++p) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[p][j] = 0.0f;
+    for (int i = 0; i < kWords; ++i) raw[p][i] = u32x4{0, 0, 0, 0};
     if (r0 + p >= rows) continue;
     const IO* src = v + (r0 + p) * cols + c0;
     if (VEC) {
-      if (c0 < cols) {
-        if constexpr (sizeof(IO) == 2) {
-          const u32x4 w = ld16(src);
+      if (c0 < cols)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[p][2 * j] = __uint_as_float(w[j] << 16);
-            x[p][2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-          }
-        } else {
-          const u32x4 w0 = ld16(src), w1 = ld16(src + 4);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[p][j] = __uint_as_float(w0[j]);
-            x[p][4 + j] = __uint_as_float(w1[j]);
-          }
-        }
-      }
+        for (int i = 0; i < kWords; ++i) raw[p][i] = ld16(src + i * 4);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (c0 + j < cols) {
-          if constexpr (sizeof(IO) == 2) x[p][j] = bf16_bits_to_f32(src[j]);
-          else x[p][j] = src[j];
+          if constexpr (sizeof(IO) == 2) raw[p][0][j / 2] |= static_cast<uint32_t>(src[j]) << (16 * (j % 2));
+          else raw[p][j / 4][j % 4] = __float_as_uint(src[j]);
         }
     }
   }
-  float rmax[8], cmax[8];
+  auto value = [&](int p, int j) {
+    if constexpr (sizeof(IO) == 2) {
+      const uint32_t w = raw[p][0][j / 2];
+      return __uint_as_float(j % 2 ? w & 0xFFFF0000u : w << 16);
+    } else {
+      return __uint_as_float(raw[p][j / 4][j % 4]);
+    }
+  };
+  float rmax[P], cmax[8];
 #pragma unroll
-  for (int p = 0; p < 8; ++p) rmax[p] = cmax[p] = 0.0f;
+  for (int p = 0; p < P; ++p) rmax[p] = 0.0f;
 #pragma unroll
-  for (int p = 0; p < 8; ++p)
+  for (int j = 0; j < 8; ++j) cmax[j] = 0.0f;
+#pragma unroll
+  for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float m = fabsf(x[p][j]);
+      const float m = fabsf(value(p, j));
       rmax[p] = fmaxf(rmax[p], m);
       cmax[j] = fmaxf(cmax[j], m);
     }
   if (BLOCK) {
-    float m = 0.0f;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) m = fmaxf(m, rmax[p]);
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-    if (tid % kWave == 0) sh[0][wave] = m;
+    float m = fmaxf(fmaxf(rmax[0], rmax[1]), fmaxf(rmax[2], rmax[3]));
+    m = row_max(m);
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    if (tid % kWave == 0) sh[wave] = m;
     __syncthreads();
-    m = fmaxf(fmaxf(sh[0][0], sh[0][1]), fmaxf(sh[0][2], sh[0][3]));
 #pragma unroll
-    for (int p = 0; p < 8; ++p) rmax[p] = cmax[p] = m;
+    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sh[w]);
+#pragma unroll
+    for (int p = 0; p < P; ++p) rmax[p] = m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cmax[j] = m;
   } else {
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
+    for (int p = 0; p < P; ++p) rmax[p] = row_max(rmax[p]);
+    if (qt) {
 #pragma unroll
-      for (int off = 8; off >= 1; off >>= 1) rmax[p] = fmaxf(rmax[p], __shfl_xor(rmax[p], off));
+      for (int j = 0; j < 8; ++j) {
+        cmax[j] = fmaxf(cmax[j], __shfl_xor(cmax[j], 16));
+        cmax[j] = fmaxf(cmax[j], __shfl_xor(cmax[j], 32));
+      }
+      if (tid % kWave < 16)
 #pragma unroll
-      for (int off = 32; off >= 16; off >>= 1) cmax[p] = fmaxf(cmax[p], __shfl_xor(cmax[p], off));
+        for (int j = 0; j < 8; ++j) atomicMax(&top[8 * cg + j], __float_as_uint(cmax[j]));
     }
-    if (tid % kWave < 16)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sh[wave][8 * cg + j] = cmax[j];
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      cmax[j] = fmaxf(fmaxf(sh[0][8 * cg + j], sh[1][8 * cg + j]),
-                      fmaxf(sh[2][8 * cg + j], sh[3][8 * cg + j]));
   }
   if (q) {
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const float sc = e4m3_scale(rmax[p]);
-      const uint32_t lo = e4m3x4(x[p][0] / sc, x[p][1] / sc, x[p][2] / sc, x[p][3] / sc);
-      const uint32_t hi = e4m3x4(x[p][4] / sc, x[p][5] / sc, x[p][6] / sc, x[p][7] / sc);
+    for (int p = 0; p < P; ++p) {
+      const BlockDivisor d(rmax[p]);
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = value(p, j);
+      const uint2 code = d.codes(x);
       if (r0 + p < rows) {
-        *reinterpret_cast<uint2*>(q + (r0 + p) * (ncb * 128) + c0) = make_uint2(lo, hi);
-        if (!BLOCK && cg == 0) s[(r0 + p) * ncb + cb] = sc;
+        *reinterpret_cast<uint2*>(q + (r0 + p) * (ncb * 128) + c0) = code;
+        if (!BLOCK && cg == 0) s[cb * rows + r0 + p] = d.s;
       }
     }
     if (BLOCK && tid == 0) s[rb * ncb + cb] = e4m3_scale(rmax[0]);
   }
   if (qt) {
+    if (!BLOCK) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cmax[j] = __uint_as_float(top[8 * cg + j]);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float sc = e4m3_scale(cmax[j]);
-      const uint32_t lo = e4m3x4(x[0][j] / sc, x[1][j] / sc, x[2][j] / sc, x[3][j] / sc);
-      const uint32_t hi = e4m3x4(x[4][j] / sc, x[5][j] / sc, x[6][j] / sc, x[7][j] / sc);
-      tile[8 * cg + j][rg ^ cg] = make_uint2(lo, hi);  // spread over the banks
-      if (!BLOCK && rg == 0 && c0 + j < cols) st[(c0 + j) * nrb + rb] = sc;
+      const BlockDivisor d(cmax[j]);
+      const float x[P] = {value(0, j), value(1, j), value(2, j), value(3, j)};
+      tile[8 * cg + j][rg ^ (2 * cg)] = d.codes(x);  // spread over the banks
+      if (!BLOCK && rg == 0 && c0 + j < cols) st[rb * cols + c0 + j] = d.s;
     }
     if (BLOCK && tid == 0) st[cb * nrb + rb] = e4m3_scale(cmax[0]);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = tid / 8 + 32 * i, ch = tid % 8, g = c / 8;
+    for (int i = 0; i < 2; ++i) {
+      const int c = tid / 8 + 64 * i, ch = tid % 8, g = c / 8;
       if (cb * 128 + c >= cols) continue;
-      const uint2 lo = tile[c][(2 * ch) ^ g], hi = tile[c][(2 * ch + 1) ^ g];
-      st16(qt + (cb * 128 + c) * (nrb * 128) + rb * 128 + 16 * ch, u32x4{lo.x, lo.y, hi.x, hi.y});
+      const u32x4 w = *reinterpret_cast<const u32x4*>(&tile[c][(4 * ch) ^ ((2 * g) & 28)]);
+      st16(qt + (cb * 128 + c) * (nrb * 128) + rb * 128 + 16 * ch,
+           g % 2 ? u32x4{w[2], w[3], w[0], w[1]} : w);
     }
   }
 }
 
 // The form of a product: the one whose tiles are estimated to take least time,
 // rounds of 256 tiles (one per compute unit) times the time of a tile's
-// 128-deep block.  Microseconds a block, measured at K = 5120 with 160 tiles:
-//   32 x 16 0.09, 32 x 32 0.14, 64 x 16 0.16, 64 x 32 0.24, 64 x 64 0.34,
-//   128 x 64 0.52, 128 x 128 0.85; 256 x 256 1.73, its halves 1.27 and
-//   quarters 1.0 (whole products of 5120 x 5120 by N = 5120: 1 row 8.5 us, 64
-//   rows 12.4, 128 rows 16.7, 256 rows 23.8, 512 rows 37, 1024 rows 54).
-struct Shape {
+// 128-deep block.  Microseconds a block, from products with N = K = 5120 (bf16
+// results: 1 row 8.5 us, 64 rows 12.4, 128 rows 16.7, 256 rows 23, 512 rows 37,
+// 1,024 rows 48, 2,048 rows 61, 8,192 rows 215; binary32 results: 64 rows 15.7,
+// 256 rows 37, 512 rows 61, 8,192 rows 404):
+struct Form {
   int bm, bn;
-  float us;
+  float us, wide;      // bf16 results, binary32 results (a negative time: not built)
+  float half, quarter; // of the 256-column tiles' halves and quarters in the last round
 };
-constexpr Shape kShapes[] = {{32, 16, 0.09f},  {32, 32, 0.14f},  {64, 16, 0.16f},  {64, 32, 0.24f},
-                             {64, 64, 0.34f},  {128, 64, 0.52f}, {128, 128, 0.85f}};
-constexpr int kShapeMany = 7;
+constexpr Form kForms[] = {
+    {32, 16, 0.09f, 0.14f, 0, 0},     {32, 32, 0.14f, 0.22f, 0, 0},
+    {64, 16, 0.16f, 0.24f, 0, 0},     {64, 32, 0.24f, 0.32f, 0, 0},
+    {64, 64, 0.34f, 0.51f, 0, 0},     {128, 64, 0.52f, 0.85f, 0, 0},
+    {128, 128, 0.85f, 1.45f, 0, 0},   {128, 256, -1.0f, 2.1f, 1.5f, 1.2f},
+    {192, 256, 1.52f, -1.0f, 1.2f, 0}, {224, 256, 1.75f, 3.5f, 0, 0},
+    {256, 256, 1.9f, -1.0f, 1.27f, 1.0f}};
+constexpr int kFormTiles = 7;  // the forms before are matmul_tile's
 
-TileGrid tile_grid(int64_t M, int64_t N, int bm) {
+TileGrid tile_grid(int64_t M, int64_t N, const Form& f) {
   TileGrid t;
   t.nt = static_cast<int>(ceil_div(N, 256));
-  t.mt = static_cast<int>(ceil_div(M, bm));
+  t.mt = static_cast<int>(ceil_div(M, f.bm));
   const int64_t tiles = static_cast<int64_t>(t.nt) * t.mt;
   t.full = static_cast<int>(tiles / 256 * 256);
   t.rest = static_cast<int>(tiles - t.full);
   t.split = 1;
-  while (t.split < 4 && t.rest * t.split * 2 <= 256) t.split *= 2;
+  if (f.half > 0 && t.rest * 2 <= 256) t.split = 2;
+  if (f.quarter > 0 && t.rest * 4 <= 256) t.split = 4;
   return t;
 }
 
-int choose_shape(int64_t M, int64_t N) {
+int choose_form(int64_t M, int64_t N, bool wide) {
   int best = 0;
   float least = 0.0f;
-  for (int i = 0; i <= kShapeMany; ++i) {
+  for (int i = 0; i < static_cast<int>(sizeof(kForms) / sizeof(kForms[0])); ++i) {
+    const Form& f = kForms[i];
+    const float each = wide ? f.wide : f.us;
+    if (each < 0) continue;
     float us;
-    if (i < kShapeMany) {
-      const Shape& s = kShapes[i];
-      us = static_cast<float>(ceil_div(ceil_div(M, s.bm) * ceil_div(N, s.bn), 256)) * s.us;
+    if (i < kFormTiles) {
+      us = static_cast<float>(ceil_div(ceil_div(M, f.bm) * ceil_div(N, f.bn), 256)) * each;
     } else {
-      const TileGrid t = tile_grid(M, N, 256);
-      us = static_cast<float>(t.full / 256) * 1.73f;
-      if (t.rest) us += t.split == 1 ? 1.73f : t.split == 2 ? 1.27f : 1.0f;
+      const TileGrid t = tile_grid(M, N, f);
+      us = static_cast<float>(t.full / 256) * each;
+      if (t.rest) us += t.split == 1 ? each : t.split == 2 ? f.half : f.quarter;
     }
     if (i == 0 || us < least) {
       least = us;
@@ -680,23 +757,33 @@ int choose_shape(int64_t M, int64_t N) {
 }
 
 template <bool ROWS, typename OUT>
-void launch_product(int64_t M, int64_t N, int64_t K, const uint8_t* a, const float* sa,
-                    const uint8_t* b, const float* sb, void* y, hipStream_t s) {
+void launch_product(int64_t M, int64_t N, int64_t K, const uint8_t* a, Scales sa,
+                    const uint8_t* b, Scales sb, void* y, hipStream_t s) {
   OUT* out = static_cast<OUT*>(y);
-  const int shape = choose_shape(M, N);
-  if (shape == kShapeMany) {
-    constexpr int BM = sizeof(OUT) == 4 ? 128 : 256;
-    const TileGrid t = tile_grid(M, N, BM);
-    const int grid = t.full + static_cast<int>(ceil_div(t.rest * t.split, 8)) * 8;
-    hipLaunchKernelGGL((matmul_many<BM, ROWS, OUT>), dim3(grid), dim3(512), 0, s, a, sa, b, sb, out,
-                       M, N, K, t);
+  constexpr bool kWide = sizeof(OUT) == 4;
+  const int form = choose_form(M, N, kWide);
+  if (form >= kFormTiles) {
+    const TileGrid t = tile_grid(M, N, kForms[form]);
+    const dim3 grid(static_cast<unsigned>(t.full + ceil_div(t.rest * t.split, 8) * 8));
+#define BEAM_MANY(BM)                                                                           \
+  hipLaunchKernelGGL((matmul_many<BM, ROWS, OUT>), grid, dim3(512), 0, s, a, sa, b, sb, out, M, \
+                     N, K, t)
+    if constexpr (kWide) {
+      if (form == 7) BEAM_MANY(128);
+      else BEAM_MANY(224);
+    } else {
+      if (form == 8) BEAM_MANY(192);
+      else if (form == 9) BEAM_MANY(224);
+      else BEAM_MANY(256);
+    }
+#undef BEAM_MANY
     return;
   }
 #define BEAM_TILE(BM, BN, KS, WM, WN, ST)                                                       \
   hipLaunchKernelGGL((matmul_tile<BM, BN, KS, WM, WN, ST, ROWS, OUT>),                          \
                      dim3(static_cast<unsigned>(ceil_div(N, BN) * ceil_div(M, BM))),            \
                      dim3(64 * KS * WM * WN), 0, s, a, sa, b, sb, out, M, N, K)
-  switch (shape) {
+  switch (form) {
     case 0: BEAM_TILE(32, 16, 8, 1, 1, 3); break;
     case 1: BEAM_TILE(32, 32, 4, 1, 1, 3); break;
     case 2: BEAM_TILE(64, 16, 4, 2, 1, 3); break;
@@ -716,7 +803,7 @@ hipError_t launch_quant_2d(int64_t rows, int64_t cols, int32_t dtype, bool block
   const dim3 grid(static_cast<unsigned>(ceil_div(rows, 128) * ncb));
   const bool vec = cols % 8 == 0;  // every row then starts 16-byte aligned
 #define BEAM_Q3(IO, B, V)                                                                     \
-  hipLaunchKernelGGL((quant_2d<IO, B, V>), grid, dim3(256), 0, stream,                        \
+  hipLaunchKernelGGL((quant_2d<IO, B, V>), grid, dim3(512), 0, stream,                        \
                      static_cast<const IO*>(v), rows, cols, ncb, q, s, qt, st)
 #define BEAM_Q2(IO, B)              \
   do {                              \
@@ -737,14 +824,16 @@ hipError_t launch_quant_2d(int64_t rows, int64_t cols, int32_t dtype, bool block
 }
 
 hipError_t launch_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, const float* sa,
-                              const uint8_t* b, const float* sb, bool rows, int32_t dtype,
-                              void* y, hipStream_t s) {
+                              const int64_t* sa_stride, const uint8_t* b, const float* sb,
+                              const int64_t* sb_stride, bool rows, int32_t dtype, void* y,
+                              hipStream_t s) {
+  const Scales za{sa, sa_stride[0], sa_stride[1]}, zb{sb, sb_stride[0], sb_stride[1]};
   if (dtype == BEAM_BF16) {
-    if (rows) launch_product<true, uint16_t>(M, N, K, a, sa, b, sb, y, s);
-    else launch_product<false, uint16_t>(M, N, K, a, sa, b, sb, y, s);
+    if (rows) launch_product<true, uint16_t>(M, N, K, a, za, b, zb, y, s);
+    else launch_product<false, uint16_t>(M, N, K, a, za, b, zb, y, s);
   } else {
-    if (rows) launch_product<true, float>(M, N, K, a, sa, b, sb, y, s);
-    else launch_product<false, float>(M, N, K, a, sa, b, sb, y, s);
+    if (rows) launch_product<true, float>(M, N, K, a, za, b, zb, y, s);
+    else launch_product<false, float>(M, N, K, a, za, b, zb, y, s);
   }
   return hipGetLastError();
 }

@@ -233,11 +233,9 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
         for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
 #pragma unroll
         for (int off = 8; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-        const float sc = e4m3_scale(m);
-        const uint32_t lo = e4m3x4(x[0] / sc, x[1] / sc, x[2] / sc, x[3] / sc);
-        const uint32_t hi = e4m3x4(x[4] / sc, x[5] / sc, x[6] / sc, x[7] / sc);
-        *reinterpret_cast<uint2*>(a.xq + base + c) = make_uint2(lo, hi);
-        if (c % 128 == 0) a.xs[(base + c) / 128] = sc;
+        const BlockDivisor d(m);
+        *reinterpret_cast<uint2*>(a.xq + base + c) = d.codes(x);
+        if (c % 128 == 0) a.xs[(base + c) / 128] = d.s;
       }
     }
   }

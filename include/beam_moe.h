@@ -309,10 +309,14 @@ int beam_moe_forward_residual(const beam_moe_desc* desc, int64_t T, const void* 
  * products and sums are binary32 throughout; with BEAM_BF16 the e4m3 matrix
  * instructions sum, which cut products at 2^-13 of the largest of eight
  * neighbours (1.5e-5 of a result of normal data, against bf16's 2e-3).
- *   a   device [M, K] uint8 e4m3fn codes   sa  device [M, K/128] fp32
+ *   a   device [M, K] uint8 e4m3fn codes
+ *   sa  device fp32: the scale of row m, block kb at sa[m * sa_row + kb *
+ *       sa_block] (beam_moe_quant_e4m3 writes rows: K/128 and 1;
+ *       beam_moe_quant_e4m3_2d blocks: 1 and M)
  *   b   device [N, K] uint8 e4m3fn codes (weights out x in)
- *   sb  device fp32: [ceil(N/128), K/128] with b_rows 0 (a scale for each
- *       128 x 128 block), [N, K/128] with b_rows 1 (for each row of b)
+ *   sb  device fp32: with b_rows 0 a scale for each 128 x 128 block, that of
+ *       rows 128 i .. at sb[i * sb_row + kb * sb_block]; with b_rows 1 one for
+ *       each row of b, as sa
  *   y   device [M, N] dtype (BEAM_F32 or BEAM_BF16)
  * K % 128 == 0, K <= 2^22, M, N < 2^23 - 127, M * N <= 2^38
  * (BEAM_ERR_UNSUPPORTED otherwise).
@@ -323,8 +327,9 @@ int beam_moe_forward_residual(const beam_moe_desc* desc, int64_t T, const void* 
  *   dx = dy w    rows of dy, blocks of w (transposed)
  *   dw = dy^T x  columns of dy, columns of x (both transposed, b_rows 1) */
 int beam_moe_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, const float* sa,
-                         const uint8_t* b, const float* sb, int32_t b_rows, int32_t dtype,
-                         void* y, void* stream);
+                         int64_t sa_row, int64_t sa_block, const uint8_t* b, const float* sb,
+                         int64_t sb_row, int64_t sb_block, int32_t b_rows, int32_t dtype, void* y,
+                         void* stream);
 
 /* e4m3 quantisation of a matrix for products along its columns and along its
  * rows, in one reading of it (scale = amax / 448 in binary32, 1 where that is
@@ -332,11 +337,12 @@ int beam_moe_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, cons
  * ceil(rows/128) and C = 128 ceil(cols/128), and zeros past the end of v:
  *   v   device [rows, cols] dtype (BEAM_F32 or BEAM_BF16)
  *   q   device [rows, C] uint8 codes, or NULL
- *   s   device fp32, with q: [rows, C/128] with block 0 (a scale for 128
- *       columns of a row), [R/128, C/128] with block 1 (for 128 x 128 values)
+ *   s   device fp32, with q: [C/128, rows] with block 0 (a scale for 128
+ *       columns of a row, block-major), [R/128, C/128] with block 1 (for 128 x
+ *       128 values)
  *   qt  device [cols, R] uint8 codes of v transposed, or NULL (not both)
- *   st  device fp32, with qt: [cols, R/128] with block 0 (a scale for 128 rows
- *       of a column), [C/128, R/128] with block 1
+ *   st  device fp32, with qt: [R/128, cols] with block 0 (a scale for 128 rows
+ *       of a column, block-major), [C/128, R/128] with block 1
  * No workspace. */
 int beam_moe_quant_e4m3_2d(int64_t rows, int64_t cols, int32_t dtype, int32_t block,
                            const void* v, uint8_t* q, float* s, uint8_t* qt, float* st,

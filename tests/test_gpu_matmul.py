@@ -114,6 +114,21 @@ def test_empty():
         assert y.shape == (m, n) and (y == 0).all()
 
 
+def test_strided_scales():
+    # scales row-major, block-major and as a column slice of something wider
+    dev = device()
+    for M in (5, 100, 700):
+        for rows in (False, True):
+            a, sa = operand(M, 640, 1, 5, dev)
+            b, sb = operand(390, 640, 1 if rows else 128, 6, dev)
+            y = gl.matmul_e4m3(a, sa, b, sb)
+            check(y, a, sa, b, sb, rows)
+            wide = torch.full((M, 12), 9.0, device=dev)
+            wide[:, ::2][:, :5] = sa
+            for va in (sa.t().contiguous().t(), wide[:, ::2][:, :5]):
+                assert torch.equal(gl.matmul_e4m3(a, va, b, sb.t().contiguous().t()), y)
+
+
 def test_rows_do_not_mix():
     # a row's result does not depend on the rows beside it, within one form
     dev = device()
@@ -204,6 +219,31 @@ def test_quantiser_bit_exact(R, C, dtype):
     assert only[0] is None and torch.equal(only[2].cpu(), wt)
     only = gl.quant_e4m3_2d(dv, block=True, transposed=False)
     assert only[3] is None and torch.equal(only[0].cpu(), wq[:R])
+
+
+def test_quantiser_at_the_borders_between_codes():
+    # values on and beside the midpoints of neighbouring codes times the scale,
+    # for scales of every size and awkward significands: the division decides
+    g = torch.Generator().manual_seed(0)
+    codes = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    mid = (codes[:-1] + codes[1:]) / 2                      # 126 midpoints
+    rows = []
+    for i in range(1000):
+        bits = int(torch.randint(0, 1 << 23, (1,), generator=g)) if i % 3 else (0x7FFFFF, 0, 1, 0x7FFFFE)[i // 3 % 4]
+        exp = int(torch.randint(-140, 117, (1,), generator=g))
+        amax = 2.0 ** exp * (1 + bits / 2 ** 23)
+        s = (torch.tensor(amax, dtype=torch.float64) / 448).float()
+        v = torch.zeros(128)
+        v[:126] = mid * s
+        v[:126] = torch.nextafter(v[:126], torch.full((126,), [0.0, float("inf"), 1e-30][i % 3]))
+        v[127] = amax
+        rows.append(v)
+    v = torch.stack(rows).clamp(-3e38, 3e38)
+    q, s, qt, st = gl.quant_e4m3_2d(v.to(device()))
+    wq, ws = ref.quantise(v, 1, 128)
+    assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu(), wq)
+    q, s, qt, st = gl.quant_e4m3_2d(v.t().contiguous().to(device()))
+    assert torch.equal(st.cpu(), ws) and torch.equal(qt.cpu(), wq)
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 128, 128), (300, 200, 520), (130, 1000, 96), (513, 257, 640)])

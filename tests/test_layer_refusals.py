@@ -114,7 +114,8 @@ def test_norm_binding_checks():
 
 
 def _mm(**kw):
-    a = dict(M=4, N=8, K=256, a=GOOD, sa=GOOD, b=GOOD, sb=GOOD, rows=0, dtype=gl.BF16, y=GOOD)
+    a = dict(M=4, N=8, K=256, a=GOOD, sa=GOOD, sa_r=2, sa_k=1, b=GOOD, sb=GOOD, sb_r=2, sb_k=1, rows=0,
+             dtype=gl.BF16, y=GOOD)
     a.update(kw)
     return gl.lib().beam_moe_matmul_e4m3(*a.values(), None)
 
@@ -126,7 +127,8 @@ def _mm(**kw):
     (dict(dtype=gl.FP8_E4M3), gl.ERR_INVALID_ARG), (dict(a=None), gl.ERR_INVALID_ARG),
     (dict(sa=None), gl.ERR_INVALID_ARG), (dict(b=None), gl.ERR_INVALID_ARG), (dict(sb=None), gl.ERR_INVALID_ARG),
     (dict(y=None), gl.ERR_INVALID_ARG), (dict(a=BAD), gl.ERR_INVALID_ARG), (dict(sb=BAD), gl.ERR_INVALID_ARG),
-    (dict(y=BAD), gl.ERR_INVALID_ARG), (dict(M=0, a=None, sa=None, y=None), gl.OK), (dict(N=0, b=None), gl.OK),
+    (dict(y=BAD), gl.ERR_INVALID_ARG), (dict(sa_r=-1), gl.ERR_INVALID_ARG), (dict(sb_k=-4), gl.ERR_INVALID_ARG),
+    (dict(M=0, a=None, sa=None, y=None), gl.OK), (dict(N=0, b=None), gl.OK),
 ])
 def test_matmul_refuses(kw, status):
     assert _mm(**kw) == status
