@@ -163,6 +163,15 @@ def _p(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _addr(t: Optional[torch.Tensor]):
+    """As _p, but a plain integer (ctypes converts it)."""
+    if t is None:
+        return None
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _p(t)  # raises
+
+
 def _torch_stream(stream, device):
     return stream if stream is not None else torch.cuda.current_stream(device)
 
@@ -249,9 +258,9 @@ def _arg(name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple,
 def _empty(stream, device, dtype: torch.dtype, *shape) -> torch.Tensor:
     """An output, allocated on the call's stream."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 def _run(fn, what: str, stream, dev: int, tensors, *args):
@@ -292,9 +301,11 @@ def route(desc: Desc, x: Optional[torch.Tensor], w_router: Optional[torch.Tensor
         logits = _empty(stream, dev, torch.float32, T, desc.n_experts)
     # routing from given logits uses no scratch memory
     buf, n = (None, 0) if lin else _ws(desc, T, workspace, dev, stream)
-    _check(lib().beam_moe_route(ctypes.byref(desc), T, _p(x), _p(w_router),
-                                _p(bias), _p(logits), _p(idx), _p(w), _p(buf),
-                                n, _stream(stream, dev)), "beam_moe_route")
+    raw = (torch._C._cuda_getCurrentRawStream(ref.get_device()) if stream is None
+           else stream.cuda_stream)
+    _check(lib().beam_moe_route(ctypes.byref(desc), T, _addr(x), _addr(w_router), _addr(bias),
+                                _addr(logits), idx.data_ptr(), w.data_ptr(), _addr(buf), n, raw),
+           "beam_moe_route")
     return idx, w, logits
 
 
@@ -309,9 +320,11 @@ def route_backward(desc: Desc, logits: torch.Tensor, topk_idx: torch.Tensor,
     pw = _arg("d_topk_w", d_topk_w, dev, torch.float32, (T, K))
     if out is None:
         out = _empty(stream, logits.device, torch.float32, T, E)
+        po = out.data_ptr()
+    else:
+        po = _arg("out", out, dev, torch.float32, (T, E))
     _run(lib().beam_moe_route_backward, "beam_moe_route_backward", stream, dev,
-         (logits, topk_idx, d_topk_w, out), ctypes.byref(desc), T, pl, pi, pw,
-         _arg("out", out, dev, torch.float32, (T, E)))
+         (logits, topk_idx, d_topk_w, out), ctypes.byref(desc), T, pl, pi, pw, po)
     return out
 
 
@@ -452,9 +465,12 @@ def matmul_e4m3(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch.
     psb = _arg("s_b", s_b, dev, torch.float32, (N if rows else (N + 127) // 128, K // 128), True)
     if out is None:
         out = _empty(stream, a.device, dtype, M, N)
+        py = out.data_ptr()
+    else:
+        py = _arg("out", out, dev, dtype, (M, N))
     _run(lib().beam_moe_matmul_e4m3, "beam_moe_matmul_e4m3", stream, dev, (a, s_a, b, s_b, out),
          M, N, K, pa, psa, *s_a.stride(), pb, psb, *s_b.stride(), 1 if rows else 0, BF16 if dtype is torch.bfloat16 else F32,
-         _arg("out", out, dev, dtype, (M, N)))
+         py)
     return out
 
 
@@ -511,7 +527,9 @@ def _norm_residual(residual, o, post_weight, gate, pre_weight, eps, alpha, beta,
     else:
         if residual_out is None:
             residual_out = _empty(stream, device, torch.float32, T, H)
-        p_out = _arg("residual_out", residual_out, dev, torch.float32, (T, H))
+            p_out = residual_out.data_ptr()
+        else:
+            p_out = _arg("residual_out", residual_out, dev, torch.float32, (T, H))
     if pp is not None and want_x:
         x = _empty(stream, device, dtype, T, H)
         px = x.data_ptr()
