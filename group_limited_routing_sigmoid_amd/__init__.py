@@ -221,6 +221,12 @@ _default_ws = {}
 def _scratch(n: int, workspace: Optional[Workspace], device, stream=None):
     s = _torch_stream(stream, device)
     if workspace is None:
+        # A call that is being captured takes memory of its graph instead:
+        # graphs are captured on one stream and replayed on any.
+        with _alloc_on(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+        if capturing:
+            return Workspace(device).get(n, s)
         key = (str(device), s.cuda_stream)
         workspace = _default_ws.setdefault(key, Workspace(device))
     return workspace.get(n, s)
@@ -294,18 +300,18 @@ def route(desc: Desc, x: Optional[torch.Tensor], w_router: Optional[torch.Tensor
     the scores and the weights."""
     lin = bool(desc.flags & ROUTE_LOGITS_IN)
     ref = logits if lin else x
-    T, dev = ref.shape[0], ref.device
-    idx = _empty(stream, dev, torch.int32, T, desc.top_k)
-    w = _empty(stream, dev, torch.float32, T, desc.top_k)
+    T, E, device, dev = ref.shape[0], desc.n_experts, ref.device, ref.get_device()
+    px, pr = (None, None) if lin else (_addr(x), _addr(w_router))
+    pb = None if bias is None else _arg("bias", bias, dev, torch.float32, (E,))
     if logits is None:
-        logits = _empty(stream, dev, torch.float32, T, desc.n_experts)
+        logits = _empty(stream, device, torch.float32, T, E)
+    pl = _arg("logits", logits, dev, torch.float32, (T, E))
+    idx = _empty(stream, device, torch.int32, T, desc.top_k)
+    w = _empty(stream, device, torch.float32, T, desc.top_k)
     # routing from given logits uses no scratch memory
-    buf, n = (None, 0) if lin else _ws(desc, T, workspace, dev, stream)
-    raw = (torch._C._cuda_getCurrentRawStream(ref.get_device()) if stream is None
-           else stream.cuda_stream)
-    _check(lib().beam_moe_route(ctypes.byref(desc), T, _addr(x), _addr(w_router), _addr(bias),
-                                _addr(logits), idx.data_ptr(), w.data_ptr(), _addr(buf), n, raw),
-           "beam_moe_route")
+    buf, n = (None, 0) if lin else _ws(desc, T, workspace, device, stream)
+    _run(lib().beam_moe_route, "beam_moe_route", stream, dev, (x, w_router, bias, logits, idx, w),
+         ctypes.byref(desc), T, px, pr, pb, pl, idx.data_ptr(), w.data_ptr(), _addr(buf), n)
     return idx, w, logits
 
 
@@ -588,15 +594,17 @@ def norm_residual_backward(residual_out: torch.Tensor,
                            workspace: Optional[Workspace] = None, stream=None) -> dict:
     """beam_moe_norm_residual_backward.  residual_out is the forward's r' (its
     residual without o); d_residual_out and d_x are the gradients of r' and x
-    (None for zero, not both).  Returns a dict: d_residual [T,H] fp32; with o
+    (None for zero, not both; d_x is needed without o).  Returns a dict: d_residual [T,H] fp32; with o
     d_o and d_post_weight, with gate d_gate, with d_x d_pre_weight."""
+    if d_residual_out is None and d_x is None:
+        raise ValueError("one of d_residual_out and d_x is needed")
+    if d_x is None and o is None:
+        raise ValueError("without o there is only the gradient of x: d_x is needed")
+    if d_x is not None and pre_weight is None:
+        raise ValueError("d_x needs the pre_weight")
     T, H, dev, dtype, po, pw, pg, cols, pp = _norm_inputs(
         residual_out, o, post_weight, gate, pre_weight,
         d_x.dtype if o is None and d_x is not None else None)
-    if d_residual_out is None and d_x is None:
-        raise ValueError("one of d_residual_out and d_x is needed")
-    if d_x is not None and pre_weight is None:
-        raise ValueError("d_x needs the pre_weight")
     device, f32 = residual_out.device, torch.float32
     pr = _arg("residual_out", residual_out, dev, f32, (T, H))
     p_dr = None if d_residual_out is None else _arg("d_residual_out", d_residual_out, dev, f32, (T, H))

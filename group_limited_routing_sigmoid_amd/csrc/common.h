@@ -140,7 +140,11 @@ struct BlockDivisor {
       return static_cast<uint32_t>(
           __builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[2]), quotient(v[3]), lo, true));
     }
-    return e4m3x4(v[0] / s, v[1] / s, v[2] / s, v[3] / s);
+    // a NaN (also an infinity over the scale it makes) stays one
+    auto code = [&](float x) { return x == x ? sat448(x) : x; };
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(code(v[0] / s), code(v[1] / s), 0, false);
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_cvt_pk_fp8_f32(code(v[2] / s), code(v[3] / s), lo, true));
   }
   __device__ __forceinline__ uint2 codes(const float (&v)[8]) const {
     const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};

@@ -161,6 +161,7 @@ struct NormGradArgs {
 };
 // Workgroups of the backward pass, each with its share of the weights' gradients.
 int norm_grad_groups(int64_t T);
+int64_t norm_max_tokens(int H);  // a launch holds fewer than 2^32 threads
 constexpr int kNormMaxH = 16384;  // 1024 threads of 16 columns
 hipError_t launch_norm_residual(const NormArgs& a, int64_t T, int32_t dtype, hipStream_t s);
 hipError_t launch_norm_residual_backward(const NormGradArgs& a, int32_t dtype, float* d_pre,
@@ -170,6 +171,7 @@ hipError_t launch_quant_2d(int64_t rows, int64_t cols, int32_t dtype, bool block
                            uint8_t* q, float* s, uint8_t* qt, float* st, hipStream_t stream);
 // Byte offsets inside a tile of 256 rows are 32-bit; tiles are counted in 31.
 constexpr int64_t kMatmulMaxK = 1 << 22, kMatmulMaxRows = (1 << 23) - 128;
+constexpr int64_t kQuantMaxTiles = (int64_t{1} << 23) - 1;  // of 512 threads, under 2^32 in all
 constexpr int64_t kMatmulMaxOut = int64_t{1} << 38;
 hipError_t launch_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, const float* sa,
                               const int64_t* sa_stride, const uint8_t* b, const float* sb,

@@ -14,7 +14,7 @@ int check_norm(int64_t T, int64_t H, int32_t dtype, float eps, float alpha, floa
   if (T < 0 || H < 1 || (dtype != BEAM_F32 && dtype != BEAM_BF16)) return BEAM_ERR_INVALID_ARG;
   if (!(eps > 0.0f) || !isfinite(eps) || !isfinite(alpha) || !isfinite(beta))
     return BEAM_ERR_INVALID_ARG;
-  if (H > kNormMaxH || T > 0x7FFFFFFF) return BEAM_ERR_UNSUPPORTED;
+  if (H > kNormMaxH || T > norm_max_tokens(static_cast<int>(H))) return BEAM_ERR_UNSUPPORTED;
   return BEAM_OK;
 }
 
@@ -67,7 +67,7 @@ int beam_moe_norm_residual(int64_t T, int64_t H, int32_t dtype, const void* o,
 
 int beam_moe_norm_residual_workspace_bytes(int64_t T, int64_t H, size_t* bytes) {
   if (!bytes || T < 0 || H < 1) return BEAM_ERR_INVALID_ARG;
-  if (H > kNormMaxH || T > 0x7FFFFFFF) return BEAM_ERR_UNSUPPORTED;
+  if (H > kNormMaxH || T > norm_max_tokens(static_cast<int>(H))) return BEAM_ERR_UNSUPPORTED;
   *bytes = static_cast<size_t>(norm_grad_groups(T)) * 2 * static_cast<size_t>(H) * sizeof(float);
   return BEAM_OK;
 }
@@ -83,9 +83,9 @@ int beam_moe_norm_residual_backward(int64_t T, int64_t H, int32_t dtype, const v
   int st = check_norm(T, H, dtype, eps, alpha, beta);
   if (st != BEAM_OK) return st;
   if (!gate_ok(T, o, gate, gate_cols, H)) return BEAM_ERR_INVALID_ARG;
-
-  if (T > 0 && !d_x && !d_residual_out) return BEAM_ERR_INVALID_ARG;
   if (T > 0) {
+    // without a block output only x has a gradient of its own
+    if (!d_x && (!d_residual_out || !o)) return BEAM_ERR_INVALID_ARG;
     if (!residual_out || !d_residual) return BEAM_ERR_INVALID_ARG;
     if (d_x && (!pre_weight || !d_pre_weight)) return BEAM_ERR_INVALID_ARG;
     if (o && (!post_weight || !d_o || !d_post_weight)) return BEAM_ERR_INVALID_ARG;
@@ -132,7 +132,7 @@ int beam_moe_quant_e4m3_2d(int64_t rows, int64_t cols, int32_t dtype, int32_t bl
       (block != 0 && block != 1))
     return BEAM_ERR_INVALID_ARG;
   if (rows > 0x7FFFFFFF || cols > 0x7FFFFFFF ||
-      ceil_div(rows, 128) * ceil_div(cols, 128) > 0x7FFFFFFF)
+      ceil_div(rows, 128) * ceil_div(cols, 128) > kQuantMaxTiles)
     return BEAM_ERR_UNSUPPORTED;
   if (rows == 0 || cols == 0) return BEAM_OK;
   if (!v || (!q && !qt) || !q != !s || !qt != !st) return BEAM_ERR_INVALID_ARG;

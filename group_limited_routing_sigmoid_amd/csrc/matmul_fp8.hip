@@ -77,9 +77,6 @@ __device__ __forceinline__ i32x8 frag(const unsigned char* tile, int row0, int l
                (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(uint16_t* p, float v) { *p = f32_to_bf16_bits(v); }
-
 // As dma16, from a buffer at byte offset voff + soff (soff uniform).
 __device__ __forceinline__ void buf_dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, void* lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff,

@@ -453,6 +453,8 @@ RowShape row_shape(int H, bool pairs) {
 
 }  // namespace
 
+int64_t norm_max_tokens(int H) { return 0xFFFFFFFF / row_shape(H, false).threads; }
+
 int norm_grad_groups(int64_t T) { return static_cast<int>(T < 512 ? T : 512); }
 
 #define BEAM_NORM_SHAPES(RUN)                            \

@@ -445,7 +445,7 @@ __global__ __launch_bounds__(256) void router_select(
   }
 
   // 4. top-K of the eligible experts by biased score, rank order: the largest
-  // key (0: not a candidate) over the wave, then the lowest lane holding it
+  // key (0: not a candidate, one whose score is a NaN of all ones made 1) over the wave, then the lowest lane holding it
   // and the lowest of its experts, as lanes hold consecutive experts.
   // (On 64-bit keys of score and index every step of the maximum took six
   // instructions for one: 96 us for 52,001 tokens of 256 experts.)
@@ -454,7 +454,7 @@ __global__ __launch_bounds__(256) void router_select(
   for (int j = 0; j < EPL; ++j) {
     const int e = lane * EPL + j;
     const int g = SEG ? lane >> lg : e / gs;
-    key[j] = (e < E && ((keep >> g) & 1)) ? ordered(u[j]) : 0;
+    key[j] = (e < E && ((keep >> g) & 1)) ? max(ordered(u[j]), 1u) : 0;
   }
   // Up to four experts a lane are first sorted (larger key first, then lower
   // index: stable), so that a choice only looks at and shifts the heads.

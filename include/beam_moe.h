@@ -320,7 +320,8 @@ int beam_moe_forward_residual(const beam_moe_desc* desc, int64_t T, const void* 
  *   y   device [M, N] dtype (BEAM_F32 or BEAM_BF16)
  * K % 128 == 0, K <= 2^22, M, N < 2^23 - 127, M * N <= 2^38
  * (BEAM_ERR_UNSUPPORTED otherwise).
- * K == 0 gives zeros.  NaN codes (0x7F, 0xFF) are outside the contract.
+ * K == 0 gives zeros.  A NaN code (0x7F, 0xFF) makes its row's or column's
+ * results NaN.
  * A linear layer's training step is three of them on what
  * beam_moe_quant_e4m3_2d makes of x [M,K], dy [M,N] and w [N,K]:
  *   y = x w^T    rows of x, blocks of w (straight)
@@ -343,7 +344,9 @@ int beam_moe_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, cons
  *   qt  device [cols, R] uint8 codes of v transposed, or NULL (not both)
  *   st  device fp32, with qt: [R/128, cols] with block 0 (a scale for 128 rows
  *       of a column, block-major), [C/128, R/128] with block 1
- * No workspace. */
+ * A NaN or an infinity makes codes or a scale that give NaN in every product
+ * its block is part of.  At most 2^23 - 1 tiles of 128 x 128
+ * (BEAM_ERR_UNSUPPORTED otherwise).  No workspace. */
 int beam_moe_quant_e4m3_2d(int64_t rows, int64_t cols, int32_t dtype, int32_t block,
                            const void* v, uint8_t* q, float* s, uint8_t* qt, float* st,
                            void* stream);
@@ -371,7 +374,8 @@ int beam_moe_quant_e4m3_2d(int64_t rows, int64_t cols, int32_t dtype, int32_t bl
  *                 beam_moe_quant_e4m3, from x before any rounding
  *   x_scales      device [T, H/128] fp32, with x_codes
  * dtype BEAM_F32 or BEAM_BF16; 1 <= H <= 16384, with x_codes H % 128 == 0
- * (BEAM_ERR_UNSUPPORTED otherwise); eps > 0, alpha and beta finite.  A token's
+ * (BEAM_ERR_UNSUPPORTED otherwise, and for more tokens than a launch holds:
+ * at least 4,194,303, 67 million at H = 128); eps > 0, alpha and beta finite.  A token's
  * sums of squares must be finite in binary32.  With H % 8 == 0 the rows are
  * read 16 bytes at a time, otherwise value by value.  No workspace. */
 int beam_moe_norm_residual(int64_t T, int64_t H, int32_t dtype, const void* o,
@@ -388,8 +392,8 @@ int beam_moe_norm_residual_workspace_bytes(int64_t T, int64_t H, size_t* bytes);
  *                    NULL)
  *   d_residual_out   device [T, H] fp32: gradient of r' from later steps, or
  *                    NULL for zero
- *   d_x              device [T, H] dtype: gradient of x, or NULL (pre_weight
- *                    and d_pre_weight are then not used)
+ *   d_x              device [T, H] dtype: gradient of x, or NULL with o
+ *                    (pre_weight and d_pre_weight are then not used)
  *   d_residual       device [T, H] fp32: output; may be d_residual_out itself
  *   d_o              device [T, H] dtype: output, with o
  *   d_gate           device [T, gate_cols] dtype: output, with gate

@@ -163,3 +163,29 @@ def test_matmul_binding_checks():
         gl.matmul_e4m3(a[0], s, a, s)
     with pytest.raises(ValueError, match="GPU"):
         gl.quant_e4m3_2d(torch.zeros(2, 3))
+
+
+def test_gradient_of_nothing_is_refused():
+    # without a block output and without x's gradient no kernel has work
+    assert _norm_grad(o=None, post=None, gate=None, cols=0, d_x=None, pre=None) == gl.ERR_INVALID_ARG
+    assert _norm_grad(o=None, post=None, gate=None, cols=0, d_x=None) == gl.ERR_INVALID_ARG
+    f = torch.zeros(2, 8)
+    with pytest.raises(ValueError, match="d_x is needed"):
+        gl.norm_residual_backward(f, d_residual_out=f, pre_weight=torch.zeros(8))
+
+
+@pytest.mark.parametrize("H,threads", [(1, 64), (128, 64), (5120, 640), (16384, 1024), (16383, 1024), (4099, 320)])
+def test_more_tokens_than_a_launch_holds(H, threads):
+    # fewer than 2^32 threads a launch
+    most = (2 ** 32 - 1) // threads
+    n = ctypes.c_size_t()
+    fn = gl.lib().beam_moe_norm_residual_workspace_bytes
+    assert fn(most, H, ctypes.byref(n)) == gl.OK and n.value == 512 * 2 * H * 4
+    assert fn(most + 1, H, ctypes.byref(n)) == gl.ERR_UNSUPPORTED
+    assert _norm(T=most + 1, H=H, cols=1) == gl.ERR_UNSUPPORTED
+    assert _norm_grad(T=most + 1, H=H) == gl.ERR_UNSUPPORTED
+
+
+def test_more_tiles_than_a_launch_holds():
+    assert _q2(rows=128 * 2 ** 23, cols=1) == gl.ERR_UNSUPPORTED
+    assert _q2(rows=2 ** 20, cols=128 * 2 ** 10) == gl.ERR_UNSUPPORTED
