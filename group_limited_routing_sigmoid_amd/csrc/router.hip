@@ -203,24 +203,24 @@ __device__ __forceinline__ float sigmoid32(float l) {
 // key); +0 and -0 map to the same key after canonicalisation.
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 
 constexpr int kSelWaves = 4;
 constexpr int kMaxE = 1024;
 constexpr int kMaxKs = 16;   // the plan splits the router's reduction at most 16 ways
-constexpr int kMaxG = 64;
+constexpr int kMaxK = 16;
 
 // ---- wave-wide helpers --------------------------------------------------
 // Reductions over the wave in data-parallel moves: swap neighbours, swap
 // pairs (quad permutations), mirror the half rows, mirror the row; every lane
-// then holds its row of 16's result, and the rows meet in the last lane or
-// are read out lane by lane.  All need every lane active.
+// then holds its row of 16's result, and the rows meet in the last lane.  All
+// need every lane active.
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return static_cast<uint32_t>(
-      __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, false));
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, true));
 }
 
 // Maximum over the wave, returned uniform.
@@ -244,8 +244,9 @@ __device__ __forceinline__ float wave_max_f32(float v) {
   step(dpp<0x4E>(__float_as_uint(v)));
   step(dpp<0x141>(__float_as_uint(v)));
   step(dpp<0x140>(__float_as_uint(v)));
-  return fmaxf(fmaxf(readlane_f(v, 0), readlane_f(v, 16)),
-               fmaxf(readlane_f(v, 32), readlane_f(v, 48)));
+  step(dpp<0x142>(__float_as_uint(v)));
+  step(dpp<0x143>(__float_as_uint(v)));
+  return readlane_f(v, 63);
 }
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
@@ -259,42 +260,49 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
   move(std::integral_constant<int, 0x4E>{});
   move(std::integral_constant<int, 0x141>{});
   move(std::integral_constant<int, 0x140>{});
-  auto row = [&](int l) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), l);
-    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), l);
-    return __builtin_bit_cast(double, static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32));
-  };
-  return (row(0) + row(16)) + (row(32) + row(48));
+  move(std::integral_constant<int, 0x142>{});
+  move(std::integral_constant<int, 0x143>{});
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), 63);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), 63);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32));
 }
 
 // Softmax scores of a token, one wave: s_e = e^(l_e - m) / sum_j e^(l_j - m)
 // with m the largest logit, the exponentials, their sum and its reciprocal
-// (one division a token: by itself a third of the scores' time) in binary64,
-// rounded once to binary32 (the selection compares these values,
-// so they are held to the rounding of the exact softmax, as the sigmoids
-// are).  Exponents below -105 give 0: such a score is below half the smallest
-// binary32 value, and 1024 of them are below the sum's last bit.  A row
-// whose logits are all -infinity has m = -infinity, every comparison false
-// and the scores 0.  Needs every lane active.
+// (one a token) in binary64, rounded once to binary32 (the selection compares
+// these values, so they are held to the rounding of the exact softmax, as the
+// sigmoids are).  Exponents below -105 give 0: such a score is below half the
+// smallest binary32 value, and 1024 of them are below the sum's last bit.  A
+// row whose logits are all -infinity has m = -infinity, every comparison false
+// and the scores 0; a NaN or +infinity makes every score of its row NaN.
+// Needs every lane active; l of places past the last expert is -infinity.
 template <int EPL>
-__device__ __forceinline__ void softmax32(const float (&l)[EPL], int lane, int E, float (&s)[EPL]) {
-  float m = -__builtin_huge_valf();
+__device__ __forceinline__ void softmax32(const float (&l)[EPL], float (&s)[EPL]) {
+  float m = l[0];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j)
-    if (lane * EPL + j < E) m = fmaxf(m, l[j]);
+  for (int j = 1; j < EPL; ++j) m = fmaxf(m, l[j]);
   m = wave_max_f32(m);
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) bad |= !(l[j] <= 3.402823466e38f);
   double ez[EPL], sum = 0.0;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     // no branch, so that the exponentials of a lane overlap
     const double z = static_cast<double>(l[j]) - static_cast<double>(m);
     const double v = exp64(__builtin_fmax(z, -105.0));
-    ez[j] = (lane * EPL + j < E && z > -105.0) ? v : 0.0;
+    ez[j] = z > -105.0 ? v : 0.0;
     sum += ez[j];
   }
   sum = wave_sum_f64(sum);
-  const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+  // 1 / sum within 2^-52 by two steps from the hardware's approximation (sum
+  // lies between 1 and 1024)
+  double inv = __builtin_amdgcn_rcp(sum);
+  inv = __builtin_fma(__builtin_fma(-sum, inv, 1.0), inv, inv);
+  inv = __builtin_fma(__builtin_fma(-sum, inv, 1.0), inv, inv);
+  if (sum == 0.0) inv = 0.0;
+  if (__ballot(bad)) inv = __builtin_nan("");
 #pragma unroll
   for (int j = 0; j < EPL; ++j) s[j] = static_cast<float>(ez[j] * inv);
 }
@@ -369,19 +377,19 @@ __global__ __launch_bounds__(256) void router_select(
 #pragma unroll
     for (int z = 1; z < KS; ++z)
       if (z < ks) l = l + pz[j][z];
-    if (SM) lv[j] = l;
+    if (SM) lv[j] = e < E ? l : ninf;
     else sv[j] = sigmoid32(l);
     if (valid && e < E && logits_out) logits_out[t * E + e] = l;
   }
-  if constexpr (SM) softmax32<EPL>(lv, lane, E, sv);
+  if constexpr (SM) softmax32<EPL>(lv, sv);
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) u[j] = lane * EPL + j < E ? sv[j] + bz[j] : ninf;
+  for (int j = 0; j < EPL; ++j) u[j] = sv[j] + bz[j];  // past E: no group, no key
 
   // 2. group scores: sum of the topn (1 or 2) largest biased scores (a
   // repeated value counts twice).  gsc ends in lane g for group g.  Not
   // needed where every group is kept.
   float gsc = ninf;
-  uint64_t keep = ~uint64_t{0};
+  uint64_t keep = ~uint64_t{0} >> (64 - G);
   const bool limited = TG < G;
   if (SEG && limited) {
     float t1 = ninf, t2 = ninf;
@@ -444,82 +452,119 @@ __global__ __launch_bounds__(256) void router_select(
     keep = __ballot(lane < G && rank < TG);
   }
 
-  // 4. top-K of the eligible experts by biased score, rank order: the largest
-  // key (0: not a candidate, one whose score is a NaN of all ones made 1) over the wave, then the lowest lane holding it
-  // and the lowest of its experts, as lanes hold consecutive experts.
-  // (On 64-bit keys of score and index every step of the maximum took six
-  // instructions for one: 96 us for 52,001 tokens of 256 experts.)
+  // 4. top-K of the eligible experts by biased score.  key: ordered scores (0:
+  // not a candidate; 1 at least, also for a NaN of all ones).  The K-th key is
+  // found by halving an interval of keys: lo with at least K keys above it,
+  // hi with fewer, until exactly K are above lo or, where the K-th key is held
+  // more than once, hi is that key.  A count is one comparison a key and
+  // scalar work beside the other waves' vector work; from four powers of two
+  // below the largest key it takes about seven.
   uint32_t key[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = lane * EPL + j;
-    const int g = SEG ? lane >> lg : e / gs;
-    key[j] = (e < E && ((keep >> g) & 1)) ? max(ordered(u[j]), 1u) : 0;
+    // a segment past the last group has no bit in keep
+    key[j] = (SEG ? (keep >> (lane >> lg)) & 1 : e < E && ((keep >> (e / gs)) & 1)) ? max(ordered(u[j]), 1u) : 0;
   }
-  // Up to four experts a lane are first sorted (larger key first, then lower
-  // index: stable), so that a choice only looks at and shifts the heads.
-  constexpr bool kSorted = EPL <= 4;
-  uint32_t order = 0x03020100u;  // byte i: which expert of the lane is i-th
-  if constexpr (kSorted && EPL > 1) {
-    auto swap = [&](int a, int b) {  // a < b: keeps equal keys in place
-      const bool s = key[b] > key[a];
-      const uint32_t lo = s ? key[a] : key[b];
-      key[a] = s ? key[b] : key[a];
-      key[b] = lo;
-      const uint32_t pa = (order >> (8 * a)) & 0xFF, pb = (order >> (8 * b)) & 0xFF;
-      const uint32_t x = s ? pa ^ pb : 0;
-      order ^= (x << (8 * a)) | (x << (8 * b));
-    };
-    // neighbours only, so that the sort is stable
-    if constexpr (EPL == 2) {
-      swap(0, 1);
+  auto above = [&](uint32_t x) {
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) n += __builtin_popcountll(__ballot(key[j] > x));
+    return n;
+  };
+  uint32_t best = key[0];
+#pragma unroll
+  for (int j = 1; j < EPL; ++j) best = max(best, key[j]);
+  uint32_t hi = wave_max_u32(best);
+  uint32_t lo = hi - min(hi, 4u << 23);
+  int n = above(lo);
+  if (n < K) {
+    hi = lo;
+    lo = 0;  // K <= TG*E/G keys at least are above 0
+    n = above(0);
+  }
+  while (n != K && hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const int m = above(mid);
+    if (m >= K) {
+      lo = mid;
+      n = m;
     } else {
-      swap(0, 1), swap(2, 3), swap(1, 2), swap(0, 1), swap(2, 3), swap(1, 2);
+      hi = mid;
     }
   }
-  int my_e = 0;
-  for (int k = 0; k < K; ++k) {
-    uint32_t best = key[0];
-    if constexpr (!kSorted) {
+  bool chosen[EPL];
 #pragma unroll
-      for (int j = 1; j < EPL; ++j) best = max(best, key[j]);
+  for (int j = 0; j < EPL; ++j) chosen[j] = key[j] > lo;
+  // number of a lane's experts before this one's, of those marked in c, in
+  // the experts' order
+  auto before = [&](const bool (&c)[EPL]) {
+    uint32_t p = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const uint64_t b = __ballot(c[j]);
+      p = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(b >> 32),
+                                    __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(b), p));
     }
-    const uint32_t top = wave_max_u32(best);
-    const int owner = __builtin_ctzll(__ballot(best == top));
-    int at;
-    if constexpr (kSorted) {
-      at = order & 0xFF;
-      const bool mine = lane == owner;
+    return static_cast<int>(p);
+  };
+  if (n != K) {  // of the keys equal to hi only the first ones
+    bool same[EPL];
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) key[j] = mine ? (j + 1 < EPL ? key[j + 1] : 0) : key[j];
-      order = mine ? order >> 8 : order;
-    } else {
-      at = 0;
+    for (int j = 0; j < EPL; ++j) same[j] = key[j] == hi;
+    int left = K - above(hi) - before(same);
 #pragma unroll
-      for (int j = EPL - 1; j >= 0; --j) at = key[j] == top ? j : at;
-      const int gone = lane == owner ? at : -1;
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) key[j] = gone == j ? 0 : key[j];
+    for (int j = 0; j < EPL; ++j) {
+      chosen[j] = key[j] > hi || (same[j] && left > 0);
+      left -= same[j] ? 1 : 0;
     }
-    // K <= TG*E/G eligible experts always remain, so top != 0; the clamp
-    // only keeps the index in range.
-    const int e = min(owner * EPL + __builtin_amdgcn_readlane(at, owner), E - 1);
-    my_e = lane == k ? e : my_e;
   }
-  // the chosen scores and, in rank order, their sum
-  float my_s = 0.0f;
+  // the chosen, in the experts' order, to lanes 0 .. K - 1
+  __shared__ __attribute__((aligned(16))) u32x4 pick[kSelWaves][kMaxK];
+  {
+    int p = before(chosen);
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const float v = __shfl(sv[j], my_e / EPL);
-    my_s = my_e % EPL == j ? v : my_s;
+    for (int j = 0; j < EPL; ++j)
+      if (chosen[j]) {
+        pick[wave][min(p, kMaxK - 1)] =
+            u32x4{key[j], static_cast<uint32_t>(lane * EPL + j), __float_as_uint(sv[j]), 0};
+        ++p;
+      }
   }
-  float D = readlane_f(my_s, 0);
-  for (int k = 1; k < K; ++k) D = D + readlane_f(my_s, k);
+  // a wave's LDS operations complete in order; this holds the compiler to it
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  const u32x4 mine = pick[wave][min(lane, K - 1)];
+  // rank order: larger key first, then lower index.  Lane l compares choice
+  // l % 16 with choices l / 16, 4 + l / 16, ..: bit l of a round's ballot is
+  // set where the other one comes first.
+  int rank = lane;
+  {
+    const int r = lane % kMaxK, own = pick[wave][min(r, K - 1)][0];
+    int n = 0;
+    for (int i0 = 0; i0 < K; i0 += kWave / kMaxK) {
+      const int i = i0 + lane / kMaxK;
+      const uint32_t o = pick[wave][min(i, K - 1)][0], k = own;
+      const uint64_t b = __ballot(i < K && (o > k || (o == k && i < r)));
+      const uint32_t of_r = 0x00010001u << r;  // r's column
+      n += __builtin_popcount(static_cast<uint32_t>(b) & of_r) +
+           __builtin_popcount(static_cast<uint32_t>(b >> 32) & of_r);
+    }
+    if (lane < K) rank = n;
+  }
+  const float my_s = __builtin_bit_cast(
+      float, __builtin_amdgcn_ds_permute(4 * rank, static_cast<int>(mine[2])));  // ranked scores
+  // their sum in rank order: with each step a lane adds its score to the lane
+  // before's sum, so that after K - 1 lane K - 1 holds ((s_0 + s_1) + s_2) ..
+  float D = my_s;
+  for (int k = 1; k < K; ++k) D = __uint_as_float(dpp<0x111>(__float_as_uint(D))) + my_s;  // row_shr:1
+  D = readlane_f(D, K - 1);
   // 5. weights: (s / D) * scale, two binary32 roundings (0 where every chosen
   // score is 0), or s * scale
   if (lane < K) {
     const float q = !normed ? my_s : D == 0.0f ? 0.0f : my_s / D;
-    idx_out[t * K + lane] = my_e;
+    idx_out[t * K + rank] = static_cast<int32_t>(mine[1]);
     w_out[t * K + lane] = q * scale;
   }
 }
@@ -593,23 +638,23 @@ __global__ __launch_bounds__(256) void route_backward(
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      p[j] = p[j] > -__builtin_huge_valf() ? expf(p[j] - m) : 0.0f;
+      p[j] = p[j] == -__builtin_huge_valf() ? 0.0f : expf(p[j] - m);
       sum += p[j];
     }
 #pragma unroll
     for (int off = kWave / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
-    rs = sum > 0.0f ? 1.0f / sum : 0.0f;
+    rs = sum == 0.0f ? 0.0f : 1.0f / sum;
   }
   // the choices: scores, then the gradient g of each choice's own logit
   float s_k = 0.0f, ds_k = 0.0f;
   if (e_k >= 0) {
-    if (SM) s_k = l_k > -__builtin_huge_valf() ? expf(l_k - m) * rs : 0.0f;
+    if (SM) s_k = l_k == -__builtin_huge_valf() ? 0.0f : expf(l_k - m) * rs;
     else sigmoid_grad(l_k, s_k, ds_k);
   }
   float D = 1.0f;
   if (normed) {
     D = sum16(s_k);
-    D = D > 0.0f ? D : __builtin_huge_valf();  // all scores 0: every quotient below is 0
+    D = D == 0.0f ? __builtin_huge_valf() : D;  // all scores 0: every quotient below is 0
   }
   // lanes 0..15 hold the sum; the dense form needs it in every lane
   const float c = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(

@@ -190,3 +190,20 @@ def test_routing_of_nan_rows_stays_distinct():
         idx = idx.cpu()
         assert ((idx >= 0) & (idx < E)).all()
         assert all(len(set(r.tolist())) == K for r in idx)
+
+
+@pytest.mark.parametrize("flags", [gl.ROUTE_SOFTMAX, gl.ROUTE_SOFTMAX | gl.ROUTE_UNNORMED])
+def test_nan_and_infinite_logits_make_their_row_nan(flags):
+    c = make(6, 10)
+    d = gl.with_flags(c["d"], flags | gl.ROUTE_LOGITS_IN)
+    lg = torch.randn(6, c["sh"].n_experts, device=device())
+    clean = gl.route(d, None, None, None, lg)
+    g = gl.route_backward(d, lg, clean[0], c["d_w"])
+    lg[1, 3], lg[4, 50] = float("nan"), float("inf")
+    idx, w, _ = gl.route(d, None, None, None, lg)
+    got = gl.route_backward(d, lg, idx, c["d_w"])
+    ok = [0, 2, 3, 5]
+    assert torch.isnan(w[[1, 4]]).all() and torch.equal(w[ok], clean[1][ok]) and torch.equal(idx[ok], clean[0][ok])
+    chosen = torch.gather(got, 1, idx.long())
+    assert torch.isnan(chosen[[1, 4]]).all() and torch.equal(got[ok], g[ok])
+    assert all(len(set(r)) == c["sh"].top_k for r in idx.tolist())
