@@ -22,7 +22,10 @@
 //                    order, then routes in binary32 exactly as specified
 //                    (sigmoid from a fixed binary64 evaluation, ties to the
 //                    lower index), so indices and weights are bitwise
-//                    reproducible from the fp32 logits.
+//                    reproducible from the fp32 logits.  Scores may instead be
+//                    the softmax over all experts, the weights unnormalised.
+//   route_backward   one wavefront per token: the gradient of the weights in
+//                    the logits, scores recomputed in binary32.
 //
 // This translation unit is compiled with -ffp-contract=off.
 #include <type_traits>
@@ -223,6 +226,14 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
       __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, true));
 }
 
+// Orders a wave's LDS writes before its other lanes' reads (a wave's LDS
+// operations complete in order; this holds the compiler to it).
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Maximum over the wave, returned uniform.
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   v = max(v, dpp<0xB1>(v));   // quad_perm(1, 0, 3, 2)
@@ -322,7 +333,7 @@ __global__ __launch_bounds__(256) void router_select(
     int TG, int K, int topn, int lg, int normed, float scale, const float* __restrict__ bias,
     float* __restrict__ logits_out, int32_t* __restrict__ idx_out,
     float* __restrict__ w_out) {
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kSelWaves + wave;
   const bool valid = t < T;   // wave-uniform
   const int64_t tc = valid ? t : T - 1;
@@ -377,11 +388,17 @@ __global__ __launch_bounds__(256) void router_select(
 #pragma unroll
     for (int z = 1; z < KS; ++z)
       if (z < ks) l = l + pz[j][z];
-    if (SM) lv[j] = e < E ? l : ninf;
+    if (SM) lv[j] = l;
     else sv[j] = sigmoid32(l);
     if (valid && e < E && logits_out) logits_out[t * E + e] = l;
   }
-  if constexpr (SM) softmax32<EPL>(lv, sv);
+  if constexpr (SM) {
+    if (E < kWave * EPL)
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (lane * EPL + j >= E) lv[j] = ninf;
+    softmax32<EPL>(lv, sv);
+  }
 #pragma unroll
   for (int j = 0; j < EPL; ++j) u[j] = sv[j] + bz[j];  // past E: no group, no key
 
@@ -458,7 +475,9 @@ __global__ __launch_bounds__(256) void router_select(
   // hi with fewer, until exactly K are above lo or, where the K-th key is held
   // more than once, hi is that key.  A count is one comparison a key and
   // scalar work beside the other waves' vector work; from four powers of two
-  // below the largest key it takes about seven.
+  // below the largest key it takes about seven.  (52,001 tokens of 256
+  // experts, softmax, top 8: 40 us, the vector units busy 94% of it; K rounds
+  // of the wave's largest key over sorted lanes: 48.)
   uint32_t key[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
@@ -493,48 +512,42 @@ __global__ __launch_bounds__(256) void router_select(
       hi = mid;
     }
   }
-  bool chosen[EPL];
+  uint64_t chosen[EPL];  // bit l: expert j of lane l
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) chosen[j] = key[j] > lo;
-  // number of a lane's experts before this one's, of those marked in c, in
-  // the experts' order
-  auto before = [&](const bool (&c)[EPL]) {
+  for (int j = 0; j < EPL; ++j) chosen[j] = __ballot(key[j] > lo);
+  // number of experts before the lane's first, of those marked in c
+  auto before = [&](const uint64_t (&c)[EPL]) {
     uint32_t p = 0;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const uint64_t b = __ballot(c[j]);
-      p = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(b >> 32),
-                                    __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(b), p));
-    }
+    for (int j = 0; j < EPL; ++j)
+      p = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(c[j] >> 32),
+                                    __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(c[j]), p));
     return static_cast<int>(p);
   };
   if (n != K) {  // of the keys equal to hi only the first ones
-    bool same[EPL];
+    uint64_t same[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) same[j] = key[j] == hi;
+    for (int j = 0; j < EPL; ++j) same[j] = __ballot(key[j] == hi);
     int left = K - above(hi) - before(same);
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      chosen[j] = key[j] > hi || (same[j] && left > 0);
-      left -= same[j] ? 1 : 0;
+      chosen[j] = __ballot(key[j] > hi || (key[j] == hi && left > 0));
+      left -= key[j] == hi ? 1 : 0;
     }
   }
-  // the chosen, in the experts' order, to lanes 0 .. K - 1
+  // the chosen, exactly K, in the experts' order to lanes 0 .. K - 1
   __shared__ __attribute__((aligned(16))) u32x4 pick[kSelWaves][kMaxK];
   {
     int p = before(chosen);
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
-      if (chosen[j]) {
-        pick[wave][min(p, kMaxK - 1)] =
+      if (__builtin_amdgcn_inverse_ballot_w64(chosen[j])) {
+        pick[wave][p] =
             u32x4{key[j], static_cast<uint32_t>(lane * EPL + j), __float_as_uint(sv[j]), 0};
         ++p;
       }
   }
-  // a wave's LDS operations complete in order; this holds the compiler to it
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  wave_order();
   const u32x4 mine = pick[wave][min(lane, K - 1)];
   // rank order: larger key first, then lower index.  Lane l compares choice
   // l % 16 with choices l / 16, 4 + l / 16, ..: bit l of a round's ballot is
@@ -582,25 +595,30 @@ __device__ __forceinline__ void sigmoid_grad(float l, float& s, float& ds) {
 
 // Sum over lanes 0..15, in every one of them (a wave's choices, K <= 16).
 __device__ __forceinline__ float sum16(float v) {
-#pragma unroll
-  for (int off = 8; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+  auto step = [&](uint32_t o) { v += __uint_as_float(o); };
+  step(dpp<0xB1>(__float_as_uint(v)));
+  step(dpp<0x4E>(__float_as_uint(v)));
+  step(dpp<0x141>(__float_as_uint(v)));
+  step(dpp<0x140>(__float_as_uint(v)));
   return v;
 }
 
 // One wave per token; lane l holds experts l*EPL .. l*EPL + EPL - 1 of the
-// row, lanes 0..K-1 also a choice each.  Every lane adds the choices that
-// name its experts in rank order (no scatter, so an expert named twice needs
-// no atomic and the row is written once, whole).  Bound by reading and
-// writing the logits' rows: a sigmoid row is only written, its K chosen
-// logits being gathered.
+// row, lanes 0..K-1 also a choice each.  The choices' gradients meet the row
+// in LDS; where an expert is named twice every lane instead adds the choices
+// that name its experts in rank order, so no sum depends on timing.  Bound by
+// reading and writing the logits' rows: a sigmoid row is only written, its K
+// chosen logits being gathered (16,384 rows of 256, softmax: 9.2 us; every
+// lane adding every choice: 12.4).
 template <int EPL, bool SM>
 __global__ __launch_bounds__(256) void route_backward(
     const float* __restrict__ logits, const int32_t* __restrict__ idx,
     const float* __restrict__ dw, int vec4, int64_t T, int E, int K, int normed, float scale,
     float* __restrict__ dl) {
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kSelWaves + wave;
   if (t >= T) return;  // wave-uniform
+  __shared__ __attribute__((aligned(16))) float sh[kSelWaves][kWave * EPL];
   const float* row = logits + t * E;
   float p[EPL];
   float m = 0.0f, rs = 0.0f;
@@ -641,8 +659,10 @@ __global__ __launch_bounds__(256) void route_backward(
       p[j] = p[j] == -__builtin_huge_valf() ? 0.0f : expf(p[j] - m);
       sum += p[j];
     }
-#pragma unroll
-    for (int off = kWave / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+    sum = sum16(sum);
+    sum += __uint_as_float(dpp<0x142>(__float_as_uint(sum)));  // rows 0 and 1, 2 and 3
+    sum += __uint_as_float(dpp<0x143>(__float_as_uint(sum)));  // all, in the last lane
+    sum = readlane_f(sum, kWave - 1);
     rs = sum == 0.0f ? 0.0f : 1.0f / sum;
   }
   // the choices: scores, then the gradient g of each choice's own logit
@@ -666,12 +686,31 @@ __global__ __launch_bounds__(256) void route_backward(
   float out[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) out[j] = SM ? -back * p[j] : 0.0f;
-  for (int k = 0; k < K; ++k) {
-    const int e = __builtin_amdgcn_readlane(e_k, k);
-    const float gk = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, g), k));
+  // an expert named twice: lane l compares choice l % 16 with l / 16, ..
+  uint64_t twice = 0;
+  for (int i0 = 0; i0 < K; i0 += kWave / 16) {
+    const int i = i0 + lane / 16;
+    const int ei = __shfl(e_k, i % 16), er = __shfl(e_k, lane % 16);
+    twice |= __ballot(i < lane % 16 && ei >= 0 && ei == er);
+  }
+  if (!twice) {
+    // through LDS: zeros, the choices' gradients where they belong, the row
+    float* row_g = sh[wave];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (lane * EPL + j == e) out[j] += gk;
+    for (int j = 0; j < EPL; ++j) row_g[lane * EPL + j] = 0.0f;
+    wave_order();
+    if (e_k >= 0) row_g[e_k] = g;
+    wave_order();
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) out[j] += row_g[lane * EPL + j];
+  } else {
+    for (int k = 0; k < K; ++k) {
+      const int e = __builtin_amdgcn_readlane(e_k, k);
+      const float gk = readlane_f(g, k);
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (lane * EPL + j == e) out[j] += gk;
+    }
   }
   float* o = dl + t * E;
   if (EPL % 4 == 0 && vec4) {
