@@ -4,7 +4,9 @@ Argument marshalling only: every step of the block runs in the library's HIP
 kernels.  torch supplies device memory and the current stream.  The names
 follow the C ABI in include/beam_moe.h (beam_moe_route, beam_moe_forward,
 beam_moe_permute, beam_moe_quant_e4m3, beam_moe_workspace_bytes,
-beam_moe_validate).  There is no CPU fallback: without the built library
+beam_moe_validate; around the block beam_moe_route_backward,
+beam_moe_matmul_e4m3, beam_moe_quant_e4m3_2d, beam_moe_norm_residual and its
+_backward).  There is no CPU fallback: without the built library
 every call raises.
 """
 from __future__ import annotations
@@ -485,8 +487,8 @@ def matmul_e4m3(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch.
     else:
         py = _arg("out", out, dev, dtype, (M, N))
     _run(lib().beam_moe_matmul_e4m3, "beam_moe_matmul_e4m3", stream, dev, (a, s_a, b, s_b, out),
-         M, N, K, pa, psa, *s_a.stride(), pb, psb, *s_b.stride(), 1 if rows else 0, BF16 if dtype is torch.bfloat16 else F32,
-         py)
+         M, N, K, pa, psa, *s_a.stride(), pb, psb, *s_b.stride(), 1 if rows else 0,
+         BF16 if dtype is torch.bfloat16 else F32, py)
     return out
 
 

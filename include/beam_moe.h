@@ -21,6 +21,9 @@
  * DeepSeek-V3's (arXiv 2412.19437, section 2.1.2); the pages invoke that
  * scheme without spelling the rule out.
  *
+ * Around the block: the gradient of the routing, dense e4m3 products with their
+ * quantiser, and the step between two blocks with its gradients.
+ *
  * Conventions for every entry point:
  *   - Pointers marked "device" are device memory owned by the caller.  The
  *     library allocates nothing, frees nothing and keeps no pointer after a
@@ -37,7 +40,8 @@
  *   - Layouts are row-major.  Weights use the out x in ("nn.Linear") layout.
  *   - Identical inputs give bitwise identical outputs (no floating-point
  *     atomics).  Calls are reentrant given distinct workspaces.
- *   - Inputs containing NaN or Inf are outside the contract.
+ *   - Inputs containing NaN or Inf are outside the contract, but where an
+ *     entry point says what they give.
  */
 #ifndef BEAM_MOE_H
 #define BEAM_MOE_H
@@ -144,7 +148,8 @@ int beam_moe_workspace_bytes(const beam_moe_desc* desc, int64_t T,
  * - max l) over all E logits, evaluated in binary64 and rounded once to
  * binary32; a logit of -infinity gives the score 0, a row of only those has
  * scores 0, and a NaN or +infinity makes its row's scores (and gradients) NaN,
- * the K experts still different ones.  With BEAM_ROUTE_UNNORMED the weights are s_k * routed_scale.
+ * the K experts still different ones.  With BEAM_ROUTE_UNNORMED the weights
+ * are s_k * routed_scale.
  * Where the K chosen scores are all 0 (logits so low that binary32 holds no
  * smaller score, or masked ones) the weights are 0.  Keeping every group
  * (topk_groups = n_groups) is plain top-K over the experts. */
