@@ -60,11 +60,19 @@ __device__ __forceinline__ f32x4 mfma_wide(const Wide& a, const Wide& b, f32x4 c
   return c;
 }
 
-// Swizzle of a tile row's eight 16-byte chunks: the same chunk of any 16
-// consecutive rows lies in 16 different places of the LDS banks' 256 bytes
-// (rows 2i and 2i + 1 in its two halves), and the key repeats every 16 rows,
-// so one lane offset serves every fragment.
-__device__ __forceinline__ int key(int row) { return (row >> 1) & 7; }
+// Swizzle of a tile row's eight 16-byte chunks: chunk c of row r lies in place
+// c ^ key(r) of the row's 128 bytes, rows 2i and 2i + 1 in the two halves of
+// the LDS banks' 256 bytes.  A fragment's reads of 16 bytes a lane (row l % 16,
+// chunk 2 (l / 16)) go through in groups of 16 lanes, {0-3, 12-15, 20-27},
+// {4-11, 16-19, 28-31} and the same 32 further on: rows 0-3 and 12-15 of one
+// chunk with rows 4-11 of the chunk two further.  So the keys of one half of
+// these row pairs are 4 .. 7 and those of the other 0 .. 3, a set that ^ 2 maps
+// to itself: every group's 16 places differ.  (With key = i every read took
+// twice its cycles, 43% of all that the LDS spent in a large product.)  The
+// key repeats every 16 rows, so one lane offset serves every fragment.
+__device__ __forceinline__ int key(int row) {
+  return ((row >> 1) & 3) | ((~((row >> 3) ^ (row >> 2)) & 1) << 2);
+}
 
 // The lane's codes of a 16-row fragment starting at tile row `row0`: its row
 // l % 16, the 32 codes from 32 (l / 16) of the block.
