@@ -476,7 +476,7 @@ __global__ __launch_bounds__(256) void router_select(
   // more than once, hi is that key.  A count is one comparison a key and
   // scalar work beside the other waves' vector work; from four powers of two
   // below the largest key it takes about seven.  (52,001 tokens of 256
-  // experts, softmax, top 8: 40 us, the vector units busy 94% of it; K rounds
+  // experts, softmax, top 8: 40 us, bound by its 345 vector instructions a token; K rounds
   // of the wave's largest key over sorted lanes: 48.)
   uint32_t key[EPL];
 #pragma unroll
