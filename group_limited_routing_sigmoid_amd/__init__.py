@@ -541,6 +541,8 @@ def _norm_residual(residual, o, post_weight, gate, pre_weight, eps, alpha, beta,
     device = residual.device
     x = q = s = p_out = px = pq = ps = None
     if o is None:
+        if residual_out is not None:
+            raise ValueError("residual_out belongs to o: without it r' is the residual itself")
         residual_out = residual
     else:
         if residual_out is None:

@@ -207,3 +207,9 @@ def test_nan_and_infinite_logits_make_their_row_nan(flags):
     chosen = torch.gather(got, 1, idx.long())
     assert torch.isnan(chosen[[1, 4]]).all() and torch.equal(got[ok], g[ok])
     assert all(len(set(r)) == c["sh"].top_k for r in idx.tolist())
+
+
+def test_residual_out_needs_a_block_output():
+    c = make(3, 11)
+    with pytest.raises(ValueError, match="belongs to o"):
+        gl.norm_residual(c["residual"], pre_weight=c["pre1"], residual_out=torch.empty_like(c["residual"]))
