@@ -271,21 +271,32 @@ _empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", N
                          "_empty_strided_cuda", None)
 
 
-def _empty(stream, device, dtype: torch.dtype, *shape) -> torch.Tensor:
+def _on(stream, dev: int):
+    """Where a call runs, for _empty and _run: True on the current device's
+    current stream, else the stream it was given (None: GPU `dev`'s current
+    one)."""
+    return True if stream is None and dev >= 0 and dev == _current_device() else stream
+
+
+def _empty(on, device, dtype: torch.dtype, *shape) -> torch.Tensor:
     """An output of one or two dimensions, allocated on the call's stream."""
-    if stream is None:
-        if _empty_strided is not None and device.index == _current_device():
-            return _empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
-        return torch.empty(*shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
+    if on is True and _empty_strided is not None:
+        return _empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
+    with _alloc_on(None if on is True else on):
         return torch.empty(*shape, dtype=dtype, device=device)
 
 
-def _run(fn, what: str, stream, dev: int, tensors, *args):
+def _run(fn, what: str, on, dev: int, tensors, *args):
     """Call a library entry point whose last argument is the stream on GPU
     `dev`, whichever is current.  Tensors read or written on a stream that is
     not the current one are marked as used there, so torch's allocator keeps
     their memory until the kernels are done."""
+    if on is True:
+        status = fn(*args, _raw_stream(dev))
+        if status != OK:
+            raise BeamError(status, what)
+        return
+    stream = on
     raw = _raw_stream(dev)
     if stream is not None and stream.cuda_stream != raw:
         if stream.device.index != dev:
@@ -313,16 +324,17 @@ def route(desc: Desc, x: Optional[torch.Tensor], w_router: Optional[torch.Tensor
     lin = bool(desc.flags & ROUTE_LOGITS_IN)
     ref = logits if lin else x
     T, E, device, dev = ref.shape[0], desc.n_experts, ref.device, ref.get_device()
+    on = _on(stream, dev)
     px, pr = (None, None) if lin else (_addr(x), _addr(w_router))
     pb = None if bias is None else _arg("bias", bias, dev, torch.float32, (E,))
     if logits is None:
-        logits = _empty(stream, device, torch.float32, T, E)
+        logits = _empty(on, device, torch.float32, T, E)
     pl = _arg("logits", logits, dev, torch.float32, (T, E))
-    idx = _empty(stream, device, torch.int32, T, desc.top_k)
-    w = _empty(stream, device, torch.float32, T, desc.top_k)
+    idx = _empty(on, device, torch.int32, T, desc.top_k)
+    w = _empty(on, device, torch.float32, T, desc.top_k)
     # routing from given logits uses no scratch memory
     buf, n = (None, 0) if lin else _ws(desc, T, workspace, device, stream)
-    _run(lib().beam_moe_route, "beam_moe_route", stream, dev, (x, w_router, bias, logits, idx, w),
+    _run(lib().beam_moe_route, "beam_moe_route", on, dev, (x, w_router, bias, logits, idx, w),
          ctypes.byref(desc), T, px, pr, pb, pl, idx.data_ptr(), w.data_ptr(), _addr(buf), n)
     return idx, w, logits
 
@@ -333,15 +345,16 @@ def route_backward(desc: Desc, logits: torch.Tensor, topk_idx: torch.Tensor,
     """beam_moe_route_backward: the gradient [T,E] fp32 of the logits from that
     of the routing weights (the selection and the bias are constants)."""
     T, E, K, dev = logits.shape[0], desc.n_experts, desc.top_k, logits.get_device()
+    on = _on(stream, dev)
     pl = _arg("logits", logits, dev, torch.float32, (T, E))
     pi = _arg("topk_idx", topk_idx, dev, torch.int32, (T, K))
     pw = _arg("d_topk_w", d_topk_w, dev, torch.float32, (T, K))
     if out is None:
-        out = _empty(stream, logits.device, torch.float32, T, E)
+        out = _empty(on, logits.device, torch.float32, T, E)
         po = out.data_ptr()
     else:
         po = _arg("out", out, dev, torch.float32, (T, E))
-    _run(lib().beam_moe_route_backward, "beam_moe_route_backward", stream, dev,
+    _run(lib().beam_moe_route_backward, "beam_moe_route_backward", on, dev,
          (logits, topk_idx, d_topk_w, out), ctypes.byref(desc), T, pl, pi, pw, po)
     return out
 
@@ -445,18 +458,19 @@ def quant_e4m3_2d(v: torch.Tensor, block: bool = False, straight: bool = True,
         raise ValueError(f"v: dtype {v.dtype}, expected torch.bfloat16 or torch.float32")
     rows, cols = v.shape
     dev, device = v.get_device(), v.device
+    on = _on(stream, dev)
     pv = _arg("v", v, dev, v.dtype, (rows, cols))
     nr, nc = (rows + 127) // 128, (cols + 127) // 128
     q = s = qt = st = None
     if straight:
-        q = _empty(stream, device, torch.uint8, rows, nc * 128)
-        s = (_empty(stream, device, torch.float32, nr, nc) if block else
-             _empty(stream, device, torch.float32, nc, rows).t())
+        q = _empty(on, device, torch.uint8, rows, nc * 128)
+        s = (_empty(on, device, torch.float32, nr, nc) if block else
+             _empty(on, device, torch.float32, nc, rows).t())
     if transposed:
-        qt = _empty(stream, device, torch.uint8, cols, nr * 128)
-        st = (_empty(stream, device, torch.float32, nc, nr) if block else
-              _empty(stream, device, torch.float32, nr, cols).t())
-    _run(lib().beam_moe_quant_e4m3_2d, "beam_moe_quant_e4m3_2d", stream, dev, (v, q, s, qt, st),
+        qt = _empty(on, device, torch.uint8, cols, nr * 128)
+        st = (_empty(on, device, torch.float32, nc, nr) if block else
+              _empty(on, device, torch.float32, nr, cols).t())
+    _run(lib().beam_moe_quant_e4m3_2d, "beam_moe_quant_e4m3_2d", on, dev, (v, q, s, qt, st),
          rows, cols, BF16 if v.dtype is torch.bfloat16 else F32, 1 if block else 0, pv,
          *(None if t is None else t.data_ptr() for t in (q, s, qt, st)))
     return q, s, qt, st
@@ -478,15 +492,16 @@ def matmul_e4m3(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch.
         raise ValueError(f"K = {K} is not a multiple of 128")
     rows = s_b.dim() == 2 and s_b.shape[0] == N
     dev = a.get_device()
+    on = _on(stream, dev)
     pa, pb = _arg("a", a, dev, torch.uint8, (M, K)), _arg("b", b, dev, torch.uint8, (N, K))
     psa = _arg("s_a", s_a, dev, torch.float32, (M, K // 128), True)
     psb = _arg("s_b", s_b, dev, torch.float32, (N if rows else (N + 127) // 128, K // 128), True)
     if out is None:
-        out = _empty(stream, a.device, dtype, M, N)
+        out = _empty(on, a.device, dtype, M, N)
         py = out.data_ptr()
     else:
         py = _arg("out", out, dev, dtype, (M, N))
-    _run(lib().beam_moe_matmul_e4m3, "beam_moe_matmul_e4m3", stream, dev, (a, s_a, b, s_b, out),
+    _run(lib().beam_moe_matmul_e4m3, "beam_moe_matmul_e4m3", on, dev, (a, s_a, b, s_b, out),
          M, N, K, pa, psa, *s_a.stride(), pb, psb, *s_b.stride(), 1 if rows else 0,
          BF16 if dtype is torch.bfloat16 else F32, py)
     return out
@@ -538,7 +553,7 @@ def _norm_residual(residual, o, post_weight, gate, pre_weight, eps, alpha, beta,
     T, H, dev, dtype, po, pw, pg, cols, pp = _norm_inputs(
         residual, o, post_weight, gate, pre_weight, dtype)
     pr = _arg("residual", residual, dev, torch.float32, (T, H))
-    device = residual.device
+    device, on = residual.device, _on(stream, dev)
     x = q = s = p_out = px = pq = ps = None
     if o is None:
         if residual_out is not None:
@@ -546,18 +561,18 @@ def _norm_residual(residual, o, post_weight, gate, pre_weight, eps, alpha, beta,
         residual_out = residual
     else:
         if residual_out is None:
-            residual_out = _empty(stream, device, torch.float32, T, H)
+            residual_out = _empty(on, device, torch.float32, T, H)
             p_out = residual_out.data_ptr()
         else:
             p_out = _arg("residual_out", residual_out, dev, torch.float32, (T, H))
     if pp is not None and want_x:
-        x = _empty(stream, device, dtype, T, H)
+        x = _empty(on, device, dtype, T, H)
         px = x.data_ptr()
     if codes:
-        q = _empty(stream, device, torch.uint8, T, H)
-        s = _empty(stream, device, torch.float32, T, H // 128)
+        q = _empty(on, device, torch.uint8, T, H)
+        s = _empty(on, device, torch.float32, T, H // 128)
         pq, ps = q.data_ptr(), s.data_ptr()
-    _run(lib().beam_moe_norm_residual, "beam_moe_norm_residual", stream, dev,
+    _run(lib().beam_moe_norm_residual, "beam_moe_norm_residual", on, dev,
          (residual, o, post_weight, gate, pre_weight, residual_out, x, q, s), T, H,
          BF16 if dtype is torch.bfloat16 else F32, po, pw, pg, cols, pp, eps, alpha, beta, pr, p_out,
          px, pq, ps)
@@ -619,24 +634,24 @@ def norm_residual_backward(residual_out: torch.Tensor,
     T, H, dev, dtype, po, pw, pg, cols, pp = _norm_inputs(
         residual_out, o, post_weight, gate, pre_weight,
         d_x.dtype if o is None and d_x is not None else None)
-    device, f32 = residual_out.device, torch.float32
+    device, f32, on = residual_out.device, torch.float32, _on(stream, dev)
     pr = _arg("residual_out", residual_out, dev, f32, (T, H))
     p_dr = None if d_residual_out is None else _arg("d_residual_out", d_residual_out, dev, f32, (T, H))
     p_dx = None if d_x is None else _arg("d_x", d_x, dev, dtype, (T, H))
     need = ctypes.c_size_t(0)
     _check(lib().beam_moe_norm_residual_workspace_bytes(T, H, ctypes.byref(need)),
            "beam_moe_norm_residual_workspace_bytes")
-    out = {"d_residual": _empty(stream, device, f32, T, H)}
+    out = {"d_residual": _empty(on, device, f32, T, H)}
     if o is not None:
-        out["d_o"] = _empty(stream, device, dtype, T, H)
-        out["d_post_weight"] = _empty(stream, device, f32, H)
+        out["d_o"] = _empty(on, device, dtype, T, H)
+        out["d_post_weight"] = _empty(on, device, f32, H)
         if gate is not None:
-            out["d_gate"] = _empty(stream, device, dtype, T, cols)
+            out["d_gate"] = _empty(on, device, dtype, T, cols)
     if d_x is not None:
-        out["d_pre_weight"] = _empty(stream, device, f32, H)
+        out["d_pre_weight"] = _empty(on, device, f32, H)
     buf = _scratch(need.value, workspace, device, stream)
     ptr = {k: v.data_ptr() for k, v in out.items()}
-    _run(lib().beam_moe_norm_residual_backward, "beam_moe_norm_residual_backward", stream, dev,
+    _run(lib().beam_moe_norm_residual_backward, "beam_moe_norm_residual_backward", on, dev,
          (residual_out, d_residual_out, d_x, o, post_weight, gate, pre_weight, *out.values()),
          T, H, BF16 if dtype is torch.bfloat16 else F32, po, pw, pg, cols, pp, eps, alpha, beta, pr,
          p_dr, p_dx, ptr["d_residual"], ptr.get("d_o"), ptr.get("d_gate"), ptr.get("d_pre_weight"),
