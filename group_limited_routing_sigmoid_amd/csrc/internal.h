@@ -160,7 +160,7 @@ struct NormGradArgs {
   float eps, alpha, beta;
 };
 // Workgroups of the backward pass, each with its share of the weights' gradients.
-int norm_grad_groups(int64_t T);
+int norm_grad_groups(int64_t T, int H);
 int64_t norm_max_tokens(int H);  // a launch holds fewer than 2^32 threads
 constexpr int kNormMaxH = 16384;  // 1024 threads of 16 columns
 hipError_t launch_norm_residual(const NormArgs& a, int64_t T, int32_t dtype, hipStream_t s);

@@ -68,7 +68,7 @@ int beam_moe_norm_residual(int64_t T, int64_t H, int32_t dtype, const void* o,
 int beam_moe_norm_residual_workspace_bytes(int64_t T, int64_t H, size_t* bytes) {
   if (!bytes || T < 0 || H < 1) return BEAM_ERR_INVALID_ARG;
   if (H > kNormMaxH || T > norm_max_tokens(static_cast<int>(H))) return BEAM_ERR_UNSUPPORTED;
-  *bytes = static_cast<size_t>(norm_grad_groups(T)) * 2 * static_cast<size_t>(H) * sizeof(float);
+  *bytes = static_cast<size_t>(norm_grad_groups(T, static_cast<int>(H))) * 2 * static_cast<size_t>(H) * sizeof(float);
   return BEAM_OK;
 }
 

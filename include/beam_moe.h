@@ -382,8 +382,7 @@ int beam_moe_quant_e4m3_2d(int64_t rows, int64_t cols, int32_t dtype, int32_t bl
  * dtype BEAM_F32 or BEAM_BF16; 1 <= H <= 16384, with x_codes H % 128 == 0
  * (BEAM_ERR_UNSUPPORTED otherwise, and for more tokens than a launch holds:
  * at least 4,194,303, 67 million at H = 128); eps > 0, alpha and beta finite.  A token's
- * sums of squares must be finite in binary32.  With H % 8 == 0 the rows are
- * read 16 bytes at a time, otherwise value by value.  No workspace. */
+ * sums of squares must be finite in binary32.  No workspace. */
 int beam_moe_norm_residual(int64_t T, int64_t H, int32_t dtype, const void* o,
                            const float* post_weight, const void* gate, int64_t gate_cols,
                            const float* pre_weight, float eps, float alpha, float beta,

@@ -276,3 +276,22 @@ def test_captured_with_work_between_replays():
         torch.cuda.synchronize()
         assert all(torch.equal(got[k], want[k]) for k in want)
         assert all(torch.equal(between[k], want_other[k]) for k in want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("gate", [None, "token", "channel"])
+@pytest.mark.parametrize("T,H", [(9, 9), (9, 10), (9, 11), (8, 12), (9, 13), (9, 14), (9, 15), (5, 17), (3, 5119),
+                                 (2, 8191), (2, 8193), (1500, 31), (2100, 70)])
+def test_rows_that_end_inside_a_chunk(T, H, gate, dtype):
+    # every odd start of a row and every length of its last chunk of 8
+    c = make(T, H, dtype, gate, True, 3 * T + H)
+    dc = on(device(), c)
+    buf = torch.full((T + 1, H), 7.0, device=device())
+    r, x = gl.norm_residual(dc["residual"], residual_out=buf[:T], **kw(dc))
+    assert r.data_ptr() == buf.data_ptr() and (buf[T] == 7.0).all()
+    check_forward(c, dtype, r, x)
+    got = gl.norm_residual_backward(r, dc["d_r"], dc["d_x"], **kw(dc))
+    check_backward(c, dtype, r, got)
+    for use in (dict(d_x=dc["d_x"]), dict(d_residual_out=dc["d_r"])):
+        part = gl.norm_residual_backward(r, **use, **kw(dc))
+        check_backward(c, dtype, r, part, use_r="d_residual_out" in use, use_x="d_x" in use)
