@@ -221,17 +221,26 @@ _default_ws = {}
 
 
 def _scratch(n: int, workspace: Optional[Workspace], device, stream=None):
-    s = _torch_stream(stream, device)
+    if n == 0:
+        return None
+    if workspace is not None:
+        return workspace.get(n, _torch_stream(stream, device))
+    # A call that is being captured takes memory of its graph instead: graphs
+    # are captured on one stream and replayed on any.
+    if stream is None:
+        capturing = torch._C._cuda_isCurrentStreamCapturing()
+    else:
+        with torch.cuda.stream(stream):
+            capturing = torch._C._cuda_isCurrentStreamCapturing()
+    if capturing:
+        return Workspace(device).get(n, _torch_stream(stream, device))
+    key = (device.index, _raw_stream(device.index) if stream is None else stream.cuda_stream)
+    workspace = _default_ws.get(key)
     if workspace is None:
-        # A call that is being captured takes memory of its graph instead:
-        # graphs are captured on one stream and replayed on any.
-        with _alloc_on(stream):
-            capturing = torch.cuda.is_current_stream_capturing()
-        if capturing:
-            return Workspace(device).get(n, s)
-        key = (str(device), s.cuda_stream)
-        workspace = _default_ws.setdefault(key, Workspace(device))
-    return workspace.get(n, s)
+        workspace = _default_ws[key] = Workspace(device)
+    elif workspace.buf is not None and workspace.buf.numel() >= n:
+        return workspace.buf  # allocated on the key's stream, used there only
+    return workspace.get(n, _torch_stream(stream, device))
 
 
 def _ws(desc: Desc, T: int, workspace: Optional[Workspace], device, stream=None):
@@ -284,6 +293,13 @@ def _empty(on, device, dtype: torch.dtype, *shape) -> torch.Tensor:
         return _empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
     with _alloc_on(None if on is True else on):
         return torch.empty(*shape, dtype=dtype, device=device)
+
+
+def _empty_t(on, device, dtype: torch.dtype, rows: int, cols: int) -> torch.Tensor:
+    """An output [rows, cols] stored column by column."""
+    if on is True and _empty_strided is not None:
+        return _empty_strided((rows, cols), (1, rows), dtype)
+    return _empty(on, device, dtype, cols, rows).t()
 
 
 def _run(fn, what: str, on, dev: int, tensors, *args):
@@ -465,11 +481,11 @@ def quant_e4m3_2d(v: torch.Tensor, block: bool = False, straight: bool = True,
     if straight:
         q = _empty(on, device, torch.uint8, rows, nc * 128)
         s = (_empty(on, device, torch.float32, nr, nc) if block else
-             _empty(on, device, torch.float32, nc, rows).t())
+             _empty_t(on, device, torch.float32, rows, nc))
     if transposed:
         qt = _empty(on, device, torch.uint8, cols, nr * 128)
         st = (_empty(on, device, torch.float32, nc, nr) if block else
-              _empty(on, device, torch.float32, nr, cols).t())
+              _empty_t(on, device, torch.float32, cols, nr))
     _run(lib().beam_moe_quant_e4m3_2d, "beam_moe_quant_e4m3_2d", on, dev, (v, q, s, qt, st),
          rows, cols, BF16 if v.dtype is torch.bfloat16 else F32, 1 if block else 0, pv,
          *(None if t is None else t.data_ptr() for t in (q, s, qt, st)))
