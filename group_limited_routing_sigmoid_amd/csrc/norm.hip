@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kMaxWaves = 16;
 
-constexpr int VEC = 8;  // columns of a thread's chunk
+constexpr int kVec = 8;  // columns of a thread's chunk
 
 // Rows of a multiple of 8 columns start 16-byte aligned and end with a chunk
 // (TAIL false).  Others (TAIL true) start anywhere, and their last chunk is the
@@ -42,8 +42,8 @@ struct Place {
 template <bool TAIL>
 __device__ __forceinline__ Place place(int i, int H) {
   Place p;
-  p.slot = (threadIdx.x + i * blockDim.x) * VEC;
-  p.col = TAIL ? min(p.slot, max(H - VEC, 0)) : p.slot;
+  p.slot = (threadIdx.x + i * blockDim.x) * kVec;
+  p.col = TAIL ? min(p.slot, max(H - kVec, 0)) : p.slot;
   p.skip = TAIL ? p.slot - p.col : 0;
   p.live = p.slot < H;
   return p;
@@ -53,18 +53,18 @@ typedef u32x4 u32x4_2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_4 __attribute__((aligned(4)));
 template <typename IO, bool TAIL>
 struct Chunk {
-  static constexpr int kWords = VEC * static_cast<int>(sizeof(IO)) / 16;
+  static constexpr int kWords = kVec * static_cast<int>(sizeof(IO)) / 16;
   using Word = std::conditional_t<!TAIL, u32x4, std::conditional_t<sizeof(IO) == 2, u32x4_2, u32x4_4>>;
   u32x4 w[kWords];  // as they lie in memory (bf16 ones two to a register)
   // n: columns of the row; of fewer than 8 the others count as zeros.
   __device__ __forceinline__ void load(const IO* p, int n) {
-    if (!TAIL || n >= VEC) {
+    if (!TAIL || n >= kVec) {
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) w[i] = *reinterpret_cast<const Word*>(p + i * (VEC / kWords));
+      for (int i = 0; i < kWords; ++i) w[i] = *reinterpret_cast<const Word*>(p + i * (kVec / kWords));
     } else {
       zero();
 #pragma unroll
-      for (int j = 0; j < VEC - 1; ++j)
+      for (int j = 0; j < kVec - 1; ++j)
         if (j < n) {
           if constexpr (sizeof(IO) == 2) w[0][j / 2] |= static_cast<uint32_t>(p[j]) << (16 * (j % 2));
           else w[j / 4][j % 4] = __float_as_uint(p[j]);
@@ -92,15 +92,15 @@ struct Chunk {
 };
 
 template <typename IO, bool TAIL>
-__device__ __forceinline__ void load_vec(const IO* p, int n, float (&v)[VEC]) {
+__device__ __forceinline__ void load_vec(const IO* p, int n, float (&v)[kVec]) {
   Chunk<IO, TAIL> c;
   c.load(p, n);
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) v[j] = c.get(j);
+  for (int j = 0; j < kVec; ++j) v[j] = c.get(j);
 }
 
 template <typename IO, bool TAIL>
-__device__ __forceinline__ void store_vec(IO* p, int n, const float (&v)[VEC]) {
+__device__ __forceinline__ void store_vec(IO* p, int n, const float (&v)[kVec]) {
   Chunk<IO, TAIL> c;
   if constexpr (sizeof(IO) == 2) {
 #pragma unroll
@@ -109,15 +109,15 @@ __device__ __forceinline__ void store_vec(IO* p, int n, const float (&v)[VEC]) {
                   (static_cast<uint32_t>(f32_to_bf16_bits(v[2 * i + 1])) << 16);
   } else {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) c.w[j / 4][j % 4] = __float_as_uint(v[j]);
+    for (int j = 0; j < kVec; ++j) c.w[j / 4][j % 4] = __float_as_uint(v[j]);
   }
-  if (!TAIL || n >= VEC) {
+  if (!TAIL || n >= kVec) {
 #pragma unroll
     for (int i = 0; i < Chunk<IO, TAIL>::kWords; ++i)
-      *reinterpret_cast<typename Chunk<IO, TAIL>::Word*>(p + i * (VEC / Chunk<IO, TAIL>::kWords)) = c.w[i];
+      *reinterpret_cast<typename Chunk<IO, TAIL>::Word*>(p + i * (kVec / Chunk<IO, TAIL>::kWords)) = c.w[i];
   } else {
 #pragma unroll
-    for (int j = 0; j < VEC - 1; ++j)
+    for (int j = 0; j < kVec - 1; ++j)
       if (j < n) {
         if constexpr (sizeof(IO) == 2) p[j] = static_cast<uint16_t>(c.w[0][j / 2] >> (16 * (j % 2)));
         else p[j] = v[j];
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
   const int H = a.H;
   const IO* o = a.o ? static_cast<const IO*>(a.o) + base : nullptr;
   const IO* gate = static_cast<const IO*>(a.gate);
-  float r[NC][VEC];
+  float r[NC][kVec];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const Place at = place<TAIL>(i, H);
@@ -200,10 +200,10 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
     if (at.live) load_vec<float, TAIL>(a.residual + base + c, H, r[i]);
     else
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) r[i][j] = 0.0f;
+      for (int j = 0; j < kVec; ++j) r[i][j] = 0.0f;
   }
   if (o) {
-    float ov[NC][VEC], gv[NC][VEC];
+    float ov[NC][kVec], gv[NC][kVec];
     float ss[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
         if (a.gate_cols > 1) load_vec<IO, TAIL>(gate + base + c, H, gv[i]);
       } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) ov[i][j] = 0.0f;
+        for (int j = 0; j < kVec; ++j) ov[i][j] = 0.0f;
       }
     }
     float scale = a.beta, dummy;
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
     for (int i = 0; i < NC; ++i) {
       const int skip = place<TAIL>(i, H).skip;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j)
+      for (int j = 0; j < kVec; ++j)
         if (j >= skip) ss[0] = __builtin_fmaf(ov[i][j], ov[i][j], ss[0]);
     }
     block_sum<1>(ss, sh[0]);
@@ -235,10 +235,10 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
       const Place at = place<TAIL>(i, H);
     const int c = at.col;
       if (!at.live) continue;
-      float w[VEC];
+      float w[kVec];
       load_vec<float, TAIL>(a.post + c, H, w);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
+      for (int j = 0; j < kVec; ++j) {
         float y = ov[i][j] * inv * w[j];
         if (a.gate_cols > 1) y *= sigmoid_fast(gv[i][j], dummy);
         r[i][j] = __builtin_fmaf(a.alpha, r[i][j], scale * y);
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
   for (int i = 0; i < NC; ++i) {
     const int skip = place<TAIL>(i, H).skip;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j)
+    for (int j = 0; j < kVec; ++j)
       if (j >= skip) ss[0] = __builtin_fmaf(r[i][j], r[i][j], ss[0]);
   }
   block_sum<1>(ss, sh[1]);
@@ -262,10 +262,10 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
     const Place at = place<TAIL>(i, H);
     const int c = at.col;
     if (!at.live) continue;
-    float w[VEC], x[VEC];
+    float w[kVec], x[kVec];
     load_vec<float, TAIL>(a.pre + c, H, w);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) x[j] = r[i][j] * inv * w[j];
+    for (int j = 0; j < kVec; ++j) x[j] = r[i][j] * inv * w[j];
     if (a.x) store_vec<IO, TAIL>(static_cast<IO*>(a.x) + base + c, H, x);
     if constexpr (!TAIL) {
       if (a.xq) {
@@ -307,24 +307,24 @@ template <typename IO, bool TAIL, int NC, bool O, bool DX, bool CG>
 __global__ __launch_bounds__(1024, NC == 1 && !CG ? 5 : 4) void norm_residual_backward(NormGradArgs a) {
   __shared__ float sh[2][3][kMaxWaves], sh2[1][kMaxWaves];
   extern __shared__ __attribute__((aligned(16))) float wts[];  // w_pre, then w_post
-  const int H = a.H, post = blockDim.x * NC * VEC;
+  const int H = a.H, post = blockDim.x * NC * kVec;
   const float rh = 1.0f / static_cast<float>(H);
-  float g_pre[NC][VEC], g_post[NC][VEC];
+  float g_pre[NC][kVec], g_post[NC][kVec];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     // a thread reads only what it wrote
     const Place pl = place<TAIL>(i, H);
     const int c = pl.col;
-    float w[VEC];
+    float w[kVec];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) g_pre[i][j] = g_post[i][j] = w[j] = 0.0f;
+    for (int j = 0; j < kVec; ++j) g_pre[i][j] = g_post[i][j] = w[j] = 0.0f;
     if (DX) {
       if (pl.live) load_vec<float, TAIL>(a.pre + c, H, w);
-      store_vec<float, false>(wts + pl.slot, VEC, w);
+      store_vec<float, false>(wts + pl.slot, kVec, w);
     }
     if (O) {
       if (pl.live) load_vec<float, TAIL>(a.post + c, H, w);
-      store_vec<float, false>(wts + post + pl.slot, VEC, w);
+      store_vec<float, false>(wts + post + pl.slot, kVec, w);
     }
   }
   struct Row {
@@ -360,10 +360,10 @@ __global__ __launch_bounds__(1024, NC == 1 && !CG ? 5 : 4) void norm_residual_ba
     for (int i = 0; i < NC; ++i) {
       const Place pl = place<TAIL>(i, H);
       const int c = pl.col;
-      float w[VEC];
-      if (DX) load_vec<float, false>(wts + pl.slot, VEC, w);
+      float w[kVec];
+      if (DX) load_vec<float, false>(wts + pl.slot, kVec, w);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
+      for (int j = 0; j < kVec; ++j) {
         if (j < pl.skip) continue;
         const float rv = x.r[i].get(j), ov = x.o[i].get(j);
         if (DX) {
@@ -384,11 +384,11 @@ __global__ __launch_bounds__(1024, NC == 1 && !CG ? 5 : 4) void norm_residual_ba
     for (int i = 0; i < NC; ++i) {
       const Place pl = place<TAIL>(i, H);
       const int c = pl.col;
-      float out[VEC], dgate[VEC], wp[VEC], wq[VEC];
-      if (DX) load_vec<float, false>(wts + pl.slot, VEC, wp);
-      if (O) load_vec<float, false>(wts + post + pl.slot, VEC, wq);
+      float out[kVec], dgate[kVec], wp[kVec], wq[kVec];
+      if (DX) load_vec<float, false>(wts + pl.slot, kVec, wp);
+      if (O) load_vec<float, false>(wts + post + pl.slot, kVec, wq);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
+      for (int j = 0; j < kVec; ++j) {
         float d = x.dr[i].get(j);
         if (DX) {
           const float rv = x.r[i].get(j), xv = x.dx[i].get(j);
@@ -426,10 +426,10 @@ __global__ __launch_bounds__(1024, NC == 1 && !CG ? 5 : 4) void norm_residual_ba
       for (int i = 0; i < NC; ++i) {
         const Place pl = place<TAIL>(i, H);
         const int c = pl.col;
-        float out[VEC], wq[VEC];
-        load_vec<float, false>(wts + post + pl.slot, VEC, wq);
+        float out[kVec], wq[kVec];
+        load_vec<float, false>(wts + post + pl.slot, kVec, wq);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
+        for (int j = 0; j < kVec; ++j) {
           const float dn = tg * x.dr[i].get(j), ov = x.o[i].get(j);
           g_post[i][j] = __builtin_fmaf(dn, ov * inv_o, g_post[i][j]);
           out[j] = inv_o * (wq[j] * dn) - ov * k_o;
@@ -486,7 +486,7 @@ struct RowShape {
 };
 RowShape row_shape(int H, bool pairs) {
   RowShape s;
-  const int chunks = static_cast<int>(ceil_div(H, VEC));
+  const int chunks = static_cast<int>(ceil_div(H, kVec));
   s.nc = chunks <= (pairs ? 256 : 1024) ? 1 : 2;
   s.threads = static_cast<int>(ceil_div(ceil_div(chunks, s.nc), kWave)) * kWave;
   return s;
@@ -507,8 +507,8 @@ int norm_grad_groups(int64_t T, int H) {
 }
 
 #define BEAM_NORM_SHAPES(RUN, H)                                          \
-  if ((H) % VEC == 0 && rs.nc == 1) RUN(false, 1);                        \
-  else if ((H) % VEC == 0) RUN(false, 2);                                 \
+  if ((H) % kVec == 0 && rs.nc == 1) RUN(false, 1);                        \
+  else if ((H) % kVec == 0) RUN(false, 2);                                 \
   else if (rs.nc == 1) RUN(true, 1);                                      \
   else RUN(true, 2)
 
@@ -532,7 +532,7 @@ hipError_t launch_norm_residual_backward(const NormGradArgs& a, int32_t dtype, f
   const RowShape rs = row_shape(a.H, false);
   const int n = norm_grad_groups(a.T, a.H);
   const dim3 grid(n), block(rs.threads);
-  const size_t lds = 2 * static_cast<size_t>(rs.threads) * rs.nc * VEC * sizeof(float);
+  const size_t lds = 2 * static_cast<size_t>(rs.threads) * rs.nc * kVec * sizeof(float);
   if (n > 0) {
 #define BEAM_NORM(V, N)                                                                       \
   do {                                                                                        \
