@@ -102,56 +102,6 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
   return sc > 0.0f ? sc : 1.0f;
 }
 
-// A block's scale s = e4m3_scale(amax) and the quotients v / s of its values,
-// bit for bit the binary32 divisions of the recipe, in three instructions a
-// quotient instead of about eleven.  With y = RN(1/b), q = RN(v y), the
-// remainder v - q b is exact in one fused multiply-add and RN(q + remainder y)
-// is the correctly rounded quotient; and y itself is RN(y0 + (1 - b y0) y0)
-// from an approximation y0 within an ulp (P. Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", 1990, which
-// excepts divisors whose significand is all ones), as long as nothing under-
-// or overflows: with amax from 2^-80 to 2^90 only a quotient below 2^-25 can,
-// which any rounding turns into the code 0.  Other blocks divide.  (Compared
-// with the divisions for every significand of amax.)
-struct BlockDivisor {
-  float s, y;
-  bool fast;
-  __device__ __forceinline__ explicit BlockDivisor(float amax) {
-    constexpr float kBy448 = 1.0f / 448.0f;
-    const float q = amax * kBy448;
-    s = __builtin_fmaf(__builtin_fmaf(q, 448.0f, -amax), -kBy448, q);
-    fast = amax >= 0x1p-80f && amax <= 0x1p90f && (__float_as_uint(s) & 0x7FFFFFu) != 0x7FFFFFu;
-    if (!fast) s = e4m3_scale(amax);
-    const float y0 = __builtin_amdgcn_rcpf(s);
-    y = __builtin_fmaf(__builtin_fmaf(-s, y0, 1.0f), y0, y0);
-  }
-  // With the remainder's and the reciprocal's signs turned, a quotient of -0
-  // keeps its sign.
-  __device__ __forceinline__ float quotient(float v) const {
-    const float q = v * y;
-    return __builtin_fmaf(__builtin_fmaf(q, s, -v), -y, q);
-  }
-  // The codes of four values no larger than the block's amax: quotients of at
-  // most 448 (1 + 2^-23), which need no clamp, where the scale is not
-  // subnormal.
-  __device__ __forceinline__ uint32_t codes(const float (&v)[4]) const {
-    if (fast) {
-      const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[0]), quotient(v[1]), 0, false);
-      return static_cast<uint32_t>(
-          __builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[2]), quotient(v[3]), lo, true));
-    }
-    // a NaN (also an infinity over the scale it makes) stays one
-    auto code = [&](float x) { return x == x ? sat448(x) : x; };
-    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(code(v[0] / s), code(v[1] / s), 0, false);
-    return static_cast<uint32_t>(
-        __builtin_amdgcn_cvt_pk_fp8_f32(code(v[2] / s), code(v[3] / s), lo, true));
-  }
-  __device__ __forceinline__ uint2 codes(const float (&v)[8]) const {
-    const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-    return make_uint2(codes(lo), codes(hi));
-  }
-};
-
 // silu(g) = g * sigmoid(g), the sigmoid from the hardware exponential and
 // reciprocal (each within about 1 ulp of binary32).  The bf16 paths round
 // silu(g) * u to 8 bits next, so an IEEE divide (about ten instructions more

@@ -129,54 +129,6 @@ struct Epilogue {
 hipError_t launch_combine(const Plan& p, const int32_t* slot_of,
                           const float* w, void* out, void* ws, hipStream_t s,
                           Timer* tm, const Epilogue* ep = nullptr);
-// norm.hip: the norms around a block, its gate and the residual stream
-struct NormArgs {
-  const void* o;          // [T, H] block output, or null: r' = residual
-  const float* post;      // [H]
-  const void* gate;       // [T, H] or [T, 1], or null
-  const float* pre;       // [H], or null: no x
-  const float* residual;  // [T, H]
-  float* residual_out;    // [T, H] (with o)
-  void* x;                // [T, H], or null
-  uint8_t* xq;            // [T, H] e4m3 codes, or null
-  float* xs;              // [T, H/128]
-  int H, gate_cols;       // gate_cols: 0 (none), 1 or H
-  float eps, alpha, beta;
-};
-struct NormGradArgs {
-  const void* o;
-  const float* post;
-  const void* gate;
-  const float* pre;
-  const float* r;      // [T, H] the forward's residual stream r'
-  const float* d_res;  // [T, H] gradient of r' from later, or null
-  const void* dx;      // [T, H] gradient of x, or null
-  float* d_residual;   // [T, H]
-  void* d_o;
-  void* d_gate;
-  float* part;         // workspace [groups][2][H]
-  int64_t T;
-  int H, gate_cols;
-  float eps, alpha, beta;
-};
-// Workgroups of the backward pass, each with its share of the weights' gradients.
-int norm_grad_groups(int64_t T, int H);
-int64_t norm_max_tokens(int H);  // a launch holds fewer than 2^32 threads
-constexpr int kNormMaxH = 16384;  // 1024 threads of 16 columns
-hipError_t launch_norm_residual(const NormArgs& a, int64_t T, int32_t dtype, hipStream_t s);
-hipError_t launch_norm_residual_backward(const NormGradArgs& a, int32_t dtype, float* d_pre,
-                                         float* d_post, hipStream_t s);
-// matmul_fp8.hip: dense e4m3 products and their operands' quantisation
-hipError_t launch_quant_2d(int64_t rows, int64_t cols, int32_t dtype, bool block, const void* v,
-                           uint8_t* q, float* s, uint8_t* qt, float* st, hipStream_t stream);
-// Byte offsets inside a tile of 256 rows are 32-bit; tiles are counted in 31.
-constexpr int64_t kMatmulMaxK = 1 << 22, kMatmulMaxRows = (1 << 23) - 128;
-constexpr int64_t kQuantMaxTiles = (int64_t{1} << 23) - 1;  // of 512 threads, under 2^32 in all
-constexpr int64_t kMatmulMaxOut = int64_t{1} << 38;
-hipError_t launch_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a, const float* sa,
-                              const int64_t* sa_stride, const uint8_t* b, const float* sb,
-                              const int64_t* sb_stride, bool rows, int32_t dtype, void* y,
-                              hipStream_t s);
 // fp8.hip
 hipError_t launch_quant_e4m3(int64_t rows, int64_t cols, int32_t dtype,
                              const void* v, uint8_t* q, float* scales,

@@ -2,8 +2,7 @@
 // launch.  See include/beam_moe.h for the contract of every entry point.
 #include <math.h>
 
-#include "common.h"
-#include "internal.h"
+#include "layer.h"
 
 using namespace beam;
 

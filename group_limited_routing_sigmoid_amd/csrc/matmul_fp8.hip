@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "grouped_tile.h"
+#include "layer.h"
 
 namespace beam {
 namespace {

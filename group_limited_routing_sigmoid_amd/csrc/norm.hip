@@ -17,8 +17,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "common.h"
-#include "internal.h"
+#include "layer.h"
 
 namespace beam {
 namespace {
