@@ -227,6 +227,14 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
       for (int j = 0; j < kVec; ++j)
         if (j >= skip) ss[0] = __builtin_fmaf(ov[i][j], ov[i][j], ss[0]);
     }
+    if (TAIL) {
+      // residual_out may be the residual: this thread has its columns before
+      // another one, past the sum's barrier, writes those that they share
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) asm volatile("" : "+v"(r[i][j]));
+    }
     block_sum<1>(ss, sh[0]);
     const float inv = 1.0f / sqrtf(ss[0] / static_cast<float>(H) + a.eps);
 #pragma unroll
@@ -372,6 +380,9 @@ __global__ __launch_bounds__(1024, NC == 1 && !CG ? 5 : 4) void norm_residual_ba
         if (O) s[2] = __builtin_fmaf(ov, ov, s[2]);
       }
     }
+    if (TAIL)  // as in the forward: d_residual may be d_residual_out
+#pragma unroll
+      for (int i = 0; i < NC; ++i) x.dr[i].repack();
     block_sum<3>(s, sh[par]);
 #pragma unroll
     for (int i = 0; i < NC; ++i) x.r[i].repack(), x.dx[i].repack(), x.o[i].repack();

@@ -295,3 +295,42 @@ def test_rows_that_end_inside_a_chunk(T, H, gate, dtype):
     for use in (dict(d_x=dc["d_x"]), dict(d_residual_out=dc["d_r"])):
         part = gl.norm_residual_backward(r, **use, **kw(dc))
         check_backward(c, dtype, r, part, use_r="d_residual_out" in use, use_x="d_x" in use)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H", [(4000, 31), (3000, 519), (2000, 5119), (600, 12345)])
+def test_odd_rows_in_place(T, H, dtype):
+    # threads of two waves share columns at a row's end: each has to have read
+    # them before the other writes
+    c = make(T, H, dtype, "token", True, H)
+    dc = on(device(), c)
+    r, x = gl.norm_residual(dc["residual"], **kw(dc))
+    want = gl.norm_residual_backward(r, dc["d_r"], dc["d_x"], **kw(dc))
+    for _ in range(3):
+        stream = dc["residual"].clone()
+        _, x2 = gl.norm_residual(stream, residual_out=stream, **kw(dc))
+        assert torch.equal(stream, r) and torch.equal(x2, x)
+        d = dc["d_r"].clone()
+        got = backward_in_place(r, d, dc)
+        assert torch.equal(d, want["d_residual"])
+        assert all(torch.equal(v, want[k]) for k, v in got.items())
+
+
+def backward_in_place(r, d, dc):
+    """norm_residual_backward through the C ABI with d_residual = d_residual_out."""
+    import ctypes
+    T, H = r.shape
+    out = {k: torch.empty_like(v) for k, v in (("d_o", dc["o"]), ("d_gate", dc["gate"]), ("d_pre_weight", dc["pre"]),
+                                               ("d_post_weight", dc["post"]))}
+    n = ctypes.c_size_t()
+    assert gl.lib().beam_moe_norm_residual_workspace_bytes(T, H, ctypes.byref(n)) == gl.OK
+    ws = torch.empty(n.value, dtype=torch.uint8, device=r.device)
+    st = gl.lib().beam_moe_norm_residual_backward(
+        T, H, gl.BF16 if dc["o"].dtype == torch.bfloat16 else gl.F32, dc["o"].data_ptr(), dc["post"].data_ptr(),
+        dc["gate"].data_ptr(), 1, dc["pre"].data_ptr(), EPS, ALPHA, BETA, r.data_ptr(), d.data_ptr(),
+        dc["d_x"].data_ptr(), d.data_ptr(), out["d_o"].data_ptr(), out["d_gate"].data_ptr(),
+        out["d_pre_weight"].data_ptr(), out["d_post_weight"].data_ptr(), ws.data_ptr(), n.value,
+        torch.cuda.current_stream().cuda_stream)
+    assert st == gl.OK
+    torch.cuda.synchronize()
+    return out
