@@ -334,3 +334,20 @@ def backward_in_place(r, d, dc):
     assert st == gl.OK
     torch.cuda.synchronize()
     return out
+
+
+def test_very_many_rows():
+    # the last of five million rows equal the same rows alone
+    T, H = 5_000_003, 9
+    g = torch.Generator(device=device()).manual_seed(1)
+    res = torch.randn(T, H, generator=g, device=device())
+    o = torch.randn(T, H, generator=g, device=device())
+    post, pre = torch.ones(H, device=device()), torch.ones(H, device=device())
+    r, x = gl.norm_residual(res, o, post, pre_weight=pre, alpha=ALPHA, beta=BETA)
+    n = slice(T - 7, T)
+    r2, x2 = gl.norm_residual(res[n].contiguous(), o[n].contiguous(), post, pre_weight=pre, alpha=ALPHA, beta=BETA)
+    assert torch.equal(r[n], r2) and torch.equal(x[n], x2)
+    got = gl.norm_residual_backward(r, res, x, o, post, pre_weight=pre, alpha=ALPHA, beta=BETA)
+    alone = gl.norm_residual_backward(r2, res[n].contiguous(), x2, o[n].contiguous(), post, pre_weight=pre,
+                                      alpha=ALPHA, beta=BETA)
+    assert torch.equal(got["d_o"][n], alone["d_o"]) and torch.equal(got["d_residual"][n], alone["d_residual"])
