@@ -23,22 +23,22 @@ namespace beam {
 namespace {
 
 constexpr int kMaxWaves = 16;
-
 constexpr int kVec = 8;  // columns of a thread's chunk
 
 // Rows of a multiple of 8 columns start 16-byte aligned and end with a chunk
-// (TAIL false).  Others (TAIL true) start anywhere, and their last chunk is the
+// (TAIL 0).  Others (TAIL 1) start anywhere, and their last chunk is the
 // row's last 8 columns: it shares some with the chunk before, of which both
 // threads write the same values and only the other one's count in sums.  The
 // card reads and writes 16 bytes at any address that the type allows, so every
-// row goes in whole chunks.  (8,192 rows of 5,119, bf16, forward with a gate for
-// each channel: 124 us, with gradients 280, against 114 and 259 for 5,120; value
-// by value 296 and 1,489.)
+// row goes in whole chunks, but for rows of fewer than 8 columns (TAIL 2).
+// (8,192 rows of 5,119, bf16, forward with a gate for each channel: 124 us, with
+// gradients 276, against 115 and 258 for 5,120; value by value 296 and 1,489.)
 struct Place {
-  int slot, col, skip;  // first column by the thread's number, of its chunk, and how many are not its own
+  int slot, col;  // first column by the thread's number and of its chunk
+  int skip;       // columns of the chunk that another thread's sums count
   bool live;
 };
-template <bool TAIL>
+template <int TAIL>
 __device__ __forceinline__ Place place(int i, int H) {
   Place p;
   p.slot = (threadIdx.x + i * blockDim.x) * kVec;
@@ -50,14 +50,14 @@ __device__ __forceinline__ Place place(int i, int H) {
 
 typedef u32x4 u32x4_2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_4 __attribute__((aligned(4)));
-template <typename IO, bool TAIL>
+template <typename IO, int TAIL>
 struct Chunk {
   static constexpr int kWords = kVec * static_cast<int>(sizeof(IO)) / 16;
   using Word = std::conditional_t<!TAIL, u32x4, std::conditional_t<sizeof(IO) == 2, u32x4_2, u32x4_4>>;
   u32x4 w[kWords];  // as they lie in memory (bf16 ones two to a register)
   // n: columns of the row; of fewer than 8 the others count as zeros.
   __device__ __forceinline__ void load(const IO* p, int n) {
-    if (!TAIL || n >= kVec) {
+    if (TAIL != 2) {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) w[i] = *reinterpret_cast<const Word*>(p + i * (kVec / kWords));
     } else {
@@ -90,7 +90,7 @@ struct Chunk {
   }
 };
 
-template <typename IO, bool TAIL>
+template <typename IO, int TAIL>
 __device__ __forceinline__ void load_vec(const IO* p, int n, float (&v)[kVec]) {
   Chunk<IO, TAIL> c;
   c.load(p, n);
@@ -98,7 +98,7 @@ __device__ __forceinline__ void load_vec(const IO* p, int n, float (&v)[kVec]) {
   for (int j = 0; j < kVec; ++j) v[j] = c.get(j);
 }
 
-template <typename IO, bool TAIL>
+template <typename IO, int TAIL>
 __device__ __forceinline__ void store_vec(IO* p, int n, const float (&v)[kVec]) {
   Chunk<IO, TAIL> c;
   if constexpr (sizeof(IO) == 2) {
@@ -110,7 +110,7 @@ __device__ __forceinline__ void store_vec(IO* p, int n, const float (&v)[kVec]) 
 #pragma unroll
     for (int j = 0; j < kVec; ++j) c.w[j / 4][j % 4] = __float_as_uint(v[j]);
   }
-  if (!TAIL || n >= kVec) {
+  if (TAIL != 2) {
 #pragma unroll
     for (int i = 0; i < Chunk<IO, TAIL>::kWords; ++i)
       *reinterpret_cast<typename Chunk<IO, TAIL>::Word*>(p + i * (kVec / Chunk<IO, TAIL>::kWords)) = c.w[i];
@@ -184,7 +184,7 @@ __device__ __forceinline__ float sigmoid_fast(float g, float& d) {
   return g >= 0.0f ? r : t * r;
 }
 
-template <typename IO, bool TAIL, int NC>
+template <typename IO, int TAIL, int NC>
 __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
   __shared__ float sh[2][1][kMaxWaves];
   const int64_t t = blockIdx.x, base = t * a.H;
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
 // ahead instead: 165 us; half the threads with twice the columns: 186 us).
 // O: there is a block output; DX: there is a gradient of x; CG: a gate for
 // each channel (or none, or one a token, in the other form).
-template <typename IO, bool TAIL, int NC, bool O, bool DX, bool CG>
+template <typename IO, int TAIL, int NC, bool O, bool DX, bool CG>
 __global__ __launch_bounds__(1024, NC == 1 && !CG ? 5 : 4) void norm_residual_backward(NormGradArgs a) {
   __shared__ float sh[2][3][kMaxWaves], sh2[1][kMaxWaves];
   extern __shared__ __attribute__((aligned(16))) float wts[];  // w_pre, then w_post
@@ -327,11 +327,11 @@ __global__ __launch_bounds__(1024, NC == 1 && !CG ? 5 : 4) void norm_residual_ba
     for (int j = 0; j < kVec; ++j) g_pre[i][j] = g_post[i][j] = w[j] = 0.0f;
     if (DX) {
       if (pl.live) load_vec<float, TAIL>(a.pre + c, H, w);
-      store_vec<float, false>(wts + pl.slot, kVec, w);
+      store_vec<float, 0>(wts + pl.slot, kVec, w);
     }
     if (O) {
       if (pl.live) load_vec<float, TAIL>(a.post + c, H, w);
-      store_vec<float, false>(wts + post + pl.slot, kVec, w);
+      store_vec<float, 0>(wts + post + pl.slot, kVec, w);
     }
   }
   struct Row {
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(1024, NC == 1 && !CG ? 5 : 4) void norm_residual_ba
       const Place pl = place<TAIL>(i, H);
       const int c = pl.col;
       float w[kVec];
-      if (DX) load_vec<float, false>(wts + pl.slot, kVec, w);
+      if (DX) load_vec<float, 0>(wts + pl.slot, kVec, w);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         if (j < pl.skip) continue;
@@ -395,8 +395,8 @@ __global__ __launch_bounds__(1024, NC == 1 && !CG ? 5 : 4) void norm_residual_ba
       const Place pl = place<TAIL>(i, H);
       const int c = pl.col;
       float out[kVec], dgate[kVec], wp[kVec], wq[kVec];
-      if (DX) load_vec<float, false>(wts + pl.slot, kVec, wp);
-      if (O) load_vec<float, false>(wts + post + pl.slot, kVec, wq);
+      if (DX) load_vec<float, 0>(wts + pl.slot, kVec, wp);
+      if (O) load_vec<float, 0>(wts + post + pl.slot, kVec, wq);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         float d = x.dr[i].get(j);
@@ -437,7 +437,7 @@ __global__ __launch_bounds__(1024, NC == 1 && !CG ? 5 : 4) void norm_residual_ba
         const Place pl = place<TAIL>(i, H);
         const int c = pl.col;
         float out[kVec], wq[kVec];
-        load_vec<float, false>(wts + post + pl.slot, kVec, wq);
+        load_vec<float, 0>(wts + post + pl.slot, kVec, wq);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
           const float dn = tg * x.dr[i].get(j), ov = x.o[i].get(j);
@@ -517,10 +517,11 @@ int norm_grad_groups(int64_t T, int H) {
 }
 
 #define BEAM_NORM_SHAPES(RUN, H)                                          \
-  if ((H) % kVec == 0 && rs.nc == 1) RUN(false, 1);                        \
-  else if ((H) % kVec == 0) RUN(false, 2);                                 \
-  else if (rs.nc == 1) RUN(true, 1);                                      \
-  else RUN(true, 2)
+  if ((H) % kVec == 0 && rs.nc == 1) RUN(0, 1);                           \
+  else if ((H) % kVec == 0) RUN(0, 2);                                    \
+  else if ((H) < kVec) RUN(2, 1);                                         \
+  else if (rs.nc == 1) RUN(1, 1);                                         \
+  else RUN(1, 2)
 
 hipError_t launch_norm_residual(const NormArgs& a, int64_t T, int32_t dtype, hipStream_t s) {
   const RowShape rs = row_shape(a.H, T >= 1024);
