@@ -447,10 +447,12 @@ __global__ __launch_bounds__(1024, NC == 1 && !CG ? 5 : 4) void norm_residual_ba
         if (pl.live) store_vec<IO, TAIL>(static_cast<IO*>(a.d_o) + base + c, H, out);
       }
     }
-    if (!a.d_res) {
+    // Chunks that the next token's loads do not replace: without d_res, and
+    // those past the row's end, where a token whose sums are not finite leaves
+    // NaN that would reach the next ones' sums.
 #pragma unroll
-      for (int i = 0; i < NC; ++i) x.dr[i].zero();
-    }
+    for (int i = 0; i < NC; ++i)
+      if (!a.d_res || !place<TAIL>(i, H).live) x.dr[i].zero();
   }
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * H;
 #pragma unroll
