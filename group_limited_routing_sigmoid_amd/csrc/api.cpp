@@ -39,8 +39,51 @@ void timer_end(Timer* t, hipStream_t s) {
   ++t->count;
 }
 
-int make_plan(const beam_moe_desc* d, int64_t T, Plan* p) {
-  const int st = beam_moe_validate(d, T);
+// A descriptor's fields, and T against what the entry point holds: slots of the
+// widest rows, or (slots false) only the tokens' logits and choices.
+static int check_desc(const beam_moe_desc* d, int64_t T, bool slots) {
+  if (!d || T < 0) return BEAM_ERR_INVALID_ARG;
+  const uint32_t tiles = BEAM_TILE_64 | BEAM_TILE_128 | BEAM_TILE_160 | BEAM_TILE_256;
+  const uint32_t known = BEAM_ROUTE_LOGITS_IN | BEAM_PATH_STREAM | BEAM_PATH_GROUPED |
+                         BEAM_ROUTE_SOFTMAX | BEAM_ROUTE_UNNORMED | tiles;
+  if (d->flags & ~known) return BEAM_ERR_INVALID_ARG;
+  const uint32_t tf = d->flags & tiles;
+  if (tf & (tf - 1)) return BEAM_ERR_INVALID_ARG;  // at most one tile height
+  if ((d->flags & BEAM_PATH_STREAM) && (d->flags & BEAM_PATH_GROUPED))
+    return BEAM_ERR_INVALID_ARG;
+  if (d->act_dtype != BEAM_F32 && d->act_dtype != BEAM_BF16) return BEAM_ERR_INVALID_ARG;
+  if (d->weight_dtype != BEAM_F32 && d->weight_dtype != BEAM_BF16 &&
+      d->weight_dtype != BEAM_FP8_E4M3 && d->weight_dtype != BEAM_MXFP4)
+    return BEAM_ERR_INVALID_ARG;
+  if (!(d->routed_scale > 0.0f) || !isfinite(d->routed_scale)) return BEAM_ERR_INVALID_ARG;
+  const int E = d->n_experts, G = d->n_groups;
+  if (E < 1 || E > 1024 || G < 1 || G > 64 || E % G) return BEAM_ERR_UNSUPPORTED;
+  const int gs = E / G;
+  if (gs > 64) return BEAM_ERR_UNSUPPORTED;
+  if (d->topk_groups < 1 || d->topk_groups > G) return BEAM_ERR_UNSUPPORTED;
+  if (d->top_k < 1 || d->top_k > 16 || d->top_k > d->topk_groups * gs)
+    return BEAM_ERR_UNSUPPORTED;
+  if (d->group_score_topn < 1 || d->group_score_topn > 2 || d->group_score_topn > gs)
+    return BEAM_ERR_UNSUPPORTED;
+  if (d->hidden < 128 || d->hidden % 128 || d->intermediate < 128 ||
+      d->intermediate % 128)
+    return BEAM_ERR_UNSUPPORTED;
+  if (d->weight_dtype == BEAM_F32 && d->act_dtype != BEAM_F32) return BEAM_ERR_UNSUPPORTED;
+  if (d->weight_dtype != BEAM_F32 && d->act_dtype != BEAM_BF16) return BEAM_ERR_UNSUPPORTED;
+  if (T > kRouteMaxTokens) return BEAM_ERR_UNSUPPORTED;
+  // slot indices and per-slot element offsets are 32-bit
+  const int64_t S = T * static_cast<int64_t>(d->top_k);
+  const int64_t wide = d->hidden > d->intermediate ? d->hidden : d->intermediate;
+  if (slots && S * wide > 0x7FFFFFFF) return BEAM_ERR_UNSUPPORTED;
+  // element (bf16, fp32) and byte (e4m3, 4-bit) offsets inside one expert's
+  // weights are 32-bit: its gate/up matrix holds 2*I*H values
+  if (2 * static_cast<int64_t>(d->intermediate) * d->hidden > 0x7FFFFFFF)
+    return BEAM_ERR_UNSUPPORTED;
+  return BEAM_OK;
+}
+
+int make_plan(const beam_moe_desc* d, int64_t T, Plan* p, bool slots) {
+  const int st = check_desc(d, T, slots);
   if (st != BEAM_OK) return st;
   memset(p, 0, sizeof(*p));
   p->H = d->hidden;
@@ -198,45 +241,7 @@ const char* beam_status_string(int status) {
   }
 }
 
-int beam_moe_validate(const beam_moe_desc* d, int64_t T) {
-  if (!d || T < 0) return BEAM_ERR_INVALID_ARG;
-  const uint32_t tiles = BEAM_TILE_64 | BEAM_TILE_128 | BEAM_TILE_160 | BEAM_TILE_256;
-  const uint32_t known = BEAM_ROUTE_LOGITS_IN | BEAM_PATH_STREAM | BEAM_PATH_GROUPED |
-                         BEAM_ROUTE_SOFTMAX | BEAM_ROUTE_UNNORMED | tiles;
-  if (d->flags & ~known) return BEAM_ERR_INVALID_ARG;
-  const uint32_t tf = d->flags & tiles;
-  if (tf & (tf - 1)) return BEAM_ERR_INVALID_ARG;  // at most one tile height
-  if ((d->flags & BEAM_PATH_STREAM) && (d->flags & BEAM_PATH_GROUPED))
-    return BEAM_ERR_INVALID_ARG;
-  if (d->act_dtype != BEAM_F32 && d->act_dtype != BEAM_BF16) return BEAM_ERR_INVALID_ARG;
-  if (d->weight_dtype != BEAM_F32 && d->weight_dtype != BEAM_BF16 &&
-      d->weight_dtype != BEAM_FP8_E4M3 && d->weight_dtype != BEAM_MXFP4)
-    return BEAM_ERR_INVALID_ARG;
-  if (!(d->routed_scale > 0.0f) || !isfinite(d->routed_scale)) return BEAM_ERR_INVALID_ARG;
-  const int E = d->n_experts, G = d->n_groups;
-  if (E < 1 || E > 1024 || G < 1 || G > 64 || E % G) return BEAM_ERR_UNSUPPORTED;
-  const int gs = E / G;
-  if (gs > 64) return BEAM_ERR_UNSUPPORTED;
-  if (d->topk_groups < 1 || d->topk_groups > G) return BEAM_ERR_UNSUPPORTED;
-  if (d->top_k < 1 || d->top_k > 16 || d->top_k > d->topk_groups * gs)
-    return BEAM_ERR_UNSUPPORTED;
-  if (d->group_score_topn < 1 || d->group_score_topn > 2 || d->group_score_topn > gs)
-    return BEAM_ERR_UNSUPPORTED;
-  if (d->hidden < 128 || d->hidden % 128 || d->intermediate < 128 ||
-      d->intermediate % 128)
-    return BEAM_ERR_UNSUPPORTED;
-  if (d->weight_dtype == BEAM_F32 && d->act_dtype != BEAM_F32) return BEAM_ERR_UNSUPPORTED;
-  if (d->weight_dtype != BEAM_F32 && d->act_dtype != BEAM_BF16) return BEAM_ERR_UNSUPPORTED;
-  // slot indices and per-slot element offsets are 32-bit
-  const int64_t S = T * static_cast<int64_t>(d->top_k);
-  const int64_t wide = d->hidden > d->intermediate ? d->hidden : d->intermediate;
-  if (S * wide > 0x7FFFFFFF) return BEAM_ERR_UNSUPPORTED;
-  // element (bf16, fp32) and byte (e4m3, 4-bit) offsets inside one expert's
-  // weights are 32-bit: its gate/up matrix holds 2*I*H values
-  if (2 * static_cast<int64_t>(d->intermediate) * d->hidden > 0x7FFFFFFF)
-    return BEAM_ERR_UNSUPPORTED;
-  return BEAM_OK;
-}
+int beam_moe_validate(const beam_moe_desc* d, int64_t T) { return check_desc(d, T, true); }
 
 int beam_moe_workspace_bytes(const beam_moe_desc* d, int64_t T, size_t* bytes) {
   if (!bytes) return BEAM_ERR_INVALID_ARG;
@@ -252,10 +257,10 @@ int beam_moe_route(const beam_moe_desc* d, int64_t T, const void* x,
                    int32_t* topk_idx, float* topk_w, void* workspace,
                    size_t ws_bytes, void* stream) {
   Plan p;
-  int st = make_plan(d, T, &p);
+  const bool lin = d && (d->flags & BEAM_ROUTE_LOGITS_IN);
+  int st = make_plan(d, T, &p, !lin);
   if (st != BEAM_OK) return st;
   if (T == 0) return BEAM_OK;
-  const bool lin = d->flags & BEAM_ROUTE_LOGITS_IN;
   if (!topk_idx || !topk_w) return BEAM_ERR_INVALID_ARG;
   if (lin ? !logits : (!x || !w_router)) return BEAM_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_router) || !aligned16(bias) ||
@@ -275,7 +280,7 @@ int beam_moe_route_backward(const beam_moe_desc* d, int64_t T, const float* logi
                             const int32_t* topk_idx, const float* d_topk_w,
                             float* d_logits, void* stream) {
   Plan p;
-  int st = make_plan(d, T, &p);
+  const int st = make_plan(d, T, &p, false);
   if (st != BEAM_OK) return st;
   if (T == 0) return BEAM_OK;
   if (!logits || !topk_idx || !d_topk_w || !d_logits) return BEAM_ERR_INVALID_ARG;

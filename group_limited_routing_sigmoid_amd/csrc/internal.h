@@ -56,8 +56,13 @@ void timer_end(Timer* t, hipStream_t s);
 static inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 static inline int hip_status(hipError_t e) { return e == hipSuccess ? BEAM_OK : BEAM_ERR_HIP; }
 
-// Builds the plan; returns a beam_status.
-int make_plan(const beam_moe_desc* d, int64_t T, Plan* p);
+// Tokens of a routing launch: one wave each, four a workgroup, and fewer than
+// 2^32 threads in all.
+constexpr int64_t kRouteMaxTokens = 4 * ((int64_t{1} << 24) - 1);
+
+// Builds the plan; returns a beam_status.  slots false: for entry points that
+// hold no slots (routing from given logits and its gradient).
+int make_plan(const beam_moe_desc* d, int64_t T, Plan* p, bool slots = true);
 
 template <typename P>
 static inline P* ws_at(void* ws, size_t off) {

@@ -118,7 +118,9 @@ const char* beam_status_string(int status);
  * H % 128 == 0 and I % 128 == 0, routed_scale finite and > 0, T >= 0,
  * T*K*max(H, I) < 2^31 (52,428 tokens for the Beam layer), 2*I*H < 2^31
  * (one expert's gate/up matrix is addressed with 32-bit offsets).  Returns
- * BEAM_OK or the first error found. */
+ * BEAM_OK or the first error found.  beam_moe_route with BEAM_ROUTE_LOGITS_IN
+ * and beam_moe_route_backward hold no slots: they take T up to 67,108,860
+ * whatever H and I are. */
 int beam_moe_validate(const beam_moe_desc* desc, int64_t T);
 
 /* Bytes of workspace beam_moe_forward / beam_moe_route need for T tokens.
