@@ -272,6 +272,16 @@ def _arg(name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple,
     raise ValueError(f"{name}: tensors passed to the HIP library must be contiguous")
 
 
+def _floats(name: str, t: torch.Tensor, dev: int, shape: tuple, more: bool = False) -> int:
+    """As _arg for fp32 values that are read or written in order: a tensor of
+    any shape with as many elements (`more`: or with room for more)."""
+    n = t.numel() - math.prod(shape)
+    if (t.dtype is torch.float32 and (n == 0 or (more and n > 0)) and t.get_device() == dev >= 0
+            and t.is_contiguous()):
+        return t.data_ptr()
+    return _arg(name, t, dev, torch.float32, shape)  # raises
+
+
 # torch.empty parses its arguments for half of its time (1.3 us): on the current
 # device and stream the allocation that torch's compiled graphs call (0.75 us)
 # is used where this torch has it
@@ -335,17 +345,19 @@ def route(desc: Desc, x: Optional[torch.Tensor], w_router: Optional[torch.Tensor
           workspace: Optional[Workspace] = None, stream=None):
     """beam_moe_route.  Returns (topk_idx [T,K] int32, topk_w [T,K] fp32,
     logits [T,E] fp32).  With ROUTE_LOGITS_IN in desc.flags, `logits` is the
-    input and x / w_router may be None.  ROUTE_SOFTMAX and ROUTE_UNNORMED choose
-    the scores and the weights."""
+    input and x / w_router may be None; without it `logits` may be a buffer for
+    them, also one with room for more.  bias and logits are contiguous fp32 on
+    x's GPU and may have other shapes of the same size.  ROUTE_SOFTMAX and
+    ROUTE_UNNORMED choose the scores and the weights."""
     lin = bool(desc.flags & ROUTE_LOGITS_IN)
     ref = logits if lin else x
     T, E, device, dev = ref.shape[0], desc.n_experts, ref.device, ref.get_device()
     on = _on(stream, dev)
     px, pr = (None, None) if lin else (_addr(x), _addr(w_router))
-    pb = None if bias is None else _arg("bias", bias, dev, torch.float32, (E,))
+    pb = None if bias is None else _floats("bias", bias, dev, (E,))
     if logits is None:
         logits = _empty(on, device, torch.float32, T, E)
-    pl = _arg("logits", logits, dev, torch.float32, (T, E))
+    pl = _floats("logits", logits, dev, (T, E), not lin)
     idx = _empty(on, device, torch.int32, T, desc.top_k)
     w = _empty(on, device, torch.float32, T, desc.top_k)
     # routing from given logits uses no scratch memory
