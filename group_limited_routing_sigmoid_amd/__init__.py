@@ -324,9 +324,10 @@ def _run(fn, what: str, on, dev: int, tensors, *args):
         return
     stream = on
     raw = _raw_stream(dev)
+    # every GPU's default stream has the same handle
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"{what}: a stream of {stream.device} for tensors on cuda:{dev}")
     if stream is not None and stream.cuda_stream != raw:
-        if stream.device.index != dev:
-            raise ValueError(f"{what}: a stream of {stream.device} for tensors on cuda:{dev}")
         raw = stream.cuda_stream
         for t in tensors:
             if t is not None:
