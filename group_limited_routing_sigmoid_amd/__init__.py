@@ -220,6 +220,17 @@ class Workspace:
 _default_ws = {}
 
 
+def _capturing(stream, device) -> bool:
+    """Whether a call's stream (None: `device`'s current one) is being captured
+    into a graph; torch answers for the current device's current stream."""
+    if stream is None:
+        if device.index == _current_device():
+            return torch._C._cuda_isCurrentStreamCapturing()
+        stream = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        return torch._C._cuda_isCurrentStreamCapturing()
+
+
 def _scratch(n: int, workspace: Optional[Workspace], device, stream=None):
     if n == 0:
         return None
@@ -227,12 +238,7 @@ def _scratch(n: int, workspace: Optional[Workspace], device, stream=None):
         return workspace.get(n, _torch_stream(stream, device))
     # A call that is being captured takes memory of its graph instead: graphs
     # are captured on one stream and replayed on any.
-    if stream is None:
-        capturing = torch._C._cuda_isCurrentStreamCapturing()
-    else:
-        with torch.cuda.stream(stream):
-            capturing = torch._C._cuda_isCurrentStreamCapturing()
-    if capturing:
+    if _capturing(stream, device):
         return Workspace(device).get(n, _torch_stream(stream, device))
     key = (device.index, _raw_stream(device.index) if stream is None else stream.cuda_stream)
     workspace = _default_ws.get(key)

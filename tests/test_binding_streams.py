@@ -1,5 +1,6 @@
 """Which stream a call is given to, without a GPU: the binding's stream queries
 are replaced by a machine of two GPUs whose current streams are set here."""
+import contextlib
 import types
 
 import pytest
@@ -48,3 +49,28 @@ def test_stream_of_another_gpu_is_refused(two_gpus, handle):
     # also its default stream, whose handle every GPU shares
     with pytest.raises(ValueError, match="a stream of cuda:1 for tensors on cuda:0"):
         call(stream(1, handle), 0, Tensor())
+
+
+def test_capture_is_asked_of_the_calls_own_stream(two_gpus, monkeypatch):
+    # GPU 0 is current; a stream of GPU 1, and its current one, may be captured
+    now = [stream(0, 0)]
+    captured = set()
+
+    @contextlib.contextmanager
+    def on(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    two_gpus[1] = 5
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: stream(d.index, two_gpus[d.index]))
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing",
+                        lambda: (now[-1].device.index, now[-1].cuda_stream) in captured, raising=False)
+    gpu = [torch.device("cuda", i) for i in range(2)]
+    for where, want in ((set(), (False, False, False)), ({(0, 0)}, (True, False, False)),
+                        ({(1, 5)}, (False, True, False)), ({(1, 9)}, (False, False, True))):
+        captured.clear()
+        captured.update(where)
+        got = (gl._capturing(None, gpu[0]), gl._capturing(None, gpu[1]), gl._capturing(stream(1, 9), gpu[1]))
+        assert got == want
