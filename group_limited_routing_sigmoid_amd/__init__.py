@@ -517,7 +517,8 @@ def matmul_e4m3(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch.
     """beam_moe_matmul_e4m3: a b^T [M,N] in `dtype` from e4m3 codes a [M,K] and
     b [N,K] (uint8), K a multiple of 128, with scales s_a [M,K/128] and s_b
     [ceil(N/128),K/128] (128 x 128 blocks) or [N,K/128] (rows of b), which may
-    have any strides."""
+    have any strides from a 16-byte aligned first element.  The product of two
+    scales that meet has to be 0 or a normal fp32 number."""
     if a.dim() != 2 or b.dim() != 2:
         raise ValueError(f"shapes {tuple(a.shape)} and {tuple(b.shape)}, expected [M, K] and [N, K]")
     (M, K), N = a.shape, b.shape[0]

@@ -328,6 +328,9 @@ int beam_moe_forward_residual(const beam_moe_desc* desc, int64_t T, const void* 
  *   y   device [M, N] dtype (BEAM_F32 or BEAM_BF16)
  * K % 128 == 0, K <= 2^22, M, N < 2^23 - 127, M * N <= 2^38
  * (BEAM_ERR_UNSUPPORTED otherwise).
+ * The two scales of a block are multiplied in binary32 before they meet its
+ * sum, so their product has to be 0 or of a size from 2^-126 to below 2^128
+ * (smaller ones lose bits, larger ones give infinities and NaN).
  * K == 0 gives zeros.  A NaN code (0x7F, 0xFF) makes its row's or column's
  * results NaN.
  * A linear layer's training step is three of them on what
