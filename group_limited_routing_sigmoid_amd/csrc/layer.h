@@ -65,8 +65,9 @@ hipError_t launch_matmul_e4m3(int64_t M, int64_t N, int64_t K, const uint8_t* a,
 // elementary functions on the IBM RISC System/6000 processor", 1990, which
 // excepts divisors whose significand is all ones), as long as nothing under-
 // or overflows: with amax from 2^-80 to 2^90 only a quotient below 2^-25 can,
-// which any rounding turns into the code 0.  Other blocks divide.  (Compared
-// with the divisions for every significand of amax.)
+// which any rounding turns into the code 0.  Other blocks divide.  (Tested
+// for every significand of amax: the scale's bits, and the codes of values on
+// and beside the midpoints of neighbouring codes.)
 struct BlockDivisor {
   float s, y;
   bool fast;
