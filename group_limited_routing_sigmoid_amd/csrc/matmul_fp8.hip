@@ -112,14 +112,6 @@ __device__ __forceinline__ void put4(uint16_t* p, float a, float b, float c, flo
                  f32_to_bf16_bits(c) | static_cast<uint32_t>(f32_to_bf16_bits(d)) << 16);
 }
 
-// Orders a wave's LDS writes before its other lanes' reads (a wave's LDS
-// operations complete in order; this holds the compiler to it).
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // A wave's fragments to y, 32 rows at a time through its own room in LDS, so
 // that they leave as whole runs of y's rows (a lane's own values lie in one
 // row, a column apart from its neighbour's: stored directly they took a third
@@ -140,7 +132,7 @@ __device__ __forceinline__ void store_tile(OUT* room, int lane, const f32x4 (&ac
       for (int n = 0; n < FN; ++n)
         put4(room + (16 * i + lane % 16) * kPitch + 16 * n + 4 * (lane / 16), acc[n][m + i][0],
              acc[n][m + i][1], acc[n][m + i][2], acc[n][m + i][3]);
-    wave_sync();
+    wave_order();
     const int row0 = rw + 16 * m;
     if (vec) {
 #pragma unroll
@@ -157,7 +149,7 @@ __device__ __forceinline__ void store_tile(OUT* room, int lane, const f32x4 (&ac
         if (row0 + r <= mr && cw + c <= nr) y[(m0 + row0 + r) * N + n0 + cw + c] = v;
       }
     }
-    wave_sync();
+    wave_order();
   }
 }
 
@@ -173,6 +165,11 @@ __device__ __forceinline__ void store_tile(OUT* room, int lane, const f32x4 (&ac
 // multiplied.  Each group copies its own block; a wave issues the same number
 // of copies for every block, so "a stage has landed" is a count of
 // outstanding copies.
+// Few rows are bound by that chain (fill the ring, five or ten stages, join the
+// groups, store), not by the host: called back to back from C, 1 x 5,120 x
+// 5,120 takes 7.7 us on one set of operands, which stay in the last-level cache
+// (3.4 TB/s), and 8.7 over sixteen; 64 x 5,125 x 2,560, 161 workgroups, 6.7 and
+// 7.5 (6.3 and 7.1 with 5,120 outputs, whose rows are stored in whole pieces).
 template <int BM, int BN, int KS, int WM, int WN, int ST, bool ROWS, typename OUT>
 __global__ __launch_bounds__(64 * KS * WM * WN) void matmul_tile(
     const uint8_t* __restrict__ a, Scales sa, const uint8_t* __restrict__ b, Scales sb,
@@ -346,6 +343,13 @@ __global__ __launch_bounds__(64 * KS * WM * WN) void matmul_tile(
 // copies are spread over the products (nine instructions a wave: issued
 // together they fill the unit's texture path and hold up every wave's LDS
 // reads).
+//
+// 8,192 x 5,120 x 5,120 in bf16: 207 us on one set of operands, 217 over three
+// (2.0 PFLOP/s; the instruction alone runs at 4.0), the matrix cores busy 42% of
+// the cycles: copies, scaling and the wait at a block's end delay products
+// instead of running beside them.  With any one of them left out, on codes of
+// zero, so that the clock stays: 141, 152 and 139 us against 174.  Real codes
+// cost the clock under power another 23.
 //
 // Order of the tiles: workgroups are dealt round-robin to the 8 XCDs, each
 // with its own L2, so workgroup b takes the (b / 8) % 32-th tile of chunk
@@ -580,7 +584,8 @@ __device__ __forceinline__ float row_max(float v) {
 // block-major, 128 consecutive words a tile, as the products' copies read
 // them.  4,099 x 5,120 bf16 both ways, 84 MB: 22.5 us (27 with the columns'
 // maxima of the eight waves read by every thread, 38 with the plain division
-// and half the threads).
+// and half the threads).  Rows that are not a multiple of 8 columns are read
+// value by value: 4,099 x 5,125 takes 41 us.
 template <typename IO, bool BLOCK, bool VEC>
 __global__ __launch_bounds__(512) void quant_2d(const IO* __restrict__ v, int64_t rows,
                                                 int64_t cols, int64_t ncb, uint8_t* __restrict__ q,

@@ -207,7 +207,7 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const Place at = place<TAIL>(i, H);
-    const int c = at.col;
+      const int c = at.col;
       if (at.live) {
         load_vec<IO, TAIL>(o + c, H, ov[i]);
         if (a.gate_cols > 1) load_vec<IO, TAIL>(gate + base + c, H, gv[i]);
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const Place at = place<TAIL>(i, H);
-    const int c = at.col;
+      const int c = at.col;
       if (!at.live) continue;
       float w[kVec];
       load_vec<float, TAIL>(a.post + c, H, w);
@@ -308,6 +308,11 @@ __global__ __launch_bounds__(1024) void norm_residual(NormArgs a) {
 // tokens, bf16, one gate a token, 160 us, 4.7 TB/s (everything unpacked in
 // registers, one workgroup a unit: 181 us; the next token's loads issued
 // ahead instead: 165 us; half the threads with twice the columns: 186 us).
+// With a gate for each channel 197 us, the same 4.7 TB/s.  Rows of more than
+// 8,192 columns take two chunks a thread, whose sums, weights' shares and packed
+// inputs exceed the 128 registers that 1,024 threads leave: up to 35 of them
+// spill without a gate a channel (8,192 x 16,384, one gate a token: 507 us, 4.8
+// TB/s all the same), 64 to 99 with one (1,114 us, 2.7 TB/s).
 // O: there is a block output; DX: there is a gradient of x; CG: a gate for
 // each channel (or none, or one a token, in the other form).
 template <typename IO, int TAIL, int NC, bool O, bool DX, bool CG>

@@ -226,14 +226,6 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
       __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, true));
 }
 
-// Orders a wave's LDS writes before its other lanes' reads (a wave's LDS
-// operations complete in order; this holds the compiler to it).
-__device__ __forceinline__ void wave_order() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // Maximum over the wave, returned uniform.
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   v = max(v, dpp<0xB1>(v));   // quad_perm(1, 0, 3, 2)
