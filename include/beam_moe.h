@@ -149,8 +149,8 @@ int beam_moe_workspace_bytes(const beam_moe_desc* desc, int64_t T,
  * With BEAM_ROUTE_SOFTMAX the scores are s_e = exp(l_e - max l) / sum exp(l_j
  * - max l) over all E logits, evaluated in binary64 and rounded once to
  * binary32; a logit of -infinity gives the score 0, a row of only those has
- * scores 0, and a NaN or +infinity makes its row's scores (and gradients) NaN,
- * the K experts still different ones.  With BEAM_ROUTE_UNNORMED the weights
+ * scores 0, and a NaN or +infinity makes its row's scores and weights NaN (and
+ * its chosen experts' gradients), the K experts still different ones.  With BEAM_ROUTE_UNNORMED the weights
  * are s_k * routed_scale.
  * Where the K chosen scores are all 0 (logits so low that binary32 holds no
  * smaller score, or masked ones) the weights are 0.  Keeping every group
