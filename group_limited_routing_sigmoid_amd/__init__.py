@@ -6,8 +6,10 @@ follow the C ABI in include/beam_moe.h (beam_moe_route, beam_moe_forward,
 beam_moe_permute, beam_moe_quant_e4m3, beam_moe_workspace_bytes,
 beam_moe_validate; around the block beam_moe_route_backward,
 beam_moe_matmul_e4m3, beam_moe_quant_e4m3_2d, beam_moe_norm_residual and its
-_backward).  There is no CPU fallback: without the built library
-every call raises.
+_backward; around a paged key-value cache beam_moe_qk_norm_rope and its
+_backward, beam_moe_paged_attention, beam_moe_pages_update, _compact and _copy,
+beam_moe_token_logprobs and its _backward).  There is no CPU fallback: without
+the built library every call raises.
 """
 from __future__ import annotations
 
@@ -39,7 +41,13 @@ SYMBOLS = ("beam_status_string", "beam_moe_validate", "beam_moe_workspace_bytes"
            "beam_moe_forward_noalloc", "beam_moe_route_backward",
            "beam_moe_norm_residual", "beam_moe_norm_residual_workspace_bytes",
            "beam_moe_norm_residual_backward", "beam_moe_matmul_e4m3",
-           "beam_moe_quant_e4m3_2d")
+           "beam_moe_quant_e4m3_2d", "beam_moe_qk_norm_rope",
+           "beam_moe_qk_norm_rope_workspace_bytes", "beam_moe_qk_norm_rope_backward",
+           "beam_moe_paged_attention", "beam_moe_paged_attention_workspace_bytes",
+           "beam_moe_pages_copy", "beam_moe_pages_workspace_bytes", "beam_moe_pages_update",
+           "beam_moe_pages_compact", "beam_moe_token_logprobs",
+           "beam_moe_token_logprobs_workspace_bytes", "beam_moe_token_logprobs_backward")
+MAX_POOLS, MAX_TOP = 8, 16
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -50,6 +58,13 @@ class Desc(ctypes.Structure):
                 ("group_score_topn", ctypes.c_int32),
                 ("routed_scale", ctypes.c_float), ("act_dtype", ctypes.c_int32),
                 ("weight_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class Pools(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int32), ("layers", ctypes.c_int32),
+                ("base", ctypes.c_void_p * MAX_POOLS), ("bytes", ctypes.c_int64 * MAX_POOLS),
+                ("layer_stride", ctypes.c_int64 * MAX_POOLS),
+                ("page_stride", ctypes.c_int64 * MAX_POOLS)]
 
 
 class BeamError(RuntimeError):
@@ -87,6 +102,28 @@ def lib():
         L.beam_moe_norm_residual_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(sz)]
         L.beam_moe_norm_residual_backward.argtypes = [i64, i64, i32, vp, vp, vp, i64, vp, f32, f32,
                                                       f32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.beam_moe_qk_norm_rope.argtypes = [i64, i32, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp,
+                                            f32, vp, vp, i32, i32, f32, f32, vp, vp, vp, vp, i64, i64,
+                                            i64, i64, i64, vp, i64, i64, vp, vp]
+        L.beam_moe_qk_norm_rope_workspace_bytes.argtypes = [i64, i32, i32, i32, ctypes.POINTER(sz)]
+        L.beam_moe_qk_norm_rope_backward.argtypes = [i64, i32, i32, i32, i32, vp, vp, vp, i64, vp, i64,
+                                                     vp, vp, f32, vp, vp, i32, i32, f32, f32, vp, vp,
+                                                     vp, vp, vp, sz, vp]
+        L.beam_moe_paged_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, ctypes.POINTER(sz)]
+        L.beam_moe_paged_attention.argtypes = [i64, i32, i32, i32, i32, vp, vp, vp, vp, i64, i64, i64,
+                                               i64, i64, vp, i64, vp, f32, i64, vp, vp, vp, sz, vp]
+        P = ctypes.POINTER(Pools)
+        L.beam_moe_pages_copy.argtypes = [P, i64, i64, vp, vp, vp]
+        L.beam_moe_pages_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(sz)]
+        L.beam_moe_pages_update.argtypes = [i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                            P, vp, sz, vp]
+        L.beam_moe_pages_compact.argtypes = [i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, P, vp, sz,
+                                             vp]
+        L.beam_moe_token_logprobs_workspace_bytes.argtypes = [i64, i64, i32, ctypes.POINTER(sz)]
+        L.beam_moe_token_logprobs.argtypes = [i64, i64, i32, vp, i64, vp, f32, f32, i32, vp, vp, vp, vp,
+                                              vp, vp, sz, vp]
+        L.beam_moe_token_logprobs_backward.argtypes = [i64, i64, i32, vp, i64, vp, f32, f32, vp, vp, vp,
+                                                       vp, vp, i64, vp]
         L.beam_moe_permute.argtypes = [D, i64, vp, vp, vp, vp, vp, vp, sz, vp]
         L.beam_moe_quant_e4m3.argtypes = [i64, i64, i32, vp, vp, vp, vp]
         L.beam_moe_quant_mxfp8.argtypes = [i64, i64, i32, vp, vp, vp, vp]
@@ -692,6 +729,375 @@ def norm_residual_backward(residual_out: torch.Tensor,
          T, H, BF16 if dtype is torch.bfloat16 else F32, po, pw, pg, cols, pp, eps, alpha, beta, pr,
          p_dr, p_dx, ptr["d_residual"], ptr.get("d_o"), ptr.get("d_gate"), ptr.get("d_pre_weight"),
          ptr.get("d_post_weight"), None if buf is None else buf.data_ptr(), need.value)
+    return out
+
+
+# ---- attention around a paged key-value cache, and the scores of tokens ------
+
+def rope_frequencies(rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Radians a position of each of rot / 2 pairs, base^(-2 i / rot), in binary64
+    as qk_norm_rope takes them."""
+    if rot < 0 or rot % 2:
+        raise ValueError(f"rot {rot}: pairs of channels turn")
+    return base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1)).to(device)
+
+
+def _dtype_code(name: str, dtype: torch.dtype) -> int:
+    if dtype is torch.bfloat16:
+        return BF16
+    if dtype is torch.float32:
+        return F32
+    raise ValueError(f"{name}: dtype {dtype}, expected torch.bfloat16 or torch.float32")
+
+
+def _heads(name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple):
+    """Address and token stride of heads [T, H, D] whose heads and values are
+    contiguous (a view of a projection's output)."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0
+            and (t.stride(2) == 1 or shape[2] == 1) and (t.stride(1) == shape[2] or shape[1] == 1)):
+        return t.data_ptr(), t.stride(0)
+    _arg(name, t, dev, dtype, shape, True)  # raises for all but the strides
+    raise ValueError(f"{name}: strides {t.stride()}, expected a token's heads in one piece")
+
+
+def _empty_like(on, device, dtype: torch.dtype, *shape) -> torch.Tensor:
+    """An output of any number of dimensions, allocated on the call's stream."""
+    if len(shape) == 3 and on is True and _empty_strided is not None:
+        return _empty_strided(shape, (shape[1] * shape[2], shape[2], 1), dtype)
+    if len(shape) < 3:
+        return _empty(on, device, dtype, *shape)
+    with _alloc_on(None if on is True else on):
+        return torch.empty(*shape, dtype=dtype, device=device)
+
+
+def _cache_args(k_cache, v_cache, tables, dev: int, dtype: torch.dtype, Hkv: int, D: int):
+    """Checked arguments of a cache: (k, v, page, token and head stride, pages,
+    page size, tables, seqs, table columns)."""
+    if k_cache.dim() != 4 or tables is None or tables.dim() != 2:
+        raise ValueError("a cache is k_cache and v_cache [pages, page_size, Hkv, D] with tables "
+                         "[seqs, columns]")
+    shape = (k_cache.shape[0], k_cache.shape[1], Hkv, D)
+    pk = _arg("k_cache", k_cache, dev, dtype, shape, True)
+    pv = _arg("v_cache", v_cache, dev, dtype, shape, True)
+    stride = k_cache.stride()
+    if stride[3] != 1 or v_cache.stride() != stride:
+        raise ValueError(f"strides of k_cache {stride} and v_cache {v_cache.stride()}: expected the "
+                         "same, values contiguous")
+    return (pk, pv, stride[0], stride[1], stride[2], shape[0], shape[1],
+            _arg("tables", tables, dev, torch.int32, tuple(tables.shape)), *tables.shape)
+
+
+def _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq, temperature):
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"shapes {tuple(q.shape)} and {tuple(k.shape)}, expected [T, heads, D]")
+    T, Hq, D = q.shape
+    Hkv, dev, dtype = k.shape[1], q.get_device(), q.dtype
+    code = _dtype_code("q", dtype)
+    pq, sq = _heads("q", q, dev, dtype, (T, Hq, D))
+    pk, sk = _heads("k", k, dev, dtype, (T, Hkv, D))
+    wq = _arg("q_weight", q_weight, dev, torch.float32, (D,))
+    wk = _arg("k_weight", k_weight, dev, torch.float32, (D,))
+    pp = pf = None
+    rot = 0
+    if positions is not None:
+        pp = _arg("positions", positions, dev, torch.int32, (T,))
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        pf = _arg("inv_freq", inv_freq, dev, torch.float64, (rot // 2,))
+    length, exponent = (0.0, 0.0) if temperature is None else temperature
+    if temperature is not None and not length > 0:
+        raise ValueError(f"temperature {temperature}: its length has to be positive")
+    if positions is None and (rot or temperature is not None) and T:
+        raise ValueError("rotation and temperature need positions")
+    return T, Hq, Hkv, D, dev, dtype, code, pq, sq, pk, sk, wq, wk, pp, pf, rot, length, exponent
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
+                 positions: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
+                 interleaved: bool = False, eps: float = 1e-6, temperature: Optional[tuple] = None,
+                 v: Optional[torch.Tensor] = None, k_cache: Optional[torch.Tensor] = None,
+                 v_cache: Optional[torch.Tensor] = None, tables: Optional[torch.Tensor] = None,
+                 rows: Optional[torch.Tensor] = None, with_k: Optional[bool] = None, stream=None):
+    """beam_moe_qk_norm_rope: q [T,Hq,D] and k [T,Hkv,D] (bf16 or fp32; views of
+    one projection's output are taken as they are) with each head normed, times
+    its weight [D], and turned by positions [T] int32 times inv_freq [rot/2]
+    float64 (rope_frequencies; None: not turned); queries times (1 + (pos + 1) /
+    length)^exponent with temperature = (length, exponent).  With k_cache and
+    v_cache [pages,page_size,Hkv,D] and tables [seqs,columns] int32 the keys and
+    v [T,Hkv,D] go to their places: positions in sequence rows [T] int32 (None:
+    token t in sequence t).  Returns (q_out, k_out); k_out is None with a cache
+    but where with_k asks for it."""
+    (T, Hq, Hkv, D, dev, dtype, code, pq, sq, pk, sk, wq, wk, pp, pf, rot, length,
+     exponent) = _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq, temperature)
+    device, on = q.device, _on(stream, dev)
+    pv, sv, pr = None, 0, None
+    cache = (None, None, 0, 0, 0, 0, 0, None, 0, 0)
+    if k_cache is not None or v_cache is not None:
+        if k_cache is None or v_cache is None or v is None:
+            raise ValueError("a cache is k_cache and v_cache, and takes v")
+        if positions is None:
+            raise ValueError("a cache needs positions")
+        cache = _cache_args(k_cache, v_cache, tables, dev, dtype, Hkv, D)
+        pv, sv = _heads("v", v, dev, dtype, (T, Hkv, D))
+        if rows is not None:
+            pr = _arg("rows", rows, dev, torch.int32, (T,))
+        elif cache[8] != T:
+            raise ValueError(f"{cache[8]} sequences for {T} tokens: rows says which is whose")
+    elif v is not None or tables is not None or rows is not None or with_k is False:
+        raise ValueError("v, tables and rows belong to a cache; without one k_out is the keys' way out")
+    q_out = _empty_like(on, device, dtype, T, Hq, D)
+    k_out = None
+    if cache[0] is None and k_cache is None or with_k:
+        k_out = _empty_like(on, device, dtype, T, Hkv, D)
+    _run(lib().beam_moe_qk_norm_rope, "beam_moe_qk_norm_rope", on, dev,
+         (q, k, v, q_weight, k_weight, positions, inv_freq, q_out, k_out, k_cache, v_cache, tables, rows),
+         T, Hq, Hkv, D, code, pq, sq, pk, sk, pv, sv, wq, wk, eps, pp, pf, rot,
+         1 if interleaved else 0, length, exponent, q_out.data_ptr(),
+         None if k_out is None else k_out.data_ptr(), *cache, pr)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: torch.Tensor,
+                          k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
+                          positions: Optional[torch.Tensor] = None,
+                          inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False,
+                          eps: float = 1e-6, temperature: Optional[tuple] = None,
+                          workspace: Optional[Workspace] = None, stream=None) -> dict:
+    """beam_moe_qk_norm_rope_backward: from the gradients of q_out and k_out
+    (contiguous) a dict: d_q and d_k in q's dtype, d_q_weight and d_k_weight [D]
+    fp32.  The other arguments are the forward's."""
+    (T, Hq, Hkv, D, dev, dtype, code, pq, sq, pk, sk, wq, wk, pp, pf, rot, length,
+     exponent) = _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq, temperature)
+    device, on = q.device, _on(stream, dev)
+    pdq = _arg("d_q_out", d_q_out, dev, dtype, (T, Hq, D))
+    pdk = _arg("d_k_out", d_k_out, dev, dtype, (T, Hkv, D))
+    need = ctypes.c_size_t(0)
+    _check(lib().beam_moe_qk_norm_rope_workspace_bytes(T, Hq, Hkv, D, ctypes.byref(need)),
+           "beam_moe_qk_norm_rope_workspace_bytes")
+    out = {"d_q": _empty_like(on, device, dtype, T, Hq, D),
+           "d_k": _empty_like(on, device, dtype, T, Hkv, D),
+           "d_q_weight": _empty(on, device, torch.float32, D),
+           "d_k_weight": _empty(on, device, torch.float32, D)}
+    buf = _scratch(need.value, workspace, device, stream)
+    _run(lib().beam_moe_qk_norm_rope_backward, "beam_moe_qk_norm_rope_backward", on, dev,
+         (d_q_out, d_k_out, q, k, q_weight, k_weight, positions, inv_freq, *out.values()),
+         T, Hq, Hkv, D, code, pdq, pdk, pq, sq, pk, sk, wq, wk, eps, pp, pf, rot,
+         1 if interleaved else 0, length, exponent, *(t.data_ptr() for t in out.values()),
+         None if buf is None else buf.data_ptr(), need.value)
+    return out
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    tables: torch.Tensor, lengths: torch.Tensor, scale: Optional[float] = None,
+                    window: int = 0, gate: Optional[torch.Tensor] = None, with_lse: bool = False,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[Workspace] = None,
+                    stream=None):
+    """beam_moe_paged_attention: attention of one token q [B,Hq,D] of each of B
+    sequences over its lengths [B] int32 cached tokens (its own among them), or
+    the last `window` of them, times sigmoid(gate [B,Hq,D]) if given.  scale is
+    1 / sqrt(D) unless given.  Returns out [B,Hq,D], or (out, lse [B,Hq] fp32)
+    with with_lse."""
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError(f"shapes {tuple(q.shape)} and {tuple(k_cache.shape)}, expected [B, Hq, D] and "
+                         "[pages, page_size, Hkv, D]")
+    B, Hq, D = shape = tuple(q.shape)
+    Hkv, dev, dtype = k_cache.shape[2], q.get_device(), q.dtype
+    code = _dtype_code("q", dtype)
+    device, on = q.device, _on(stream, dev)
+    pq = _arg("q", q, dev, dtype, shape)
+    cache = _cache_args(k_cache, v_cache, tables, dev, dtype, Hkv, D)
+    if cache[8] != B:
+        raise ValueError(f"tables of {cache[8]} sequences for {B} queries")
+    pl = _arg("lengths", lengths, dev, torch.int32, (B,))
+    pg = None if gate is None else _arg("gate", gate, dev, dtype, shape)
+    need = ctypes.c_size_t(0)
+    _check(lib().beam_moe_paged_attention_workspace_bytes(B, Hq, Hkv, D, ctypes.byref(need)),
+           "beam_moe_paged_attention_workspace_bytes")
+    if out is None:
+        out = _empty_like(on, device, dtype, B, Hq, D)
+        po = out.data_ptr()
+    else:
+        po = _arg("out", out, dev, dtype, shape)
+    lse = _empty(on, device, torch.float32, B, Hq) if with_lse else None
+    buf = _scratch(need.value, workspace, device, stream)
+    _run(lib().beam_moe_paged_attention, "beam_moe_paged_attention", on, dev,
+         (q, gate, k_cache, v_cache, tables, lengths, out, lse), B, Hq, Hkv, D, code, pq, pg,
+         *cache[:8], cache[9], pl, 1.0 / math.sqrt(D) if scale is None else scale, window, po,
+         None if lse is None else lse.data_ptr(), None if buf is None else buf.data_ptr(), need.value)
+    return (out, lse) if with_lse else out
+
+
+def _pools(pools, pages: int, dev: int) -> Pools:
+    """The arrays whose pages are copied: tensors [layers, pages, ...] of any
+    dtype, each page of 16-byte multiples and in one piece."""
+    p = Pools()
+    if len(pools) > MAX_POOLS:
+        raise ValueError(f"{len(pools)} pools, at most {MAX_POOLS}")
+    p.count = len(pools)
+    for i, t in enumerate(pools):
+        if t.dim() < 2 or t.shape[1] != pages:
+            raise ValueError(f"pool of shape {tuple(t.shape)}, expected [layers, {pages} pages, ...]")
+        if i and t.shape[0] != p.layers:
+            raise ValueError(f"pools of {p.layers} and {t.shape[0]} layers")
+        if t.get_device() != dev:
+            raise ValueError(f"a pool on {t.device}, the tables on cuda:{dev}")
+        size = 1
+        for n, stride in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
+            if n != 1 and stride != size:
+                raise ValueError(f"pool strides {t.stride()}: a page has to be in one piece")
+            size *= n
+        item = t.element_size()
+        p.layers = t.shape[0]
+        p.base[i], p.bytes[i] = t.data_ptr(), size * item
+        p.layer_stride[i], p.page_stride[i] = t.stride(0) * item, t.stride(1) * item
+    return p
+
+
+def _pages_inputs(tables, lengths, refs, page_size: int):
+    if tables.dim() != 2 or refs.dim() != 1:
+        raise ValueError(f"tables {tuple(tables.shape)} and refs {tuple(refs.shape)}, expected [rows, "
+                         "columns] and [pages]")
+    rows, cols = tables.shape
+    pages, dev = refs.shape[0], refs.get_device()
+    return (rows, cols, pages, dev, _arg("tables", tables, dev, torch.int32, (rows, cols)),
+            _arg("lengths", lengths, dev, torch.int32, (rows,)),
+            _arg("refs", refs, dev, torch.int32, (pages,)))
+
+
+def _pages_scratch(pages: int, rows: int, workspace, device, stream):
+    need = ctypes.c_size_t(0)
+    _check(lib().beam_moe_pages_workspace_bytes(pages, rows, ctypes.byref(need)),
+           "beam_moe_pages_workspace_bytes")
+    buf = _scratch(need.value, workspace, device, stream)
+    return None if buf is None else buf.data_ptr(), need.value
+
+
+def pages_update(tables: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor, page_size: int,
+                 parents: Optional[torch.Tensor] = None, grow: Optional[torch.Tensor] = None,
+                 pools=(), workspace: Optional[Workspace] = None, stream=None) -> dict:
+    """beam_moe_pages_update: the page tables of a batch's next step.  Row i goes
+    on from row parents[i] of tables [B,columns] with lengths [B] (an id outside
+    [0, B): a new sequence; None: each from itself) and gets room for grow[i] more
+    tokens (None: 0).  refs [pages] counts each page's references; pools are the
+    arrays [layers,pages,...] whose shared last pages are copied before they are
+    written.  All int32.  Returns a dict: tables, lengths (with the growth), refs,
+    and missing [1], the pages that were wanted and not to be had."""
+    old, cols, pages, dev, pt, pl, pr = _pages_inputs(tables, lengths, refs, page_size)
+    rows = old if parents is None else parents.shape[0]
+    pp = None if parents is None else _arg("parents", parents, dev, torch.int32, (rows,))
+    pg = None if grow is None else _arg("grow", grow, dev, torch.int32, (rows,))
+    device, on, i32 = refs.device, _on(stream, dev), torch.int32
+    p = _pools(pools, pages, dev)
+    out = {"tables": _empty(on, device, i32, rows, cols), "lengths": _empty(on, device, i32, rows),
+           "refs": _empty(on, device, i32, pages), "missing": _empty(on, device, i32, 1)}
+    ws, need = _pages_scratch(pages, rows, workspace, device, stream)
+    _run(lib().beam_moe_pages_update, "beam_moe_pages_update", on, dev,
+         (tables, lengths, refs, parents, grow, *pools, *out.values()), old, rows, cols, pages,
+         page_size, pt, pl, pr, pp, pg, *(t.data_ptr() for t in out.values()), ctypes.byref(p), ws, need)
+    return out
+
+
+def pages_compact(tables: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor, page_size: int,
+                  pools=(), workspace: Optional[Workspace] = None, stream=None) -> dict:
+    """beam_moe_pages_compact: the used pages (refs > 0) moved to the pool's
+    front, in the arrays of pools too.  Returns a dict: tables and refs with the
+    new ids, new_id [pages] (-1: free) and live [1], how many there are."""
+    rows, cols, pages, dev, pt, pl, pr = _pages_inputs(tables, lengths, refs, page_size)
+    device, on, i32 = refs.device, _on(stream, dev), torch.int32
+    p = _pools(pools, pages, dev)
+    out = {"tables": _empty(on, device, i32, rows, cols), "refs": _empty(on, device, i32, pages),
+           "new_id": _empty(on, device, i32, pages), "live": _empty(on, device, i32, 1)}
+    ws, need = _pages_scratch(pages, rows, workspace, device, stream)
+    _run(lib().beam_moe_pages_compact, "beam_moe_pages_compact", on, dev,
+         (tables, lengths, refs, *pools, *out.values()), rows, cols, pages, page_size, pt, pl, pr,
+         *(t.data_ptr() for t in out.values()), ctypes.byref(p), ws, need)
+    return out
+
+
+def pages_copy(pools, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """beam_moe_pages_copy: page src[i] to page dst[i] (int32) in every layer of
+    every array [layers,pages,...] of pools."""
+    if not pools or pools[0].dim() < 2:
+        raise ValueError("pools: at least one array [layers, pages, ...]")
+    n, dev, pages = src.shape[0], src.get_device(), pools[0].shape[1]
+    ps = _arg("src", src, dev, torch.int32, (n,))
+    pd = _arg("dst", dst, dev, torch.int32, (n,))
+    p = _pools(pools, pages, dev)
+    _run(lib().beam_moe_pages_copy, "beam_moe_pages_copy", _on(stream, dev), dev, (src, dst, *pools),
+         ctypes.byref(p), pages, n, ps, pd)
+
+
+def _logits(name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple):
+    """Address and row stride of logits [T, V] with contiguous rows."""
+    p = _arg(name, t, dev, dtype, shape, True)
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: strides {t.stride()}, expected contiguous rows")
+    return p, t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, softcap: float = 0.0,
+                   scale: float = 1.0, top: int = 0, workspace: Optional[Workspace] = None,
+                   stream=None) -> dict:
+    """beam_moe_token_logprobs of logits [T,V] (bf16 or fp32, rows any stride):
+    z = scale * softcap * tanh(l / softcap) (softcap 0: scale * l).  Returns a
+    dict of fp32 [T]: lse, entropy, with targets [T] int64 logprobs (0 where the
+    target is outside [0, V)); with top > 0 also top_ids [T,top] int32 and
+    top_logprobs [T,top]."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits: shape {tuple(logits.shape)}, expected [T, V]")
+    (T, V), dev = logits.shape, logits.get_device()
+    code = _dtype_code("logits", logits.dtype)
+    pl, stride = _logits("logits", logits, dev, logits.dtype, (T, V))
+    pt = None if targets is None else _arg("targets", targets, dev, torch.int64, (T,))
+    device, on, f32 = logits.device, _on(stream, dev), torch.float32
+    need = ctypes.c_size_t(0)
+    _check(lib().beam_moe_token_logprobs_workspace_bytes(T, V, top, ctypes.byref(need)),
+           "beam_moe_token_logprobs_workspace_bytes")
+    out = {"lse": _empty(on, device, f32, T), "entropy": _empty(on, device, f32, T)}
+    lp = ids = tl = None
+    if targets is not None:
+        lp = out["logprobs"] = _empty(on, device, f32, T)
+    if top:
+        ids = out["top_ids"] = _empty(on, device, torch.int32, T, top)
+        tl = out["top_logprobs"] = _empty(on, device, f32, T, top)
+    buf = _scratch(need.value, workspace, device, stream)
+    _run(lib().beam_moe_token_logprobs, "beam_moe_token_logprobs", on, dev,
+         (logits, targets, *out.values()), T, V, code, pl, stride, pt, softcap, scale, top,
+         None if lp is None else lp.data_ptr(), out["entropy"].data_ptr(), out["lse"].data_ptr(),
+         None if ids is None else ids.data_ptr(), None if tl is None else tl.data_ptr(),
+         None if buf is None else buf.data_ptr(), need.value)
+    return out
+
+
+def token_logprobs_backward(logits: torch.Tensor, lse: torch.Tensor, entropy: torch.Tensor,
+                            targets: Optional[torch.Tensor] = None,
+                            d_logprobs: Optional[torch.Tensor] = None,
+                            d_entropy: Optional[torch.Tensor] = None, softcap: float = 0.0,
+                            scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                            stream=None) -> torch.Tensor:
+    """beam_moe_token_logprobs_backward: the gradient [T,V] of the logits, in
+    their dtype, from those of logprobs and entropy (None: zero; not both) and the
+    forward's lse and entropy.  out may be logits itself."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits: shape {tuple(logits.shape)}, expected [T, V]")
+    if d_logprobs is None and d_entropy is None:
+        raise ValueError("one of d_logprobs and d_entropy is needed")
+    if d_logprobs is not None and targets is None:
+        raise ValueError("d_logprobs needs the targets")
+    (T, V), dev, f32 = logits.shape, logits.get_device(), torch.float32
+    code = _dtype_code("logits", logits.dtype)
+    pl, stride = _logits("logits", logits, dev, logits.dtype, (T, V))
+    ps, pe = _arg("lse", lse, dev, f32, (T,)), _arg("entropy", entropy, dev, f32, (T,))
+    pt = None if targets is None else _arg("targets", targets, dev, torch.int64, (T,))
+    pdl = None if d_logprobs is None else _arg("d_logprobs", d_logprobs, dev, f32, (T,))
+    pde = None if d_entropy is None else _arg("d_entropy", d_entropy, dev, f32, (T,))
+    on = _on(stream, dev)
+    if out is None:
+        out = _empty(on, logits.device, logits.dtype, T, V)
+    po, so = _logits("out", out, dev, logits.dtype, (T, V))
+    _run(lib().beam_moe_token_logprobs_backward, "beam_moe_token_logprobs_backward", on, dev,
+         (logits, lse, entropy, targets, d_logprobs, d_entropy, out), T, V, code, pl, stride, pt,
+         softcap, scale, ps, pe, pdl, pde, po, so)
     return out
 
 

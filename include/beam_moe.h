@@ -22,7 +22,10 @@
  * scheme without spelling the rule out.
  *
  * Around the block: the gradient of the routing, dense e4m3 products with their
- * quantiser, and the step between two blocks with its gradients.
+ * quantiser, the step between two blocks with its gradients, the norms and
+ * rotation of attention heads with their gradients, attention of new tokens over
+ * a paged cache, the cache's page tables, and the scores of tokens with their
+ * gradient.
  *
  * Conventions for every entry point:
  *   - Pointers marked "device" are device memory owned by the caller.  The
@@ -419,6 +422,222 @@ int beam_moe_norm_residual_backward(int64_t T, int64_t H, int32_t dtype, const v
                                     float* d_residual, void* d_o, void* d_gate,
                                     float* d_pre_weight, float* d_post_weight,
                                     void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- attention around a paged key-value cache -------------------------------
+ * A cache is two arrays of pages, keys and values, each page holding page_size
+ * tokens (a power of two) of Hkv heads of D values: value d of head h of token
+ * j of page p lies at p * page_stride + j * token_stride + h * head_stride + d,
+ * the same strides (in elements, multiples of 8; 4 with BEAM_F32) in both.
+ * tables [seqs, table_cols] int32 name the pages of each sequence in order:
+ * token i of sequence s lies in page tables[s, i / page_size] at i % page_size.
+ * An id outside [0, pages) names no page: nothing is written there, and its
+ * tokens take no part in attention.
+ * D is a multiple of 8 from 8 to 256. */
+
+/* Norms of query and key heads and their rotation by position, in one pass,
+ * and the keys' and values' way into a paged cache ("Hugging Face releases
+ * Beam ..."; "Reflection Beam", section "Hybrid Attention and Unusual
+ * Residuals": RMSNorm on queries and keys, rotation in the sliding-window
+ * layers, none in the global ones, whose queries are scaled by
+ * (1 + (pos + 1) / 2048)^0.1).  Per head x of D values of token t:
+ *   n = x / sqrt(mean(x^2) + eps) * weight
+ *   the pair (n_a, n_b) turned by the angle positions[t] * inv_freq[i], for
+ *   i < rot / 2: (a, b) = (i, i + rot / 2), with interleaved (2i, 2i + 1)
+ *   queries times (1 + (positions[t] + 1) / temp_length)^temp_exponent
+ *   q, k, v     device [T, heads, D] dtype, heads and values contiguous, tokens
+ *               q_stride, k_stride, v_stride elements apart (views of one
+ *               projection's output; multiples of 8, 4 with BEAM_F32); v only
+ *               with a cache
+ *   q_weight, k_weight  device [D] fp32
+ *   positions   device [T] int32; NULL only with rot 0, temp_length 0 and no cache
+ *   inv_freq    device [rot / 2] binary64, radians a position; angles are
+ *               reduced in binary64.  rot: 0 or a multiple of 16 up to D
+ *   temp_length 0: no temperature; else > 0, positions > -1 - temp_length
+ *   q_out       device [T, Hq, D] dtype
+ *   k_out       device [T, Hkv, D] dtype, or NULL (with a cache)
+ *   k_cache, v_cache  a cache, or both NULL: token t's key (as k_out) and value
+ *               go to place positions[t] of sequence rows[t] (rows NULL: of
+ *               sequence t).  A token whose position is negative or past the
+ *               table, or whose row is outside [0, seqs), is not written.  No two
+ *               tokens may name one place.
+ * Outputs do not overlap inputs.  T * (Hq + 2 Hkv) < 2^31, Hq, Hkv <= 4096.
+ * No workspace. */
+int beam_moe_qk_norm_rope(int64_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
+                          const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const float* q_weight,
+                          const float* k_weight, float eps, const int32_t* positions,
+                          const double* inv_freq, int32_t rot, int32_t interleaved,
+                          float temp_length, float temp_exponent, void* q_out, void* k_out,
+                          void* k_cache, void* v_cache, int64_t page_stride, int64_t token_stride,
+                          int64_t head_stride, int64_t pages, int64_t page_size,
+                          const int32_t* tables, int64_t seqs, int64_t table_cols,
+                          const int32_t* rows, void* stream);
+
+/* Bytes of workspace beam_moe_qk_norm_rope_backward needs (0 for T == 0). */
+int beam_moe_qk_norm_rope_workspace_bytes(int64_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                                          size_t* bytes);
+
+/* Gradients of beam_moe_qk_norm_rope's q_out and k_out.
+ *   d_q_out, d_k_out  device [T, heads, D] dtype, contiguous
+ *   d_q, d_k          device [T, heads, D] dtype: outputs, contiguous
+ *   d_q_weight, d_k_weight  device [D] fp32: outputs (sums over tokens and heads,
+ *                     0 for T == 0)
+ * Other arguments as in the forward.  Identical inputs give bitwise identical
+ * outputs. */
+int beam_moe_qk_norm_rope_backward(int64_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
+                                   const void* d_q_out, const void* d_k_out, const void* q,
+                                   int64_t q_stride, const void* k, int64_t k_stride,
+                                   const float* q_weight, const float* k_weight, float eps,
+                                   const int32_t* positions, const double* inv_freq, int32_t rot,
+                                   int32_t interleaved, float temp_length, float temp_exponent,
+                                   void* d_q, void* d_k, float* d_q_weight, float* d_k_weight,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace beam_moe_paged_attention needs (0 for seqs == 0). */
+int beam_moe_paged_attention_workspace_bytes(int64_t seqs, int32_t Hq, int32_t Hkv, int32_t D,
+                                             size_t* bytes);
+
+/* Attention of one new token of every sequence over its cached tokens, the new
+ * one's own key and value among them (beam_moe_qk_norm_rope has put them there):
+ *   out = softmax(scale q k^T) v [* sigmoid(gate)]
+ * over the last `window` of lengths[s] tokens (window 0: all), query head h
+ * reading key-value head h / (Hq / Hkv) ("Reflection Beam", section "Hybrid
+ * Attention and Unusual Residuals": a window of 512 or the whole context, 48
+ * query and 8 key-value heads, a sigmoid gate for each head's channels).
+ *   q        device [seqs, Hq, D] dtype, contiguous
+ *   gate     device [seqs, Hq, D] dtype, contiguous, before the sigmoid, or NULL
+ *   lengths  device [seqs] int32: tokens held, the new one among them; a length
+ *            past the table counts as the table's, a negative one as 0
+ *   out      device [seqs, Hq, D] dtype
+ *   lse      device [seqs, Hq] fp32, or NULL: ln sum exp(scale q k^T)
+ * A sequence without tokens that take part (length 0, or no page) gives zeros
+ * and an lse of -infinity.  What pages hold behind a sequence's length or before
+ * its window is not read.  Sums and softmax statistics are binary32, and so are
+ * the products with the values; one rounding to dtype.
+ * scale > 0 and finite, Hq % Hkv == 0, seqs * Hq < 2^24, table_cols * page_size <
+ * 2^31.  Identical inputs give bitwise identical outputs. */
+int beam_moe_paged_attention(int64_t seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
+                             const void* q, const void* gate, const void* k_cache,
+                             const void* v_cache, int64_t page_stride, int64_t token_stride,
+                             int64_t head_stride, int64_t pages, int64_t page_size,
+                             const int32_t* tables, int64_t table_cols, const int32_t* lengths,
+                             float scale, int64_t window, void* out, float* lse, void* workspace,
+                             size_t ws_bytes, void* stream);
+
+/* The arrays whose pages beam_moe_pages_* copy, up to 8 of them: page p of layer
+ * l of array i is `bytes[i]` bytes at base[i] + l * layer_stride[i] + p *
+ * page_stride[i] (bytes, multiples of 16). */
+typedef struct {
+  int32_t count;
+  int32_t layers;
+  void* base[8];
+  int64_t bytes[8];
+  int64_t layer_stride[8];
+  int64_t page_stride[8];
+} beam_moe_pools;
+
+/* Copies page src[i] to page dst[i] in every layer of every array, i < n.
+ *   src, dst  device [n] int32; a pair with an id outside [0, pages) is left
+ *             out.  No page is written twice, none that is written is read.
+ * No workspace. */
+int beam_moe_pages_copy(const beam_moe_pools* pools, int64_t pages, int64_t n, const int32_t* src,
+                        const int32_t* dst, void* stream);
+
+/* Bytes of workspace beam_moe_pages_update and _compact need for a pool of
+ * `pages` pages and `rows` rows (of the new batch; any for _compact). */
+int beam_moe_pages_workspace_bytes(int64_t pages, int64_t rows, size_t* bytes);
+
+/* The step of a batch's page tables between two decode steps: row i of the new
+ * batch goes on from row parents[i] of the old one, or starts anew, and gets
+ * room for grow[i] more tokens.  Pages are shared by counting references;
+ * a shared last page is copied before its row may write to it; old rows that
+ * nobody goes on from give their references up.
+ *   tables    device [old_rows, cols] int32; of row s the first ceil(lengths[s] /
+ *             page_size) entries count (lengths held to [0, cols * page_size])
+ *   lengths   device [old_rows] int32: tokens held
+ *   refs      device [pages] int32: references to each page, those of this
+ *             batch's rows among them; a page with 0 or fewer is free
+ *   parents   device [rows] int32, an id outside [0, old_rows) starts a new
+ *             sequence; or NULL: rows == old_rows, each goes on from itself
+ *   grow      device [rows] int32 (negative: 0), or NULL: 0 for all
+ *   tables_out, lengths_out, refs_out  device [rows, cols], [rows], [pages]
+ *             int32: outputs that overlap no input; entries of a table behind its
+ *             last page are -1; lengths_out = held + grow, at most cols * page_size
+ *   missing   device [1] int32: pages that rows wanted and did not get, for want
+ *             of free pages (their entries are -1) or of columns
+ * References are first counted for the new rows' held pages.  A page that is the
+ * unfilled last page of a row that grows is left to that row if nothing else
+ * refers to it, and to the lowest of them if only such rows do; every other such
+ * row gets a copy.  Rows in order want a page for their copy, then their new
+ * ones in order, and get the free pages in order of their ids, each with one
+ * reference.  pools' pages are copied in the same call (count 0: none).
+ * Nothing but integers decides anything, and no order of execution.
+ * rows, old_rows <= 65536, pages < 2^24, rows * cols and old_rows * cols < 2^31,
+ * page_size a power of two, cols * page_size < 2^31. */
+int beam_moe_pages_update(int64_t old_rows, int64_t rows, int64_t cols, int64_t pages,
+                          int64_t page_size, const int32_t* tables, const int32_t* lengths,
+                          const int32_t* refs, const int32_t* parents, const int32_t* grow,
+                          int32_t* tables_out, int32_t* lengths_out, int32_t* refs_out,
+                          int32_t* missing, const beam_moe_pools* pools, void* workspace,
+                          size_t ws_bytes, void* stream);
+
+/* Packs the used pages of a pool to its front: with n used pages, those with
+ * ids from n up move, in order of their ids, into the free ones below n, in order.
+ *   refs        device [pages] int32 as above
+ *   tables, lengths  as above; tables_out device [rows, cols]: the new ids, -1
+ *               behind a row's last page and for an id outside [0, pages) or of
+ *               a free page; may be tables itself
+ *   refs_out    device [pages] int32, not refs itself
+ *   new_id      device [pages] int32: where each page is now, -1 for a free one
+ *               (for tables kept elsewhere)
+ *   live        device [1] int32: n
+ * pools' pages are moved in the same call.  Limits as above. */
+int beam_moe_pages_compact(int64_t rows, int64_t cols, int64_t pages, int64_t page_size,
+                           const int32_t* tables, const int32_t* lengths, const int32_t* refs,
+                           int32_t* tables_out, int32_t* refs_out, int32_t* new_id, int32_t* live,
+                           const beam_moe_pools* pools, void* workspace, size_t ws_bytes,
+                           void* stream);
+
+/* ---- scores of tokens ---------------------------------------------------------
+ * Bytes of workspace beam_moe_token_logprobs needs (0 for T == 0). */
+int beam_moe_token_logprobs_workspace_bytes(int64_t T, int64_t V, int32_t top, size_t* bytes);
+
+/* Log probabilities of given tokens with the entropy of the distribution and
+ * its best alternatives, in one reading of the logits, per row t:
+ *   z = scale * softcap * tanh(l / softcap)   (softcap 0: z = scale * l)
+ *   logp = z - ln sum exp(z)
+ * ("Reflection Beam", section "Hybrid Attention and Unusual Residuals": logits
+ * capped by tanh at 30).
+ *   logits    device [T, V] dtype, rows row_stride >= V elements apart
+ *   targets   device [T] int64, or NULL; one outside [0, V) gives logprob 0
+ *   logprobs  device [T] fp32, with targets: logp of the target
+ *   entropy   device [T] fp32: -sum p logp
+ *   lse       device [T] fp32: ln sum exp(z)
+ *   top_ids, top_logprobs  device [T, top] int32 and fp32, top > 0: the tokens of
+ *             the highest logits in order, equal ones by their index
+ * A logit of -infinity is masked: it has probability 0, logp -infinity and
+ * gradient 0, also under the cap.  A row of only those has lse and logp
+ * -infinity and entropy 0.  A NaN or +infinity makes its row's results NaN
+ * (+infinity under the cap is the cap).
+ * 0 <= top <= min(16, V); softcap >= 0, scale > 0, finite; V <= 2^24, T < 2^23. */
+int beam_moe_token_logprobs(int64_t T, int64_t V, int32_t dtype, const void* logits,
+                            int64_t row_stride, const int64_t* targets, float softcap, float scale,
+                            int32_t top, float* logprobs, float* entropy, float* lse,
+                            int32_t* top_ids, float* top_logprobs, void* workspace,
+                            size_t ws_bytes, void* stream);
+
+/* Gradient of the logits from those of logprobs and entropy (NULL: zero; not
+ * both):
+ *   d l_j = z'(l_j) (d_logprob ([j = target] - p_j) - d_entropy p_j (logp_j + entropy))
+ *   lse, entropy  device [T] fp32: the forward's
+ *   d_logits      device [T, V] dtype, rows row_stride elements apart; may be
+ *                 logits itself
+ * A target outside [0, V) has no gradient of its logprob.  No workspace. */
+int beam_moe_token_logprobs_backward(int64_t T, int64_t V, int32_t dtype, const void* logits,
+                                     int64_t row_stride, const int64_t* targets, float softcap,
+                                     float scale, const float* lse, const float* entropy,
+                                     const float* d_logprobs, const float* d_entropy,
+                                     void* d_logits, int64_t d_row_stride, void* stream);
 
 /* Auxiliary-loss-free load balancing step.  The load-balancing paragraph of
  * "Reflection AI Introduces Beam ..." says Beam builds on DeepSeek-V3's
