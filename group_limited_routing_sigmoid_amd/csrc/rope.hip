@@ -12,7 +12,10 @@
 // wave stays with one token: each lane takes the sine and cosine of one pair
 // (two at D > 128) and all heads of the token take theirs from LDS.  An angle
 // is reduced in binary64, in quarter turns, so that what is left is exact to
-// 2^-26 of a quarter turn at any position.
+// 2^-26 of a quarter turn at any position.  One token a wave and the next step's
+// loads ahead of the work: 16,381 tokens of 48 + 8 heads of 128 into a cache take
+// 101 us (5.3 TB/s); waves that stay for several tokens, with loads ahead across
+// them, took 139, and two to eight waves a token 119 to 173.
 #include <algorithm>
 
 #include "serve.h"
@@ -23,9 +26,9 @@ namespace {
 constexpr int kRopeWaves = 4;
 constexpr double kQuartersPerRadian = 0.63661977236758134308;  // 2 / pi
 
-// (cos, sin) of pos * f
+// (cos, sin) of pos * f quarter turns
 __device__ __forceinline__ float2 turn(int pos, double f) {
-  const double u = static_cast<double>(pos) * (f * kQuartersPerRadian);
+  const double u = static_cast<double>(pos) * f;
   const double n = rint(u);
   float s, c;
   sincospif(0.5f * static_cast<float>(u - n), &s, &c);
@@ -38,61 +41,68 @@ __device__ __forceinline__ float2 turn(int pos, double f) {
   return quarter & 2 ? make_float2(-c, -s) : make_float2(c, s);
 }
 
+// Sum over the LPH lanes of a head, by data-parallel moves: neighbours, pairs,
+// then each half of 8 and of 16 lanes mirrored.
 template <int LPH>
 __device__ __forceinline__ float head_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < LPH; m *= 2) v += __shfl_xor(v, m);
+#define BEAM_ADD(ctrl) \
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), ctrl, 0xF, 0xF, true))
+  if (LPH >= 2) BEAM_ADD(0xB1);
+  if (LPH >= 4) BEAM_ADD(0x4E);
+  if (LPH >= 8) BEAM_ADD(0x141);
+  if (LPH >= 16) BEAM_ADD(0x140);
+#undef BEAM_ADD
+  if (LPH >= 32) v += __shfl_xor(v, 16);
   return v;
 }
 
-// What a lane needs to turn its 8 values: for each the cosine and the sine with
-// the sign that meets its partner's value.
+// A lane's 8 values of a turn: with o a value's partner, y = c v + s o.
 struct Turn {
   float c[8], s[8];
-  int partner;  // lane of the partner's values (pairs half a rotation apart)
-  bool turns;
+  int partner;  // lane of the partners (pairs half a rotation apart; else itself)
 };
 template <int LPH>
-__device__ __forceinline__ Turn make_turn(const RopeArgs& a, int pos, float2* cs, int lane) {
-  const int pairs = a.rot / 2, chunk = lane % LPH, col = chunk * 8;
-  Turn t;
-  t.turns = col < a.rot;
+__device__ __forceinline__ void make_turn(const RopeArgs& a, int pos, const double* freq,
+                                          float2* cs, int lane, Turn& t) {
+  const int pairs = a.rot / 2, col = lane % LPH * 8;
   t.partner = lane;
-  if (a.rot == 0) return t;
-  for (int i = lane; i < pairs; i += kWave) cs[i] = turn(pos, a.inv_freq[i]);
-  wave_order();
-  if (!t.turns) return t;
-  const bool second = !a.interleaved && col >= pairs;
-  if (!a.interleaved) t.partner = second ? lane - pairs / 8 : lane + pairs / 8;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float2 v = cs[a.interleaved ? (col + j) / 2 : second ? col - pairs + j : col + j];
-    t.c[j] = v.x;
-    t.s[j] = (a.interleaved ? j % 2 == 0 : !second) ? -v.y : v.y;
+    t.c[j] = 1.0f;
+    t.s[j] = 0.0f;
+  }
+  if (a.rot == 0) return;
+  for (int i = lane; i < pairs; i += kWave) cs[i] = turn(pos, freq[i]);
+  wave_order();
+  if (col < a.rot) {
+    const bool second = !a.interleaved && col >= pairs;
+    if (!a.interleaved) t.partner = second ? lane - pairs / 8 : lane + pairs / 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 v = cs[a.interleaved ? (col + j) / 2 : second ? col - pairs + j : col + j];
+      t.c[j] = v.x;
+      t.s[j] = (a.interleaved ? j % 2 == 0 : !second) ? -v.y : v.y;
+    }
   }
   wave_order();  // the next token's pairs
-  return t;
 }
 
-// y = the turned v, where `back` turns the other way.  Every lane of the wave
-// calls it.
-template <int LPH, bool back>
-__device__ __forceinline__ void rotate(const RopeArgs& a, const Turn& t, float (&v)[8]) {
-  if (a.rot == 0) return;
-  float other[8];
-  if (a.interleaved) {
+// The partners of a lane's values (every lane of the wave calls it).
+template <typename IO>
+__device__ __forceinline__ void partners(const RopeArgs& a, const Turn& t, const Eight<IO>& e,
+                                         float (&o)[8]) {
+  if (a.interleaved || a.rot == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) other[j] = v[j ^ 1];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) other[j] = __shfl(v[j], t.partner);
+    for (int j = 0; j < 8; ++j) o[j] = e.get(j ^ 1);
+    return;
   }
-  if (!t.turns) return;
+  Eight<IO> x;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float s = back ? -t.s[j] : t.s[j];
-    v[j] = v[j] * t.c[j] + other[j] * s;
-  }
+  for (int i = 0; i < Eight<IO>::kWords; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x.w[i][j] = __shfl(static_cast<int>(e.w[i][j]), t.partner);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = x.get(j);
 }
 
 __device__ __forceinline__ float temperature(const RopeArgs& a, int pos) {
@@ -112,76 +122,119 @@ __device__ __forceinline__ int64_t place(const RopeArgs& a, int64_t t, int pos) 
   return page * c.page_stride + (pos & ((1 << c.shift) - 1)) * c.token_stride;
 }
 
-// Lane groups of LPH lanes hold a head; a wave takes 64 / LPH heads at a time:
+// What the workgroup's waves share: both weights, the frequencies in quarter
+// turns a position, and each wave's sines and cosines.
+struct Shared {
+  float w[2][kMaxHeadDim];
+  double freq[kMaxHeadDim / 2];
+  float2 pairs[kRopeWaves][kMaxHeadDim / 2];
+  __device__ __forceinline__ void stage(const RopeArgs& a) {
+    for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+      w[0][c] = a.wq[c];
+      w[1][c] = a.wk[c];
+    }
+    for (int i = threadIdx.x; i < a.rot / 2; i += blockDim.x)
+      freq[i] = a.inv_freq[i] * kQuartersPerRadian;
+    __syncthreads();
+  }
+};
+
+// Lane groups of LPH lanes hold a head; a wave takes 64 / LPH heads at a step:
 // first the queries', then the keys', then the values' (which are copied).
-// `parts` waves share a token.
+// `parts` waves share a token.  Loads are never masked (a lane without a head
+// reads its step's last one), so that the next step's are on their way while one
+// is worked on; stores are.
 template <typename IO, int LPH>
 __global__ __launch_bounds__(kRopeWaves* kWave) void rope_forward(RopeArgs a, int parts) {
   constexpr int kHeads = kWave / LPH;
-  __shared__ float2 pairs[kRopeWaves][kMaxHeadDim / 2];
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  __shared__ Shared sh;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kRopeWaves + wave;
-  const int64_t t = id / parts;
-  const int part = static_cast<int>(id % parts);
-  if (t >= a.T) return;
-  const int pos = a.pos ? a.pos[t] : 0;
-  const int col = lane % LPH * 8, sub = lane / LPH;
-  const bool in = col < a.D;
-  const Turn tn = make_turn<LPH>(a, pos, pairs[wave], lane);
-  const float temp = temperature(a, pos);
-  const int64_t at = a.cache.k ? place(a, t, pos) : -1;
+  const int64_t t = min<int64_t>(id / parts, a.T - 1);
+  int i = static_cast<int>(id % parts);
+  const bool in = lane % LPH * 8 < a.D;
+  const int col = in ? lane % LPH * 8 : 0, sub = lane / LPH;
   const int nq = (a.Hq + kHeads - 1) / kHeads, nk = (a.Hkv + kHeads - 1) / kHeads;
-  float w[8];
-  auto weights = [&](const float* p) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = in ? p[col + j] : 0.0f;
+  const IO* q = static_cast<const IO*>(a.q) + t * a.q_stride + col;
+  const IO* k = static_cast<const IO*>(a.k) + t * a.k_stride + col;
+  const IO* v = static_cast<const IO*>(a.v) + t * a.v_stride + col;
+  auto read = [&](const IO* p, int step, int H) {
+    Eight<IO> e;
+    e.load(p + min(step * kHeads + sub, H - 1) * a.D);
+    return e;
   };
-  auto normed = [&](const IO* x, bool live, float scale, Eight<IO>& e) {
-    if (live) e.load(x);
-    else e.zero();
-    float v[8], ss = 0.0f;
+  // what the wave starts with
+  Eight<IO> e = i < nq ? read(q, i, a.Hq) : i < nq + nk ? read(k, i - nq, a.Hkv)
+                : a.cache.k ? read(v, i - nq - nk, a.Hkv) : read(k, 0, a.Hkv);
+  const int pos = a.pos ? a.pos[t] : 0;
+  sh.stage(a);
+  if (id / parts >= a.T) return;
+  const int64_t at = a.cache.k ? place(a, t, pos) : -1;
+  Turn tn;
+  make_turn<LPH>(a, pos, sh.freq, sh.pairs[wave], lane, tn);
+  const float per = in ? 1.0f / static_cast<float>(a.D) : 0.0f;
+  // y = inv (c v + s o) with the weights and the scale in c and s
+  float c[8], s[8];
+  auto factors = [&](const float* w, float scale) {
+    const int other = tn.partner % LPH * 8;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = e.get(j);
-      ss += v[j] * v[j];
+      c[j] = tn.c[j] * w[col + j] * scale;
+      s[j] = tn.s[j] * w[a.interleaved ? col + (j ^ 1) : other + j] * scale;
     }
-    const float inv = 1.0f / sqrtf(head_sum<LPH>(ss) / static_cast<float>(a.D) + a.eps);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v[j] * inv * w[j];
-    rotate<LPH, false>(a, tn, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= scale;
-    e.set(v);
   };
-  weights(a.wq);
-  const IO* q = static_cast<const IO*>(a.q) + t * a.q_stride + col;
-  IO* qo = static_cast<IO*>(a.q_out) + t * a.Hq * a.D + col;
-  int i = part;
-  for (; i < nq; i += parts) {
-    const int h = i * kHeads + sub;
-    const bool live = in && h < a.Hq;
-    Eight<IO> e;
-    normed(q + h * a.D, live, temp, e);
-    if (live) e.store(qo + h * a.D);
+  auto normed = [&](Eight<IO>& e) {
+    float x[8], o[8], ss = 0.0f;
+    partners(a, tn, e, o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = e.get(j);
+      ss += x[j] * x[j];
+    }
+    const float inv = __builtin_amdgcn_rsqf(head_sum<LPH>(ss * per) + a.eps);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = (x[j] * c[j] + o[j] * s[j]) * inv;
+    e.set(x);
+  };
+  if (i < nq) {
+    factors(sh.w[0], temperature(a, pos));
+    IO* out = static_cast<IO*>(a.q_out) + t * a.Hq * a.D + col;
+    do {
+      const Eight<IO> next = i + parts < nq ? read(q, i + parts, a.Hq)
+                                            : read(k, min(i + parts - nq, nk - 1), a.Hkv);
+      normed(e);
+      const int h = i * kHeads + sub;
+      if (in && h < a.Hq) e.store(out + h * a.D);
+      e = next;
+      i += parts;
+    } while (i < nq);
+    // (where its next step is a value's, the wave has read a key's in vain)
+    if (a.cache.k && i >= nq + nk) e = read(v, min(i - nq - nk, nk - 1), a.Hkv);
   }
-  weights(a.wk);
-  for (i -= nq; i < nk; i += parts) {
-    const int h = i * kHeads + sub;
-    const bool live = in && h < a.Hkv;
-    Eight<IO> e;
-    normed(static_cast<const IO*>(a.k) + t * a.k_stride + h * a.D + col, live, 1.0f, e);
-    if (live && a.k_out)
-      e.store(static_cast<IO*>(a.k_out) + (t * a.Hkv + h) * a.D + col);
-    if (live && at >= 0)
-      e.store(static_cast<IO*>(a.cache.k) + at + h * a.cache.head_stride + col);
+  i -= nq;
+  if (i < nk) {
+    factors(sh.w[1], 1.0f);
+    do {
+      Eight<IO> next = e;
+      if (i + parts < nk) next = read(k, i + parts, a.Hkv);
+      else if (at >= 0) next = read(v, min(i + parts - nk, nk - 1), a.Hkv);
+      normed(e);
+      const int h = i * kHeads + sub;
+      if (in && h < a.Hkv) {
+        if (a.k_out) e.store(static_cast<IO*>(a.k_out) + (t * a.Hkv + h) * a.D + col);
+        if (at >= 0) e.store(static_cast<IO*>(a.cache.k) + at + h * a.cache.head_stride + col);
+      }
+      e = next;
+      i += parts;
+    } while (i < nk);
   }
   if (at < 0) return;
   for (i -= nk; i < nk; i += parts) {
+    const Eight<IO> next = read(v, min(i + parts, nk - 1), a.Hkv);
     const int h = i * kHeads + sub;
-    if (!in || h >= a.Hkv) continue;
-    Eight<IO> e;
-    e.load(static_cast<const IO*>(a.v) + t * a.v_stride + h * a.D + col);
-    e.store(static_cast<IO*>(a.cache.v) + at + h * a.cache.head_stride + col);
+    if (in && h < a.Hkv) e.store(static_cast<IO*>(a.cache.v) + at + h * a.cache.head_stride + col);
+    e = next;
   }
 }
 
@@ -193,62 +246,69 @@ template <typename IO, int LPH>
 __global__ __launch_bounds__(kRopeWaves* kWave) void rope_backward(RopeGradArgs g) {
   constexpr int kHeads = kWave / LPH;
   const RopeArgs& a = g.f;
-  __shared__ float2 pairs[kRopeWaves][kMaxHeadDim / 2];
+  __shared__ Shared sh;
   __shared__ float sums[kRopeWaves][kHeads][LPH * 8];
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int col = lane % LPH * 8, sub = lane / LPH;
-  const bool in = col < a.D;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const bool in = lane % LPH * 8 < a.D;
+  const int col = in ? lane % LPH * 8 : 0, sub = lane / LPH;
+  const float per = in ? 1.0f / static_cast<float>(a.D) : 0.0f;
+  sh.stage(a);
   float acc[2][8] = {};
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kRopeWaves;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRopeWaves + wave; t < a.T; t += step) {
+  const int64_t every = static_cast<int64_t>(gridDim.x) * kRopeWaves;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRopeWaves + wave; t < a.T; t += every) {
+    const IO* x[2] = {static_cast<const IO*>(a.q) + t * a.q_stride + col,
+                      static_cast<const IO*>(a.k) + t * a.k_stride + col};
+    const IO* dy[2] = {static_cast<const IO*>(g.dq_out) + t * a.Hq * a.D + col,
+                       static_cast<const IO*>(g.dk_out) + t * a.Hkv * a.D + col};
+    Eight<IO> ex, ed;
+    auto read = [&](int kind, int i, int H) {
+      const int off = min(i * kHeads + sub, H - 1) * a.D;
+      ex.load(x[kind] + off);
+      ed.load(dy[kind] + off);
+    };
+    read(0, 0, a.Hq);
     const int pos = a.pos ? a.pos[t] : 0;
-    const Turn tn = make_turn<LPH>(a, pos, pairs[wave], lane);
+    Turn tn;
+    make_turn<LPH>(a, pos, sh.freq, sh.pairs[wave], lane, tn);
     const float temp = temperature(a, pos);
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
-      const int H = kind ? a.Hkv : a.Hq;
-      const IO* x = static_cast<const IO*>(kind ? a.k : a.q) +
-                    t * (kind ? a.k_stride : a.q_stride) + col;
-      const IO* dy = static_cast<const IO*>(kind ? g.dk_out : g.dq_out) + t * H * a.D + col;
+      const int H = kind ? a.Hkv : a.Hq, n = (H + kHeads - 1) / kHeads;
       IO* dx = static_cast<IO*>(kind ? g.dk : g.dq) + t * H * a.D + col;
+      const float scale = kind ? 1.0f : temp;
       float w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = in ? (kind ? a.wk : a.wq)[col + j] : 0.0f;
-      const float scale = kind ? 1.0f : temp;
-      for (int h0 = 0; h0 < H; h0 += kHeads) {
-        const int h = h0 + sub;
-        const bool live = in && h < H;
-        Eight<IO> ex, ed;
-        if (live) {
-          ex.load(x + h * a.D);
-          ed.load(dy + h * a.D);
-        } else {
-          ex.zero();
-          ed.zero();
-        }
-        float v[8], d[8], ss = 0.0f;
+      for (int j = 0; j < 8; ++j) w[j] = sh.w[kind][col + j];
+      for (int i = 0; i < n; ++i) {
+        const Eight<IO> nx = ex, nd = ed;
+        if (i + 1 < n) read(kind, i + 1, H);
+        else if (kind == 0) read(1, 0, a.Hkv);
+        float v[8], d[8], o[8], ss = 0.0f;
+        partners(a, tn, nd, o);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          v[j] = ex.get(j);
-          d[j] = ed.get(j) * scale;
+          v[j] = nx.get(j);
           ss += v[j] * v[j];
+          d[j] = (nd.get(j) * tn.c[j] - o[j] * tn.s[j]) * scale;
         }
-        const float inv = 1.0f / sqrtf(head_sum<LPH>(ss) / static_cast<float>(a.D) + a.eps);
-        rotate<LPH, true>(a, tn, d);
+        const float inv = __builtin_amdgcn_rsqf(head_sum<LPH>(ss * per) + a.eps);
+        const bool live = in && i * kHeads + sub < H;
         float dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           v[j] *= inv;
-          acc[kind][j] += d[j] * v[j];
+          acc[kind][j] += live ? d[j] * v[j] : 0.0f;
           d[j] *= w[j];
           dot += d[j] * v[j];
         }
-        const float mean = head_sum<LPH>(dot) / static_cast<float>(a.D);
+        const float mean = head_sum<LPH>(dot * per);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] = inv * (d[j] - v[j] * mean);
         if (live) {
-          ed.set(d);
-          ed.store(dx + h * a.D);
+          Eight<IO> out;
+          out.set(d);
+          out.store(dx + (i * kHeads + sub) * a.D);
         }
       }
     }
@@ -257,30 +317,35 @@ __global__ __launch_bounds__(kRopeWaves* kWave) void rope_backward(RopeGradArgs 
   for (int kind = 0; kind < 2; ++kind) {
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sums[wave][sub][col + j] = acc[kind][j];
+    for (int j = 0; j < 8; ++j) sums[wave][sub][lane % LPH * 8 + j] = acc[kind][j];
     __syncthreads();
     for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
       float s = 0.0f;
       for (int i = 0; i < kRopeWaves; ++i)
+#pragma unroll 4
         for (int j = 0; j < kHeads; ++j) s += sums[i][j][c];
       g.part[(static_cast<int64_t>(blockIdx.x) * 2 + kind) * a.D + c] = s;
     }
   }
 }
 
-// The workgroups' shares added: 16 columns a workgroup, 16 threads a column.
-__global__ __launch_bounds__(256) void rope_weight_sums(const float* part, int groups, int D,
-                                                         float* d_wq, float* d_wk) {
-  __shared__ float sums[16][17];
-  const int c = blockIdx.x * 16 + threadIdx.x % 16, row = threadIdx.x / 16;
+// The workgroups' shares added: 8 columns a workgroup, 32 threads a column.
+constexpr int kSumCols = 8, kSumRows = 32;
+__global__ __launch_bounds__(kSumCols* kSumRows) void rope_weight_sums(const float* part, int groups,
+                                                                        int D, float* d_wq,
+                                                                        float* d_wk) {
+  __shared__ float sums[kSumRows][kSumCols + 1];
+  const int in = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols;
+  const int c = blockIdx.x * kSumCols + in;  // D is a multiple of 8
   float s = 0.0f;
-  if (c < 2 * D)
-    for (int g = row; g < groups; g += 16) s += part[static_cast<int64_t>(g) * 2 * D + c];
-  sums[row][threadIdx.x % 16] = s;
+#pragma unroll 8
+  for (int g = row; g < groups; g += kSumRows) s += part[static_cast<int64_t>(g) * 2 * D + c];
+  sums[row][in] = s;
   __syncthreads();
-  if (row || c >= 2 * D) return;
+  if (row) return;
   s = 0.0f;
-  for (int i = 0; i < 16; ++i) s += sums[i][threadIdx.x];
+#pragma unroll
+  for (int i = 0; i < kSumRows; ++i) s += sums[i][in];
   (c < D ? d_wq : d_wk)[c < D ? c : c - D] = s;
 }
 
@@ -318,7 +383,7 @@ hipError_t forward(const RopeArgs& a, hipStream_t s) {
 
 template <typename IO>
 hipError_t backward(const RopeGradArgs& a, float* d_wq, float* d_wk, hipStream_t s) {
-  const int groups = rope_grad_groups(a.f.T, a.f.Hq, a.f.Hkv, a.f.D);
+  const int groups = rope_grad_groups(a.f.T);
   if (groups) {
     const hipError_t e = by_lanes<IO>(a.f.D, [&](auto lanes) {
       hipLaunchKernelGGL((rope_backward<IO, decltype(lanes)::value>), dim3(groups),
@@ -327,15 +392,17 @@ hipError_t backward(const RopeGradArgs& a, float* d_wq, float* d_wk, hipStream_t
     });
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(rope_weight_sums, dim3(ceil_div(2 * a.f.D, 16)), dim3(256), 0, s, a.part,
+  hipLaunchKernelGGL(rope_weight_sums, dim3(2 * a.f.D / kSumCols), dim3(kSumCols * kSumRows), 0, s, a.part,
                      groups, a.f.D, d_wq, d_wk);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int rope_grad_groups(int64_t T, int, int, int) {
-  return static_cast<int>(std::min<int64_t>(ceil_div(T, kRopeWaves), 1024));
+// Three workgroups a compute unit, as their registers allow (8,191 tokens with the
+// forward: 128 us; two 133, four 141).
+int rope_grad_groups(int64_t T) {
+  return static_cast<int>(std::min<int64_t>(ceil_div(T, kRopeWaves), 768));
 }
 
 hipError_t launch_qk_norm_rope(const RopeArgs& a, int32_t dtype, hipStream_t s) {

@@ -52,7 +52,7 @@ int make_cache(void* k, void* v, int64_t page_stride, int64_t token_stride, int6
       !stride_ok(head_stride, dtype))
     return BEAM_ERR_INVALID_ARG;
   if (!power_of_two(page_size) || page_size > (1 << 30) || pages > 0x7FFFFFFF ||
-      cols > 0x7FFFFFFF || cols * page_size > 0x7FFFFFFF)
+      cols > 0x7FFFFFFF || cols * page_size > 0x7FFFFFFF || token_stride >= (1 << 25))
     return BEAM_ERR_UNSUPPORTED;
   c->k = k;
   c->v = v;
@@ -169,7 +169,7 @@ int beam_moe_qk_norm_rope_workspace_bytes(int64_t T, int32_t Hq, int32_t Hkv, in
   if (!bytes) return BEAM_ERR_INVALID_ARG;
   const int st = check_rope(T, Hq, Hkv, D, BEAM_BF16, 0, 0, 1.0f, 0.0f, 0.0f);
   if (st != BEAM_OK) return st;
-  *bytes = static_cast<size_t>(rope_grad_groups(T, Hq, Hkv, D)) * 2 * static_cast<size_t>(D) *
+  *bytes = static_cast<size_t>(rope_grad_groups(T)) * 2 * static_cast<size_t>(D) *
            sizeof(float);
   return BEAM_OK;
 }
@@ -257,6 +257,8 @@ int beam_moe_paged_attention(int64_t seqs, int32_t Hq, int32_t Hkv, int32_t D, i
                   token_stride, head_stride, pages, page_size, tables, seqs, table_cols, dtype,
                   &a.cache);
   if (st != BEAM_OK) return st;
+  // units of work are counted in 32 bits
+  if (seqs * (table_cols * page_size) >= (int64_t{1} << 36)) return BEAM_ERR_UNSUPPORTED;
   if (seqs == 0) return BEAM_OK;
   if (!q || !k_cache || !v_cache || !lengths || !out || (!tables && table_cols > 0))
     return BEAM_ERR_INVALID_ARG;

@@ -432,7 +432,7 @@ int beam_moe_norm_residual_backward(int64_t T, int64_t H, int32_t dtype, const v
  * token i of sequence s lies in page tables[s, i / page_size] at i % page_size.
  * An id outside [0, pages) names no page: nothing is written there, and its
  * tokens take no part in attention.
- * D is a multiple of 8 from 8 to 256. */
+ * D is a multiple of 8 from 8 to 256, token_stride < 2^25. */
 
 /* Norms of query and key heads and their rotation by position, in one pass,
  * and the keys' and values' way into a paged cache ("Hugging Face releases
@@ -515,7 +515,7 @@ int beam_moe_paged_attention_workspace_bytes(int64_t seqs, int32_t Hq, int32_t H
  * its window is not read.  Sums and softmax statistics are binary32, and so are
  * the products with the values; one rounding to dtype.
  * scale > 0 and finite, Hq % Hkv == 0, seqs * Hq < 2^24, table_cols * page_size <
- * 2^31.  Identical inputs give bitwise identical outputs. */
+ * 2^31, seqs times that < 2^36.  Identical inputs give bitwise identical outputs. */
 int beam_moe_paged_attention(int64_t seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
                              const void* q, const void* gate, const void* k_cache,
                              const void* v_cache, int64_t page_stride, int64_t token_stride,
