@@ -6,17 +6,19 @@
 // (logits capped by tanh at 30: "Reflection Beam", section "Hybrid Attention
 // and Unusual Residuals".)
 //
-// A row is cut into pieces of at most 16,384 logits, which a workgroup holds in
-// registers: the largest first (the cap keeps the order, so the raw logits are
-// compared), then the sums relative to each thread's own largest, in base 2:
-// S and sum (z - m) exp(z - m), which meet by rescaling.  Few rows get smaller
-// pieces, so that they fill the card.  The alternatives are taken in turn: a
-// wave's best by the largest value and the lowest index, after which the lane
-// that held it looks for its next.  A second kernel joins a row's pieces.
-// Bound by reading the logits (with the cap: by two exponentials and a
-// reciprocal an element).
+// A row is cut into pieces, more of them for few rows, so that they fill the
+// card.  Without alternatives a workgroup runs through its piece with the sums
+// relative to each thread's largest logit so far, in base 2: S and sum (z - m)
+// exp(z - m), which meet by rescaling; under a cap of ordinary size, whose z
+// binary32's exponentials hold as they are, m is 0.  With alternatives the piece,
+// of at most 16,384 logits, is held in registers (the cap keeps the order, so the
+// raw logits are compared): a wave's best is the largest value at the lowest
+// index, one after another, with each lane's largest of eight kept.  A second
+// kernel joins a row's pieces.  Bound by reading the logits; with the cap by two
+// exponentials and a reciprocal an element as much (4,096 x 100,003
+// bf16: 165 us, 5.0 TB/s; the gradient 308 us, 5.3 TB/s).
 #include <algorithm>
-#include <climits>
+#include <cfloat>
 
 #include "serve.h"
 
@@ -28,7 +30,6 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kChunk = kThreads * 8;   // logits of a workgroup's step
 constexpr int kMaxSteps = 8;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLowest = -3.0e38f;
 
 typedef u32x4 u32x4_2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_4 __attribute__((aligned(4)));
@@ -73,6 +74,40 @@ __device__ __forceinline__ void store8(const Eight<IO>& e, IO* p, int64_t n) {
       else p[j] = __uint_as_float(e.w[j / 4][j % 4]);
     }
 }
+// Rows start anywhere.  What runs through them steps in whole 16 bytes of memory
+// (4,096 x 100,003 bf16, capped: 161 us, as for 100,000; from the row's start
+// 208), so that its first and last eight may lie over the row's ends: `skew` is
+// how many values the row starts behind such a place.
+template <typename IO>
+__device__ __forceinline__ int skew_of(const IO* row) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(IO));
+}
+// Eight logits from i on, of which those outside [0, V) are masked ones.
+template <typename IO>
+__device__ __forceinline__ void load_over(Eight<IO>& e, const IO* row, int i, int V) {
+  if (i >= 0) return load8(e, row + i, V - i);
+  load8(e, row, 0);
+#pragma unroll
+  for (int j = 1; j < 8; ++j)
+    if (i + j >= 0 && i + j < V) {
+      if constexpr (sizeof(IO) == 2) {
+        const int sh = 16 * (j % 2);
+        e.w[0][j / 2] = (e.w[0][j / 2] & ~(0xFFFFu << sh)) | static_cast<uint32_t>(row[i + j]) << sh;
+      } else {
+        e.w[j / 4][j % 4] = __float_as_uint(row[i + j]);
+      }
+    }
+}
+template <typename IO>
+__device__ __forceinline__ void store_over(const Eight<IO>& e, IO* row, int i, int V) {
+  if (i >= 0) return store8(e, row + i, V - i);
+#pragma unroll
+  for (int j = 1; j < 8; ++j)
+    if (i + j >= 0 && i + j < V) {
+      if constexpr (sizeof(IO) == 2) row[i + j] = static_cast<uint16_t>(e.w[0][j / 2] >> (16 * (j % 2)));
+      else row[i + j] = __uint_as_float(e.w[j / 4][j % 4]);
+    }
+}
 template <typename IO>
 __device__ __forceinline__ float value(IO v) {
   if constexpr (sizeof(IO) == 2) return bf16_bits_to_f32(v);
@@ -83,92 +118,111 @@ __device__ __forceinline__ float value(IO v) {
 // dz/dl = 4 r (1 - r) scale.
 struct Cap {
   float a, b;  // no cap: z = b l;  cap: z = a - 2 a r, r of exp2(b l)
+  float scale;
   bool on;
 };
 __host__ __device__ __forceinline__ Cap make_cap(float softcap, float scale) {
   Cap c;
   c.on = softcap > 0.0f;
+  c.scale = scale;
   c.a = scale * softcap * kLog2E;
   c.b = c.on ? 2.0f * kLog2E / softcap : scale * kLog2E;
   return c;
 }
-template <bool CAP>
-__device__ __forceinline__ float z_of(const Cap& c, float l, float& r) {
-  if constexpr (!CAP) return c.b * l;
-  r = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(c.b * l));
-  return c.a - 2.0f * c.a * r;
-}
-__device__ __forceinline__ float z_of(const Cap& c, float l) {
-  if (l == -INFINITY) return l;
-  float r;
-  return c.on ? z_of<true>(c, l, r) : z_of<false>(c, l, r);
-}
+// How z is made: without a cap, with one, and with one small enough that 2^z and
+// its sums need no maximum.
+enum Form { kPlain, kCapped, kSmall };
+constexpr float kSmallCap = 50.0f;
+Form form_of(const Cap& c) { return !c.on ? kPlain : c.a <= kSmallCap ? kSmall : kCapped; }
 
-// Sums relative to 2^m: s of 2^(z - m), w of (z - m) 2^(z - m).
+__device__ __forceinline__ float cap_r(const Cap& c, float l) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(c.b * l));
+}
+// In nats, where the lowest logits still have a z.
+__device__ __forceinline__ float z_of(const Cap& c, float l) {
+  if (l == -INFINITY) return l;  // masked
+  return c.on ? (c.a - 2.0f * c.a * cap_r(c, l)) * kLn2 : c.scale * l;
+}
+// Times a logit: at most 5e-7 of a finite one, an infinite one all the same.
+constexpr float kTrace = 0x1p-149f;
+
+// Sums relative to m (in nats): with d = (z - m) / ln 2, s of 2^d, w of d 2^d.
 struct Sums {
   float m, s, w;
 };
+// In base 2, and finite, so that it times 0 is 0.
+__device__ __forceinline__ float apart(float m, float to) { return fmaxf((m - to) * kLog2E, -1e30f); }
 __device__ __forceinline__ Sums meet(const Sums& x, const Sums& y) {
   Sums o;
   o.m = fmaxf(x.m, y.m);
   // (a side without logits has s and w 0 and any m)
-  const float dx = fmaxf(x.m - o.m, -1e30f), dy = fmaxf(y.m - o.m, -1e30f);
+  const float dx = apart(x.m, o.m), dy = apart(y.m, o.m);
   const float fx = __builtin_amdgcn_exp2f(dx), fy = __builtin_amdgcn_exp2f(dy);
   o.s = x.s * fx + y.s * fy;
   o.w = (x.w + dx * x.s) * fx + (y.w + dy * y.s) * fy;
   return o;
 }
-__device__ __forceinline__ Sums wave_meet(Sums v) {
-#pragma unroll
-  for (int i = 1; i < kWave; i *= 2) {
-    const Sums o = {__shfl_xor(v.m, i), __shfl_xor(v.s, i), __shfl_xor(v.w, i)};
-    v = meet(v, o);
-  }
-  return v;
+
+// Reductions over the wave by data-parallel moves; the result in every lane.
+template <typename F>
+__device__ __forceinline__ float wave_reduce(float v, F f) {
+#define BEAM_STEP(ctrl, rows)                                                                \
+  v = f(v, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), \
+                                                      ctrl, rows, 0xF, false)))
+  BEAM_STEP(0xB1, 0xF);   // neighbours, pairs, halves of 8, of 16
+  BEAM_STEP(0x4E, 0xF);
+  BEAM_STEP(0x141, 0xF);
+  BEAM_STEP(0x140, 0xF);
+#undef BEAM_STEP
+  const float a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0)),
+              b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16)),
+              c = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32)),
+              d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
+  return f(f(a, b), f(c, d));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return wave_reduce(v, [](float x, float y) { return fmaxf(x, y); });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  return wave_reduce(v, [](float x, float y) { return x + y; });
+}
+// Indexes below 2^24 as binary32 are exact, and so is their order.
+__device__ __forceinline__ int wave_min(int v) {
+  return static_cast<int>(-wave_max(-static_cast<float>(v)));
+}
+__device__ __forceinline__ Sums wave_meet(const Sums& v) {
+  Sums o;
+  o.m = wave_max(v.m);
+  const float d = apart(v.m, o.m), f = __builtin_amdgcn_exp2f(d);
+  o.s = wave_sum(v.s * f);
+  o.w = wave_sum((v.w + d * v.s) * f);
+  return o;
 }
 
-// A candidate: the highest value, then the lowest index.  index INT_MAX: none.
+// A candidate: the highest value, then the lowest index.
+constexpr int kNoIndex = 1 << 24;
 struct Best {
   float v;
-  int i;
+  int i;  // kNoIndex: none
 };
-__device__ __forceinline__ bool before(float v, int i, const Best& b) {
-  return v > b.v || (v == b.v && i < b.i);
-}
+constexpr Best kNobody = {-INFINITY, kNoIndex};
 // The wave's best, in every lane.
 __device__ __forceinline__ Best wave_best(const Best& mine) {
-  Best b = mine;
-#pragma unroll
-  for (int i = 1; i < kWave; i *= 2) {
-    const float v = __shfl_xor(b.v, i);
-    const int x = __shfl_xor(b.i, i);
-    if (before(v, x, b)) b = Best{v, x};
-  }
+  Best b;
+  b.v = wave_max(mine.v);
+  b.i = wave_min(mine.v == b.v ? mine.i : kNoIndex);
   return b;
 }
-constexpr Best kNobody = {-INFINITY, INT_MAX};
-// A NaN ranks first, so that a row's alternatives are always different tokens.
-__device__ __forceinline__ float ranked(float v) { return v == v ? v : INFINITY; }
-
-// The best `top` of the wave's lanes' candidates, one after another; next(last)
-// gives the calling lane's best behind `last`.  Lane i keeps the i-th.
-template <typename F>
-__device__ __forceinline__ Best take_best(int top, Best mine, F next) {
-  const int lane = threadIdx.x % kWave;
-  Best kept = kNobody;
-  for (int k = 0; k < top; ++k) {
-    const Best b = wave_best(mine);
-    if (lane == k) kept = b;
-    if (b.i != INT_MAX && mine.i == b.i) mine = next(b);
-  }
-  return kept;
+// Whether (v, i) ranks behind `last`.
+__device__ __forceinline__ bool behind(float v, int i, const Best& last) {
+  return v < last.v || (v == last.v && i > last.i);
 }
 
 struct Shared {
   Sums sums[kWaves];
   Best best[kWaves][kMaxTop];
 };
-// The waves' sums and best meet in wave 0 (whose lanes i < top get the i-th best).
+// The waves' sums and best meet in wave 0, whose lanes i < top get the i-th best.
 __device__ __forceinline__ void join(Shared& sh, int top, Sums& sums, Best& kept) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   sums = wave_meet(sums);
@@ -181,249 +235,406 @@ __device__ __forceinline__ void join(Shared& sh, int top, Sums& sums, Best& kept
   if (top == 0) return;
   Best mine = kNobody;
   if (lane % kMaxTop < top) mine = sh.best[lane / kMaxTop][lane % kMaxTop];
-  kept = take_best(top, mine, [](const Best&) { return kNobody; });
+  kept = kNobody;
+  for (int k = 0; k < top; ++k) {
+    const Best b = wave_best(mine);
+    if (lane == k) kept = b;
+    if (mine.i == b.i) mine = kNobody;
+  }
 }
 static_assert(kWaves * kMaxTop == kWave, "one lane for each wave's candidate");
 
+// A row's target and its logit, read ahead of what they meet.
+struct Target {
+  float l;
+  bool counts;
+};
+template <typename IO>
+__device__ __forceinline__ Target target_of(const ScoreArgs& a, int64_t t) {
+  Target g = {0.0f, false};
+  if (!a.logprobs) return g;
+  const int64_t x = a.targets[t];
+  g.counts = x >= 0 && x < a.V;
+  if (g.counts) g.l = value(static_cast<const IO*>(a.logits)[t * a.stride + x]);
+  return g;
+}
 // A row's results, by wave 0.
 template <typename IO>
 __device__ __forceinline__ void finish(const ScoreArgs& a, const Cap& c, int64_t t,
-                                       const Sums& u, const Best& kept) {
+                                       const Sums& u, const Best& kept, const Target& g) {
   const int lane = threadIdx.x % kWave;
-  const bool none = u.s == 0.0f;  // every logit masked
-  const float log2s = __log2f(u.s);
-  const float lse2 = none ? -INFINITY : u.m + log2s;
-  const IO* row = static_cast<const IO*>(a.logits) + t * a.stride;
+  const bool none = u.s == 0.0f;      // every logit masked
+  const bool bad = !(u.s <= FLT_MAX);  // a NaN or +infinity among them
+  const float log2s = bad ? NAN : __log2f(u.s), lns = log2s * kLn2;
+  auto logp = [&](float l) {
+    const float z = z_of(c, l);
+    return z == -INFINITY && !bad ? z : (z - u.m) - lns;
+  };
   if (lane == 0) {
-    a.lse[t] = lse2 * kLn2;
+    a.lse[t] = none ? -INFINITY : u.m + lns;
     a.entropy[t] = none ? 0.0f : (log2s - u.w / u.s) * kLn2;
-    if (a.logprobs) {
-      const int64_t x = a.targets[t];
-      float lp = 0.0f;
-      if (x >= 0 && x < a.V) {
-        const float z = z_of(c, value(row[x]));
-        lp = z == -INFINITY ? z : (z - lse2) * kLn2;
-        if (u.s != u.s) lp = u.s;
-      }
-      a.logprobs[t] = lp;
-    }
+    if (a.logprobs) a.logprobs[t] = g.counts ? logp(g.l) : 0.0f;
   }
+  if (a.top == 0) return;
+  // where NaNs leave too few, the first tokens stand in, so that they differ
+  const bool few = __any(lane < a.top && kept.i == kNoIndex);
   if (lane < a.top) {
-    const float z = z_of(c, value(row[kept.i]));
-    a.top_ids[t * a.top + lane] = kept.i;
-    float lp = z == -INFINITY ? z : (z - lse2) * kLn2;
-    if (u.s != u.s) lp = u.s;
-    a.top_logprobs[t * a.top + lane] = lp;
+    a.top_ids[t * a.top + lane] = few ? lane : kept.i;
+    a.top_logprobs[t * a.top + lane] = few ? NAN : logp(kept.v);
   }
 }
 
-// A piece of a row: `len` logits, STEPS steps of the workgroup at most.
-template <typename IO, int STEPS, bool CAP, bool TOP>
-__global__ __launch_bounds__(kThreads) void score_pieces(ScoreArgs a, Cap c, int pieces, int len,
-                                                          float* part) {
+// What a thread's sums are relative to: a logit, and under a large cap its z (base
+// 2).  kSmall: to 0, and w is a sum of r.
+struct Ref {
+  float l, z;
+};
+template <Form F>
+__device__ __forceinline__ Ref ref_of(const Cap& c, float l) {
+  Ref r = {fmaxf(l, -FLT_MAX), 0.0f};
+  if constexpr (F == kCapped) r.z = c.a - 2.0f * c.a * cap_r(c, r.l);
+  return r;
+}
+template <Form F>
+__device__ __forceinline__ void add(const Cap& c, float l, const Ref& ref, float& s, float& w) {
+  if constexpr (F == kPlain) {
+    // the difference first: exact for logits alike, however large
+    const float d = c.b * (l - ref.l), p = __builtin_amdgcn_exp2f(d);
+    s += p;
+    w += p * fmaxf(d, -160.0f);  // 0, not NaN, where p is 0
+  } else if constexpr (F == kCapped) {
+    const float d = c.a - 2.0f * c.a * cap_r(c, l) - ref.z;
+    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(l, kTrace, d));
+    s += p;
+    w += p * d;
+  } else {
+    const float r = cap_r(c, l);
+    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(-2.0f * c.a, r, __builtin_fmaf(l, kTrace, c.a)));
+    s += p;
+    w += p * r;
+  }
+}
+template <Form F>
+__device__ __forceinline__ Sums sums_of(const Cap& c, const Ref& ref, float s, float w) {
+  if constexpr (F == kPlain) return Sums{fmaxf(c.scale * ref.l, -FLT_MAX), s, w};
+  else if constexpr (F == kCapped) return Sums{ref.z * kLn2, s, w};
+  else return Sums{0.0f, s, c.a * s - 2.0f * c.a * w};
+}
+
+// Workspace: four floats of sums for each piece of each row, then the pieces'
+// best, `top` each.
+__device__ __forceinline__ void put_sums(float* part, int64_t i, const Sums& u) {
+  *reinterpret_cast<f32x4*>(part + 4 * i) = f32x4{u.m, u.s, u.w, 0.0f};
+}
+__device__ __forceinline__ Best* best_of(float* part, int64_t T, int pieces, int64_t i, int top) {
+  return reinterpret_cast<Best*>(part + 4 * T * pieces) + i * top;
+}
+
+// Sums of a piece of a row, read as it goes, the next logits ahead.
+template <typename IO, Form F>
+__global__ __launch_bounds__(kThreads) void score_sums(ScoreArgs a, Cap c, int pieces, int len,
+                                                        float* part) {
   __shared__ Shared sh;
   const int64_t t = blockIdx.x / pieces;
-  const int piece = blockIdx.x % pieces;
-  const int first = piece * len, end = min(first + len, a.V);
   const IO* row = static_cast<const IO*>(a.logits) + t * a.stride;
-  const int base = first + static_cast<int>(threadIdx.x) * 8;
+  const int skew = skew_of(row), from = blockIdx.x % pieces * len;
+  const int first = from - skew, end = min(first + len, a.V);
+  Ref ref = ref_of<F>(c, -FLT_MAX);
+  float s = 0.0f, w = 0.0f;
+  auto use = [&](const Eight<IO>& e) {
+    if constexpr (F != kSmall) {
+      float top = e.get(0);
+#pragma unroll
+      for (int j = 1; j < 8; ++j) top = fmaxf(top, e.get(j));
+      if (top > ref.l) {  // raise the maximum
+        const Ref to = ref_of<F>(c, top);
+        const float d = fmaxf(F == kPlain ? c.b * (ref.l - to.l) : ref.z - to.z, -1e30f);
+        const float f = __builtin_amdgcn_exp2f(d);
+        w = (w + d * s) * f;
+        s *= f;
+        ref = to;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) add<F>(c, e.get(j), ref, s, w);
+  };
+  // the step over the row's start; whole ones, four at a time; what is left
+  const int in = static_cast<int>(threadIdx.x) * 8;
+  int i = first;
+  auto step = [&] {
+    Eight<IO> e;
+    load_over(e, row, i + in, end);
+    use(e);
+    i += kChunk;
+  };
+  if (i < 0) step();
+  constexpr int kAhead = 4;
+  for (; i + kAhead * kChunk <= end; i += kAhead * kChunk) {
+    Eight<IO> e[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) e[u].load(row + i + in + u * kChunk);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) use(e[u]);
+  }
+  while (i < end) step();
+  Sums u = sums_of<F>(c, ref, s, w);
+  Best kept = kNobody;
+  join(sh, 0, u, kept);
+  if (threadIdx.x >= kWave) return;
+  if (pieces == 1) finish<IO>(a, c, t, u, kept, target_of<IO>(a, t));
+  else if (threadIdx.x == 0) put_sums(part, blockIdx.x, u);
+}
+
+// Sums and the best `top` of a piece of a row of `len` logits, STEPS steps of the
+// workgroup at most, held in registers.
+template <typename IO, int STEPS, Form F>
+__global__ __launch_bounds__(kThreads) void score_top(ScoreArgs a, Cap c, int pieces, int len,
+                                                       float* part) {
+  __shared__ Shared sh;
+  const int64_t t = blockIdx.x / pieces;
+  const int first = blockIdx.x % pieces * len, end = min(first + len, a.V);
+  const IO* row = static_cast<const IO*>(a.logits) + t * a.stride;
+  const int base = first + static_cast<int>(threadIdx.x) * 8, lane = threadIdx.x % kWave;
   Eight<IO> e[STEPS];
 #pragma unroll
   for (int k = 0; k < STEPS; ++k) load8(e[k], row + base + k * kChunk, end - (base + k * kChunk));
-  float top = -INFINITY;
+  float most[STEPS], all = -INFINITY;  // of each eight, of the lane
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    most[k] = e[k].get(0);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) most[k] = fmaxf(most[k], e[k].get(j));
+    all = fmaxf(all, most[k]);
+  }
+  const Ref ref = ref_of<F>(c, all);
+  float s = 0.0f, w = 0.0f;
 #pragma unroll
   for (int k = 0; k < STEPS; ++k)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, e[k].get(j));
-  Sums u;
-  float r;
-  top = fmaxf(top, kLowest);
-  u.m = fmaxf(z_of<CAP>(c, top, r), kLowest);
-  u.s = u.w = 0.0f;
+    for (int j = 0; j < 8; ++j) add<F>(c, e[k].get(j), ref, s, w);
+  Best kept = kNobody, last = {INFINITY, -1};
+  for (int x = 0; x < a.top; ++x) {
+    Best b;
+    b.v = wave_max(all);
+    int at = kNoIndex;  // the lane's lowest index of that value, not taken yet
+    if (all == b.v) {
 #pragma unroll
-  for (int k = 0; k < STEPS; ++k)
+      for (int k = STEPS - 1; k >= 0; --k)
+        if (most[k] == b.v)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float l = e[k].get(j);
-      if constexpr (CAP) {
-        const float d = z_of<CAP>(c, l, r) - u.m;
-        float p = __builtin_amdgcn_exp2f(d);
-        p = l == -INFINITY ? 0.0f : p;
-        u.w += p * d;
-        u.s += p;
-      } else {  // the difference first: exact for logits alike, however large
-        const float d = c.b * (l - top), p = __builtin_amdgcn_exp2f(d);
-        u.w += p * fmaxf(d, -160.0f);  // 0, not NaN, where p is 0
-        u.s += p;
+          for (int j = 7; j >= 0; --j) {
+            const int i = base + k * kChunk + j;
+            if (e[k].get(j) == b.v && i < end && behind(b.v, i, last)) at = i;
+          }
+    }
+    b.i = wave_min(at);
+    if (lane == x) kept = b;
+    last = b;
+    if (at == b.i && at != kNoIndex) {  // the lane that held it
+      all = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) {
+        if (most[k] == b.v) {
+          most[k] = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float v = e[k].get(j);
+            if (behind(v, base + k * kChunk + j, b)) most[k] = fmaxf(most[k], v);
+          }
+        }
+        all = fmaxf(all, most[k]);
       }
     }
+  }
+  Sums u = sums_of<F>(c, ref, s, w);
+  join(sh, a.top, u, kept);
+  if (threadIdx.x >= kWave) return;
+  if (pieces == 1) {
+    finish<IO>(a, c, t, u, kept, target_of<IO>(a, t));
+    return;
+  }
+  if (lane == 0) put_sums(part, blockIdx.x, u);
+  if (lane < a.top) best_of(part, a.T, pieces, blockIdx.x, a.top)[lane] = kept;
+}
+
+// Joins a row's pieces.  Each piece's best are in order: a thread stands at the
+// first one of its piece that is not taken yet, all of them in LDS (`staged` of
+// them; 0: there are more pieces than threads, and each looks through its own).
+template <typename IO>
+__global__ __launch_bounds__(kThreads) void score_join(ScoreArgs a, Cap c, int pieces,
+                                                        float* part, int staged) {
+  __shared__ Shared sh;
+  extern __shared__ Best all[];
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x % kWave;
+  const Best* best = best_of(part, a.T, pieces, t * pieces, a.top);
+#pragma unroll 4
+  for (int x = threadIdx.x; x < staged; x += kThreads) all[x] = best[x];
+  Sums u = {-FLT_MAX, 0.0f, 0.0f};
+  for (int i = threadIdx.x; i < pieces; i += kThreads) {
+    const f32x4 p = *reinterpret_cast<const f32x4*>(part + 4 * (t * pieces + i));
+    u = meet(u, Sums{p[0], p[1], p[2]});
+  }
+  const Target g = target_of<IO>(a, t);
   Best kept = kNobody;
-  if constexpr (TOP) {
-    auto next = [&](const Best& last) {
+  if (a.top) {
+    __syncthreads();
+    int at = threadIdx.x * a.top;
+    const int stop = min(at + a.top, staged);
+    auto first = [&](const Best& last) {
       Best b = kNobody;
-#pragma unroll
-      for (int k = 0; k < STEPS; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float v = ranked(e[k].get(j));
-          const int i = base + k * kChunk + j;
-          if (i < end && before(v, i, b) && (v < last.v || (v == last.v && i > last.i)))
-            b = Best{v, i};
+      if (staged) return at < stop ? all[at] : b;
+      for (int i = threadIdx.x; i < pieces; i += kThreads)
+        for (int x = 0; x < a.top; ++x) {
+          const Best y = best[i * a.top + x];
+          if (!behind(y.v, y.i, last)) continue;
+          if (y.v > b.v || (y.v == b.v && y.i < b.i)) b = y;
+          break;
         }
       return b;
     };
-    kept = take_best(a.top, next(Best{INFINITY, -1}), next);
-  }
-  join(sh, TOP ? a.top : 0, u, kept);
-  if (threadIdx.x >= kWave) return;
-  if (pieces == 1) {
-    finish<IO>(a, c, t, u, kept);
-    return;
-  }
-  float* to = part + static_cast<int64_t>(blockIdx.x) * (4 + 2 * a.top);
-  if (threadIdx.x == 0) {
-    to[0] = u.m;
-    to[1] = u.s;
-    to[2] = u.w;
-  }
-  if (TOP && static_cast<int>(threadIdx.x) < a.top) {
-    to[4 + threadIdx.x] = kept.v;
-    to[4 + a.top + threadIdx.x] = __int_as_float(kept.i);
-  }
-}
-
-// Joins a row's pieces.
-template <typename IO>
-__global__ __launch_bounds__(kThreads) void score_join(ScoreArgs a, Cap c, int pieces,
-                                                        const float* part) {
-  __shared__ Shared sh;
-  const int64_t t = blockIdx.x;
-  const int size = 4 + 2 * a.top;
-  const float* row = part + t * pieces * size;
-  Sums u = {kLowest, 0.0f, 0.0f};
-  for (int i = threadIdx.x; i < pieces; i += kThreads) {
-    const float* p = row + static_cast<int64_t>(i) * size;
-    u = meet(u, Sums{p[0], p[1], p[2]});
-  }
-  Best kept = kNobody;
-  if (a.top) {
-    auto next = [&](const Best& last) {
-      Best b = kNobody;
-      for (int x = threadIdx.x; x < pieces * a.top; x += kThreads) {
-        const float* p = row + static_cast<int64_t>(x / a.top) * size + 4 + x % a.top;
-        const float v = p[0];
-        const int i = __float_as_int(p[a.top]);
-        if (i != INT_MAX && before(v, i, b) && (v < last.v || (v == last.v && i > last.i)))
-          b = Best{v, i};
+    Best mine = first(Best{INFINITY, -1});
+    // (a wave without a piece has nobody)
+    const int rounds = threadIdx.x - lane < pieces ? a.top : 0;
+    for (int k = 0; k < rounds; ++k) {
+      const Best b = wave_best(mine);
+      if (lane == k) kept = b;
+      if (mine.i == b.i && b.i != kNoIndex) {
+        ++at;
+        mine = first(b);
       }
-      return b;
-    };
-    kept = take_best(a.top, next(Best{INFINITY, -1}), next);
+    }
   }
-  join(sh, a.top, u, kept);
-  if (threadIdx.x < kWave) finish<IO>(a, c, t, u, kept);
+  // with pieces in one wave alone, its best are the row's
+  join(sh, pieces > kWave ? a.top : 0, u, kept);
+  if (threadIdx.x < kWave) finish<IO>(a, c, t, u, kept, g);
 }
 
 template <typename IO, bool CAP>
 __global__ __launch_bounds__(kThreads) void score_backward(ScoreGradArgs a, Cap c, int pieces,
                                                             int len) {
   const int64_t t = blockIdx.x / pieces;
-  const int first = blockIdx.x % pieces * len, end = min(first + len, a.V);
   const IO* row = static_cast<const IO*>(a.logits) + t * a.stride;
+  const int skew = skew_of(row), from = blockIdx.x % pieces * len;
+  const int first = from - skew, end = min(first + len, a.V);
   IO* out = static_cast<IO*>(a.d_logits) + t * a.d_stride;
   const int64_t target = a.targets ? a.targets[t] : -1;
   const bool counts = target >= 0 && target < a.V;
   const float g = counts && a.d_logprobs ? a.d_logprobs[t] * a.scale : 0.0f;
   const float h = a.d_entropy ? a.d_entropy[t] * a.scale : 0.0f;
-  const float lse2 = a.lse[t] * kLog2E;
-  const float both = g + h * a.entropy[t], h2 = h * kLn2;
+  const float given = a.lse[t], lse = given == -INFINITY ? 0.0f : given;  // (all masked: p is 0)
+  const float lse2 = lse * kLog2E;
+  const float both = -(g + h * a.entropy[t]), h2 = -h * kLn2;
   const int at = counts ? static_cast<int>(target) : -1;
-  for (int i = first + static_cast<int>(threadIdx.x) * 8; i < end; i += kChunk) {
-    Eight<IO> e;
-    load8(e, row + i, end - i);
-    float d[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float l = e.get(j);
-      float r;
-      const float logp = fminf(fmaxf(z_of<CAP>(c, l, r) - lse2, -200.0f), 0.0f);
-      const float p = __builtin_amdgcn_exp2f(logp);
-      d[j] = -p * (both + h2 * logp);
+  // a logit's gradient, in which the target's own g is missing; q: z'
+  auto gradient = [&](float l, float& q) {
+    if constexpr (CAP) {
+      const float r = cap_r(c, l), r4 = 4.0f * r;
+      const float logp = __builtin_fmaf(-2.0f * c.a, r, c.a - lse2);
+      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(l, kTrace, logp));
+      q = __builtin_fmaf(-r4, r, r4);
+      return p * __builtin_fmaf(h2, logp, both) * q;
+    } else {
+      q = 1.0f;
+      const float logp = fminf(fmaxf((c.scale * l - lse) * kLog2E, -200.0f), 0.0f);
+      return __builtin_amdgcn_exp2f(logp) * __builtin_fmaf(h2, logp, both);
     }
+  };
+  auto use = [&](Eight<IO>& e, int i) {
+    float d[8], q;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j] = gradient(e.get(j), q);
     if (at >= i && at < i + 8) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] += at == i + j ? g : 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float l = e.get(j);
-      if constexpr (CAP) {
-        float r;
-        z_of<CAP>(c, l, r);
-        d[j] *= 4.0f * r * (1.0f - r);
-      }
-      d[j] = l == -INFINITY ? 0.0f : d[j];
+      for (int j = 0; j < 8; ++j)
+        if (at == i + j && e.get(j) != -INFINITY) {
+          gradient(e.get(j), q);
+          d[j] += g * q;
+        }
     }
     e.set(d);
-    store8(e, out + i, end - i);
+  };
+  const int in = static_cast<int>(threadIdx.x) * 8;
+  int i = first;
+  auto step = [&] {
+    Eight<IO> e;
+    load_over(e, row, i + in, end);
+    use(e, i + in);
+    store_over(e, out, i + in, end);
+    i += kChunk;
+  };
+  if (i < 0) step();
+  constexpr int kAhead = 2;
+  for (; i + kAhead * kChunk <= end; i += kAhead * kChunk) {
+    Eight<IO> e[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) e[u].load(row + i + in + u * kChunk);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      use(e[u], i + in + u * kChunk);
+      store8(e[u], out + i + in + u * kChunk, 8);
+    }
   }
+  while (i < end) step();
 }
 
-// Steps of a piece: 8, or fewer where that leaves the card empty.
-int steps_for(int64_t T, int64_t V) {
-  int steps = kMaxSteps;
+// Steps of a piece: `most`, or fewer where that leaves the card empty.
+int steps_for(int64_t T, int64_t V, int most) {
+  int steps = most;
   while (steps > 1 && T * ceil_div(V, int64_t{kChunk} * steps) < 1024) steps /= 2;
   return steps;
 }
+// Without alternatives a piece is as long as fills the card.
+constexpr int kLongSteps = 1 << 13;
+int most_steps(int top) { return top ? kMaxSteps : kLongSteps; }
 struct Cut {
   int pieces, len;
 };
-// Pieces of like length, a multiple of 8.
-Cut cut(int64_t V, int steps) {
+// Pieces of like length, a multiple of 8; `over`: values that a row's first eight
+// may start before it.
+Cut cut(int64_t V, int steps, int over) {
   Cut c;
   c.pieces = static_cast<int>(ceil_div(V, int64_t{kChunk} * steps));
-  c.len = static_cast<int>(ceil_div(ceil_div(V, c.pieces), 8) * 8);
+  c.len = static_cast<int>(ceil_div(ceil_div(V + over, c.pieces), 8) * 8);
   return c;
 }
 
-template <typename IO, int STEPS, bool CAP>
-void pieces_top(const ScoreArgs& a, const Cap& c, const Cut& k, float* part, hipStream_t s) {
+template <typename IO, Form F>
+void pieces(const ScoreArgs& a, const Cap& c, int steps, const Cut& k, float* part, hipStream_t s) {
   const dim3 grid(a.T * k.pieces), block(kThreads);
-  if (a.top)
-    hipLaunchKernelGGL((score_pieces<IO, STEPS, CAP, true>), grid, block, 0, s, a, c, k.pieces,
-                       k.len, part);
-  else
-    hipLaunchKernelGGL((score_pieces<IO, STEPS, CAP, false>), grid, block, 0, s, a, c, k.pieces,
-                       k.len, part);
-}
-template <typename IO, bool CAP>
-void pieces_steps(const ScoreArgs& a, const Cap& c, int steps, const Cut& k, float* part,
-                  hipStream_t s) {
-  switch (steps) {
-    case 1: return pieces_top<IO, 1, CAP>(a, c, k, part, s);
-    case 2: return pieces_top<IO, 2, CAP>(a, c, k, part, s);
-    case 4: return pieces_top<IO, 4, CAP>(a, c, k, part, s);
-    default: return pieces_top<IO, 8, CAP>(a, c, k, part, s);
-  }
+#define BEAM_TOP(n) \
+  hipLaunchKernelGGL((score_top<IO, n, F>), grid, block, 0, s, a, c, k.pieces, k.len, part)
+  if (!a.top)
+    hipLaunchKernelGGL((score_sums<IO, F>), grid, block, 0, s, a, c, k.pieces, k.len, part);
+  else if (steps == 1) BEAM_TOP(1);
+  else if (steps == 2) BEAM_TOP(2);
+  else if (steps == 4) BEAM_TOP(4);
+  else BEAM_TOP(8);
+#undef BEAM_TOP
 }
 
 template <typename IO>
 hipError_t forward(const ScoreArgs& a, float* part, hipStream_t s) {
   const Cap c = make_cap(a.softcap, a.scale);
-  const int steps = steps_for(a.T, a.V);
-  const Cut k = cut(a.V, steps);
-  if (c.on) pieces_steps<IO, true>(a, c, steps, k, part, s);
-  else pieces_steps<IO, false>(a, c, steps, k, part, s);
+  const int steps = steps_for(a.T, a.V, most_steps(a.top));
+  const Cut k = cut(a.V, steps, a.top ? 0 : 7);
+  switch (form_of(c)) {
+    case kPlain: pieces<IO, kPlain>(a, c, steps, k, part, s); break;
+    case kCapped: pieces<IO, kCapped>(a, c, steps, k, part, s); break;
+    default: pieces<IO, kSmall>(a, c, steps, k, part, s);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || k.pieces == 1) return e;
-  hipLaunchKernelGGL((score_join<IO>), dim3(a.T), dim3(kThreads), 0, s, a, c, k.pieces, part);
+  const int staged = k.pieces <= kThreads ? k.pieces * a.top : 0;
+  hipLaunchKernelGGL((score_join<IO>), dim3(a.T), dim3(kThreads), staged * sizeof(Best), s, a, c,
+                     k.pieces, part, staged);
   return hipGetLastError();
 }
 
 template <typename IO>
 hipError_t backward(const ScoreGradArgs& a, hipStream_t s) {
   const Cap c = make_cap(a.softcap, a.scale);
-  const Cut k = cut(a.V, steps_for(a.T, a.V));
+  const Cut k = cut(a.V, steps_for(a.T, a.V, kMaxSteps), 7);
   const dim3 grid(a.T * k.pieces), block(kThreads);
   if (c.on)
     hipLaunchKernelGGL((score_backward<IO, true>), grid, block, 0, s, a, c, k.pieces, k.len);
@@ -434,11 +645,13 @@ hipError_t backward(const ScoreGradArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int64_t score_pieces_count(int64_t T, int64_t V) { return T * cut(V, steps_for(T, V)).pieces; }
+int64_t score_pieces_count(int64_t T, int64_t V) {
+  return T * cut(V, steps_for(T, V, kMaxSteps), 0).pieces;
+}
 
 size_t score_workspace(int64_t T, int64_t V, int top) {
-  const int64_t n = score_pieces_count(T, V);
-  return n == T ? 0 : static_cast<size_t>(n) * (4 + 2 * top) * sizeof(float);
+  const int n = cut(V, steps_for(T, V, most_steps(top)), 0).pieces;
+  return n == 1 ? 0 : static_cast<size_t>(T) * n * (4 + 2 * top) * sizeof(float);
 }
 
 hipError_t launch_token_logprobs(const ScoreArgs& a, int32_t dtype, void* ws, hipStream_t s) {

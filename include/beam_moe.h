@@ -617,8 +617,9 @@ int beam_moe_token_logprobs_workspace_bytes(int64_t T, int64_t V, int32_t top, s
  *             the highest logits in order, equal ones by their index
  * A logit of -infinity is masked: it has probability 0, logp -infinity and
  * gradient 0, also under the cap.  A row of only those has lse and logp
- * -infinity and entropy 0.  A NaN or +infinity makes its row's results NaN
- * (+infinity under the cap is the cap).
+ * -infinity and entropy 0.  A mask of the type's lowest value is a logit like any
+ * other (a row of only those is uniform).  A NaN or +infinity makes its row's
+ * results NaN.
  * 0 <= top <= min(16, V); softcap >= 0, scale > 0, finite; V <= 2^24, T < 2^23. */
 int beam_moe_token_logprobs(int64_t T, int64_t V, int32_t dtype, const void* logits,
                             int64_t row_stride, const int64_t* targets, float softcap, float scale,
@@ -632,7 +633,8 @@ int beam_moe_token_logprobs(int64_t T, int64_t V, int32_t dtype, const void* log
  *   lse, entropy  device [T] fp32: the forward's
  *   d_logits      device [T, V] dtype, rows row_stride elements apart; may be
  *                 logits itself
- * A target outside [0, V) has no gradient of its logprob.  No workspace. */
+ * A target outside [0, V) has no gradient of its logprob.  Probabilities come from
+ * z and the binary32 lse: off by 2^-23 of the larger, relative.  No workspace. */
 int beam_moe_token_logprobs_backward(int64_t T, int64_t V, int32_t dtype, const void* logits,
                                      int64_t row_stride, const int64_t* targets, float softcap,
                                      float scale, const float* lse, const float* entropy,

@@ -190,3 +190,47 @@ def test_empty_batch_and_no_targets():
     assert set(got) == {"lse", "entropy"}
     assert gl.token_logprobs_backward(torch.empty(0, 50, device=dev), *[torch.empty(0, device=dev)] * 2,
                                       d_entropy=torch.empty(0, device=dev)).shape == (0, 50)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [40, 5000, 40000])
+def test_masks_of_the_lowest_value(V, dtype):
+    dev, low = device(), torch.finfo(dtype).min
+    c = make(4, V, dtype, V)
+    c["targets"] = torch.tensor([5, 3, 0, -1])
+    c["logits"][0, ::2], c["logits"][1, 4:], c["logits"][2, :] = low, low, low
+    for softcap in (0.0, 30.0, 500.0):
+        for top in (0, 3):
+            got = gl.token_logprobs(c["logits"].to(dev), c["targets"].to(dev), softcap=softcap, top=top)
+            # (the bound grows with the largest |z|: the rows of ordinary ones alone, too)
+            check(c, got, softcap, 1.0, top)
+            keep = dict(logits=c["logits"][:1, 1::2].contiguous(), targets=torch.tensor([2]))
+            if not softcap:
+                check(keep, {k: got[k][:1] for k in ("lse", "entropy", "logprobs")}, 0.0, 1.0, 0)
+            # a row of the lowest value only is uniform
+            assert abs(got["logprobs"][2].item() + math.log(V)) <= 2e-5 * math.log(V)
+            assert abs(got["entropy"][2].item() - math.log(V)) <= 2e-5 * math.log(V)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0, 500.0])
+def test_infinity_makes_its_row_nan(softcap):
+    dev = device()
+    x = make(3, 700, F32, 11)["logits"]
+    x[1, 650] = math.inf
+    for top in (0, 2):
+        got = gl.token_logprobs(x.to(dev), torch.zeros(3, dtype=torch.int64, device=dev), softcap=softcap, top=top)
+        for k in got:
+            if k != "top_ids":
+                assert torch.isnan(got[k][1]).all() and torch.isfinite(got[k][[0, 2]]).all(), k
+
+
+@pytest.mark.parametrize("softcap,scale", [(30.0, 1.0), (300.0, 1.0), (30.0, 20.0), (0.0, 1.0)])
+@pytest.mark.parametrize("T,V,top", [(1, 300000, 16), (2, 600001, 3), (1500, 9000, 16), (600, 17000, 2)])
+def test_pieces_of_every_length(T, V, top, softcap, scale):
+    # every number of steps a piece, joins of more pieces than threads, caps whose
+    # exponentials need a maximum
+    c = make(T, V, BF16, T, masked=0.01)
+    dev = device()
+    x, t = c["logits"].to(dev), c["targets"].to(dev)
+    for k in (0, top):
+        check(c, gl.token_logprobs(x, t, softcap=softcap, scale=scale, top=k), softcap, scale, k)
