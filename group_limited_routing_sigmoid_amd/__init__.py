@@ -15,8 +15,10 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -112,7 +114,7 @@ def lib():
         L.beam_moe_paged_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, ctypes.POINTER(sz)]
         L.beam_moe_paged_attention.argtypes = [i64, i32, i32, i32, i32, vp, vp, vp, vp, i64, i64, i64,
                                                i64, i64, vp, i64, vp, f32, i64, vp, vp, vp, sz, vp]
-        P = ctypes.POINTER(Pools)
+        P = vp  # a beam_moe_pools, also as its bytes
         L.beam_moe_pages_copy.argtypes = [P, i64, i64, vp, vp, vp]
         L.beam_moe_pages_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(sz)]
         L.beam_moe_pages_update.argtypes = [i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp,
@@ -742,6 +744,14 @@ def rope_frequencies(rot: int, base: float = 10000.0, device="cuda") -> torch.Te
     return base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1)).to(device)
 
 
+@functools.lru_cache(maxsize=256)
+def _size_of(fn: str, *sizes) -> int:
+    """Bytes of workspace of a call of these sizes."""
+    need = ctypes.c_size_t(0)
+    _check(getattr(lib(), fn)(*sizes, ctypes.byref(need)), fn)
+    return need.value
+
+
 def _dtype_code(name: str, dtype: torch.dtype) -> int:
     if dtype is torch.bfloat16:
         return BF16
@@ -753,11 +763,12 @@ def _dtype_code(name: str, dtype: torch.dtype) -> int:
 def _heads(name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple):
     """Address and token stride of heads [T, H, D] whose heads and values are
     contiguous (a view of a projection's output)."""
+    st = t.stride()
     if (t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0
-            and (t.stride(2) == 1 or shape[2] == 1) and (t.stride(1) == shape[2] or shape[1] == 1)):
-        return t.data_ptr(), t.stride(0)
+            and (st[2] == 1 or shape[2] == 1) and (st[1] == shape[2] or shape[1] == 1)):
+        return t.data_ptr(), st[0]
     _arg(name, t, dev, dtype, shape, True)  # raises for all but the strides
-    raise ValueError(f"{name}: strides {t.stride()}, expected a token's heads in one piece")
+    raise ValueError(f"{name}: strides {st}, expected a token's heads in one piece")
 
 
 def _empty_like(on, device, dtype: torch.dtype, *shape) -> torch.Tensor:
@@ -776,15 +787,17 @@ def _cache_args(k_cache, v_cache, tables, dev: int, dtype: torch.dtype, Hkv: int
     if k_cache.dim() != 4 or tables is None or tables.dim() != 2:
         raise ValueError("a cache is k_cache and v_cache [pages, page_size, Hkv, D] with tables "
                          "[seqs, columns]")
-    shape = (k_cache.shape[0], k_cache.shape[1], Hkv, D)
-    pk = _arg("k_cache", k_cache, dev, dtype, shape, True)
-    pv = _arg("v_cache", v_cache, dev, dtype, shape, True)
-    stride = k_cache.stride()
+    shape, stride, cols = k_cache.shape, k_cache.stride(), tables.shape
+    if not (k_cache.dtype is dtype and v_cache.dtype is dtype and shape[2] == Hkv and shape[3] == D
+            and v_cache.shape == shape and k_cache.get_device() == dev == v_cache.get_device() >= 0):
+        want = (shape[0], shape[1], Hkv, D)
+        _arg("k_cache", k_cache, dev, dtype, want, True)
+        _arg("v_cache", v_cache, dev, dtype, want, True)
     if stride[3] != 1 or v_cache.stride() != stride:
         raise ValueError(f"strides of k_cache {stride} and v_cache {v_cache.stride()}: expected the "
                          "same, values contiguous")
-    return (pk, pv, stride[0], stride[1], stride[2], shape[0], shape[1],
-            _arg("tables", tables, dev, torch.int32, tuple(tables.shape)), *tables.shape)
+    return (k_cache.data_ptr(), v_cache.data_ptr(), stride[0], stride[1], stride[2], shape[0], shape[1],
+            _arg("tables", tables, dev, torch.int32, cols), *cols)
 
 
 def _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq, temperature):
@@ -871,19 +884,17 @@ def qk_norm_rope_backward(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: torch
     device, on = q.device, _on(stream, dev)
     pdq = _arg("d_q_out", d_q_out, dev, dtype, (T, Hq, D))
     pdk = _arg("d_k_out", d_k_out, dev, dtype, (T, Hkv, D))
-    need = ctypes.c_size_t(0)
-    _check(lib().beam_moe_qk_norm_rope_workspace_bytes(T, Hq, Hkv, D, ctypes.byref(need)),
-           "beam_moe_qk_norm_rope_workspace_bytes")
+    need = _size_of("beam_moe_qk_norm_rope_workspace_bytes", T, Hq, Hkv, D)
     out = {"d_q": _empty_like(on, device, dtype, T, Hq, D),
            "d_k": _empty_like(on, device, dtype, T, Hkv, D),
            "d_q_weight": _empty(on, device, torch.float32, D),
            "d_k_weight": _empty(on, device, torch.float32, D)}
-    buf = _scratch(need.value, workspace, device, stream)
+    buf = _scratch(need, workspace, device, stream)
     _run(lib().beam_moe_qk_norm_rope_backward, "beam_moe_qk_norm_rope_backward", on, dev,
          (d_q_out, d_k_out, q, k, q_weight, k_weight, positions, inv_freq, *out.values()),
          T, Hq, Hkv, D, code, pdq, pdk, pq, sq, pk, sk, wq, wk, eps, pp, pf, rot,
          1 if interleaved else 0, length, exponent, *(t.data_ptr() for t in out.values()),
-         None if buf is None else buf.data_ptr(), need.value)
+         None if buf is None else buf.data_ptr(), need)
     return out
 
 
@@ -910,47 +921,46 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         raise ValueError(f"tables of {cache[8]} sequences for {B} queries")
     pl = _arg("lengths", lengths, dev, torch.int32, (B,))
     pg = None if gate is None else _arg("gate", gate, dev, dtype, shape)
-    need = ctypes.c_size_t(0)
-    _check(lib().beam_moe_paged_attention_workspace_bytes(B, Hq, Hkv, D, ctypes.byref(need)),
-           "beam_moe_paged_attention_workspace_bytes")
+    need = _size_of("beam_moe_paged_attention_workspace_bytes", B, Hq, Hkv, D)
     if out is None:
         out = _empty_like(on, device, dtype, B, Hq, D)
         po = out.data_ptr()
     else:
         po = _arg("out", out, dev, dtype, shape)
     lse = _empty(on, device, torch.float32, B, Hq) if with_lse else None
-    buf = _scratch(need.value, workspace, device, stream)
+    buf = _scratch(need, workspace, device, stream)
     _run(lib().beam_moe_paged_attention, "beam_moe_paged_attention", on, dev,
          (q, gate, k_cache, v_cache, tables, lengths, out, lse), B, Hq, Hkv, D, code, pq, pg,
          *cache[:8], cache[9], pl, 1.0 / math.sqrt(D) if scale is None else scale, window, po,
-         None if lse is None else lse.data_ptr(), None if buf is None else buf.data_ptr(), need.value)
+         None if lse is None else lse.data_ptr(), None if buf is None else buf.data_ptr(), need)
     return (out, lse) if with_lse else out
 
 
-def _pools(pools, pages: int, dev: int) -> Pools:
-    """The arrays whose pages are copied: tensors [layers, pages, ...] of any
-    dtype, each page of 16-byte multiples and in one piece."""
-    p = Pools()
+_pack_pools = struct.Struct(f"ii{MAX_POOLS}Q{3 * MAX_POOLS}q").pack  # as Pools
+
+
+def _pools(pools, pages: int, dev: int) -> bytes:
+    """beam_moe_pools of the arrays whose pages are copied: tensors [layers,
+    pages, ...] of any dtype, each page of 16-byte multiples and in one piece."""
     if len(pools) > MAX_POOLS:
         raise ValueError(f"{len(pools)} pools, at most {MAX_POOLS}")
-    p.count = len(pools)
+    layers, base, size, by_layer, by_page = 0, [0] * MAX_POOLS, [0] * MAX_POOLS, [0] * MAX_POOLS, [0] * MAX_POOLS
     for i, t in enumerate(pools):
-        if t.dim() < 2 or t.shape[1] != pages:
-            raise ValueError(f"pool of shape {tuple(t.shape)}, expected [layers, {pages} pages, ...]")
-        if i and t.shape[0] != p.layers:
-            raise ValueError(f"pools of {p.layers} and {t.shape[0]} layers")
+        shape, stride = t.shape, t.stride()
+        if len(shape) < 2 or shape[1] != pages:
+            raise ValueError(f"pool of shape {tuple(shape)}, expected [layers, {pages} pages, ...]")
+        if i and shape[0] != layers:
+            raise ValueError(f"pools of {layers} and {shape[0]} layers")
         if t.get_device() != dev:
             raise ValueError(f"a pool on {t.device}, the tables on cuda:{dev}")
-        size = 1
-        for n, stride in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
-            if n != 1 and stride != size:
-                raise ValueError(f"pool strides {t.stride()}: a page has to be in one piece")
-            size *= n
-        item = t.element_size()
-        p.layers = t.shape[0]
-        p.base[i], p.bytes[i] = t.data_ptr(), size * item
-        p.layer_stride[i], p.page_stride[i] = t.stride(0) * item, t.stride(1) * item
-    return p
+        n = 1
+        for d in range(len(shape) - 1, 1, -1):
+            if shape[d] != 1 and stride[d] != n:
+                raise ValueError(f"pool strides {stride}: a page has to be in one piece")
+            n *= shape[d]
+        item, layers = t.element_size(), shape[0]
+        base[i], size[i], by_layer[i], by_page[i] = t.data_ptr(), n * item, stride[0] * item, stride[1] * item
+    return _pack_pools(len(pools), layers, *base, *size, *by_layer, *by_page)
 
 
 def _pages_inputs(tables, lengths, refs, page_size: int):
@@ -965,11 +975,9 @@ def _pages_inputs(tables, lengths, refs, page_size: int):
 
 
 def _pages_scratch(pages: int, rows: int, workspace, device, stream):
-    need = ctypes.c_size_t(0)
-    _check(lib().beam_moe_pages_workspace_bytes(pages, rows, ctypes.byref(need)),
-           "beam_moe_pages_workspace_bytes")
-    buf = _scratch(need.value, workspace, device, stream)
-    return None if buf is None else buf.data_ptr(), need.value
+    need = _size_of("beam_moe_pages_workspace_bytes", pages, rows)
+    buf = _scratch(need, workspace, device, stream)
+    return None if buf is None else buf.data_ptr(), need
 
 
 def pages_update(tables: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor, page_size: int,
@@ -993,7 +1001,7 @@ def pages_update(tables: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor
     ws, need = _pages_scratch(pages, rows, workspace, device, stream)
     _run(lib().beam_moe_pages_update, "beam_moe_pages_update", on, dev,
          (tables, lengths, refs, parents, grow, *pools, *out.values()), old, rows, cols, pages,
-         page_size, pt, pl, pr, pp, pg, *(t.data_ptr() for t in out.values()), ctypes.byref(p), ws, need)
+         page_size, pt, pl, pr, pp, pg, *(t.data_ptr() for t in out.values()), p, ws, need)
     return out
 
 
@@ -1010,7 +1018,7 @@ def pages_compact(tables: torch.Tensor, lengths: torch.Tensor, refs: torch.Tenso
     ws, need = _pages_scratch(pages, rows, workspace, device, stream)
     _run(lib().beam_moe_pages_compact, "beam_moe_pages_compact", on, dev,
          (tables, lengths, refs, *pools, *out.values()), rows, cols, pages, page_size, pt, pl, pr,
-         *(t.data_ptr() for t in out.values()), ctypes.byref(p), ws, need)
+         *(t.data_ptr() for t in out.values()), p, ws, need)
     return out
 
 
@@ -1024,7 +1032,7 @@ def pages_copy(pools, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None
     pd = _arg("dst", dst, dev, torch.int32, (n,))
     p = _pools(pools, pages, dev)
     _run(lib().beam_moe_pages_copy, "beam_moe_pages_copy", _on(stream, dev), dev, (src, dst, *pools),
-         ctypes.byref(p), pages, n, ps, pd)
+         p, pages, n, ps, pd)
 
 
 def _logits(name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple):
@@ -1050,9 +1058,7 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     pl, stride = _logits("logits", logits, dev, logits.dtype, (T, V))
     pt = None if targets is None else _arg("targets", targets, dev, torch.int64, (T,))
     device, on, f32 = logits.device, _on(stream, dev), torch.float32
-    need = ctypes.c_size_t(0)
-    _check(lib().beam_moe_token_logprobs_workspace_bytes(T, V, top, ctypes.byref(need)),
-           "beam_moe_token_logprobs_workspace_bytes")
+    need = _size_of("beam_moe_token_logprobs_workspace_bytes", T, V, top)
     out = {"lse": _empty(on, device, f32, T), "entropy": _empty(on, device, f32, T)}
     lp = ids = tl = None
     if targets is not None:
@@ -1060,12 +1066,12 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     if top:
         ids = out["top_ids"] = _empty(on, device, torch.int32, T, top)
         tl = out["top_logprobs"] = _empty(on, device, f32, T, top)
-    buf = _scratch(need.value, workspace, device, stream)
+    buf = _scratch(need, workspace, device, stream)
     _run(lib().beam_moe_token_logprobs, "beam_moe_token_logprobs", on, dev,
          (logits, targets, *out.values()), T, V, code, pl, stride, pt, softcap, scale, top,
          None if lp is None else lp.data_ptr(), out["entropy"].data_ptr(), out["lse"].data_ptr(),
          None if ids is None else ids.data_ptr(), None if tl is None else tl.data_ptr(),
-         None if buf is None else buf.data_ptr(), need.value)
+         None if buf is None else buf.data_ptr(), need)
     return out
 
 

@@ -21,12 +21,15 @@
 // tokens meet the other lanes' at the end.
 //
 // The work is counted in units of 64 tokens (16 for each of a workgroup's four
-// waves).  Where a sequence can hold only few units (a window) a workgroup takes
-// one block of heads of one sequence.  Else the units of all sequences are cut
-// into slices of one size, whatever the sequences' lengths, a workgroup for each
-// slice and block of heads (neighbouring workgroups read the heads of the same
-// tokens at the same time): each finds its first unit from the lengths, and leaves
-// sums for the sequences that it did not see whole, which a second kernel joins.
+// waves; 256 where sixteen waves share a sequence).  Where a sequence can hold
+// only few units (a window) a workgroup takes one block of heads of one sequence.
+// Else the units of all sequences are cut into slices of one size, whatever the
+// sequences' lengths, a workgroup for each slice and block of heads (neighbouring
+// workgroups read the heads of the same tokens at the same time): each finds its
+// first unit from the lengths, and leaves sums for the sequences that it did not
+// see whole, which a second kernel joins.
+// 1,000,003 tokens of 8 heads of 128: 690 us, 5.9 TB/s (6.35 is what reading alone
+// reaches); 64 sequences of 100 to 32,000: 257 us, 5.7; 256 windows of 512: 100.
 #include <algorithm>
 
 #include "serve.h"
@@ -34,10 +37,9 @@
 namespace beam {
 namespace {
 
-constexpr int kUnit = 64;    // tokens of a unit
 constexpr int kStep = 16;    // tokens of a wave's step
-constexpr int kWaves = 4;
 constexpr int kRows = 16;    // query heads of a block
+constexpr int kSplitWaves = 4;
 constexpr int kSlots = 512;  // workgroups that the split form fills
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.0e38f;  // a maximum that any score passes
@@ -48,6 +50,7 @@ struct Seq {
   int first, end;  // tokens that take part
   int unit0, units;
 };
+template <int kUnit>
 __device__ __forceinline__ Seq seq_of(int len, int window, int most) {
   Seq q;
   q.end = min(max(len, 0), most);
@@ -116,9 +119,10 @@ struct Segment {
 
 // FAST: pages of 16 tokens or more, so that a wave's step lies in one page, and D
 // = DK; else a lane looks up its token's page and masks the values past D.
-template <typename IO, int DK, bool FAST>
+template <typename IO, int DK, bool FAST, int W>
 struct Attend {
   using T = Tile<IO, DK>;
+  static constexpr int kWaves = W, kUnit = W * kStep;
   static constexpr int kAcc = DK / 16;
   static constexpr int kPad = 4;
 
@@ -395,16 +399,16 @@ struct Attend {
 };
 
 // A workgroup for each block of heads of each sequence.
-template <typename IO, int DK, bool FAST>
-__global__ __launch_bounds__(kWaves* kWave) void attend_whole(AttendArgs a) {
-  using A = Attend<IO, DK, FAST>;
+template <typename IO, int DK, bool FAST, int W>
+__global__ __launch_bounds__(W* kWave) void attend_whole(AttendArgs a) {
+  using A = Attend<IO, DK, FAST, W>;
   extern __shared__ float sh[];
   A at(a);
   const int blocks = a.Hkv * at.rows_blocks;
   Segment g;
   g.seq = blockIdx.x / blocks;
   g.block = blockIdx.x % blocks;
-  at.s = seq_of(a.lengths[g.seq], a.window, a.cache.cols << a.cache.shift);
+  at.s = seq_of<A::kUnit>(a.lengths[g.seq], a.window, a.cache.cols << a.cache.shift);
   g.from = 0;
   g.to = at.s.units;
   at.run(g, nullptr, sh);
@@ -440,9 +444,9 @@ __device__ __forceinline__ float* part_of(const AttendArgs& a, int blocks, int s
 
 // The units of all sequences in slices of one size, at least `least` units.
 template <typename IO, int DK, bool FAST>
-__global__ __launch_bounds__(kWaves* kWave) void attend_split(AttendArgs a, Open* open, int slices,
+__global__ __launch_bounds__(kSplitWaves* kWave) void attend_split(AttendArgs a, Open* open, int slices,
                                                                uint32_t least) {
-  using A = Attend<IO, DK, FAST>;
+  using A = Attend<IO, DK, FAST, kSplitWaves>;
   extern __shared__ float sh[];
   A at(a);
   const int blocks = a.Hkv * at.rows_blocks, most = a.cache.cols << a.cache.shift;
@@ -450,7 +454,7 @@ __global__ __launch_bounds__(kWaves* kWave) void attend_split(AttendArgs a, Open
   const int slice = blockIdx.x / blocks;
   // every wave counts the units for itself
   auto units = [&](int b) -> uint32_t {
-    return b < seqs ? seq_of(a.lengths[b], a.window, most).units : 0;
+    return b < seqs ? seq_of<A::kUnit>(a.lengths[b], a.window, most).units : 0;
   };
   uint32_t total = 0;
   for (int b = lane; b < seqs; b += kWave) total += units(b);
@@ -479,7 +483,7 @@ __global__ __launch_bounds__(kWaves* kWave) void attend_split(AttendArgs a, Open
   Segment g;
   g.seq = __builtin_amdgcn_readfirstlane(b);
   g.block = blockIdx.x % blocks;
-  at.s = seq_of(a.lengths[g.seq], a.window, most);
+  at.s = seq_of<A::kUnit>(a.lengths[g.seq], a.window, most);
   g.from = static_cast<int>(unit - before);
   Open left = {-1, 0};
   while (unit < stop) {
@@ -490,7 +494,7 @@ __global__ __launch_bounds__(kWaves* kWave) void attend_split(AttendArgs a, Open
     at.run(g, begins && ends ? nullptr : part_of(a, blocks, slice, g.block, begins), sh);
     unit += g.to - g.from;
     g.from = 0;
-    if (++g.seq < seqs) at.s = seq_of(a.lengths[g.seq], a.window, most);
+    if (++g.seq < seqs) at.s = seq_of<A::kUnit>(a.lengths[g.seq], a.window, most);
   }
   if (threadIdx.x == 0) open[slice] = left;
 }
@@ -566,21 +570,32 @@ int slices_of(int blocks) {
   return std::max(1, kSlots / blocks);
 }
 
+template <typename IO, int DK, bool FAST, int W>
+hipError_t whole(const AttendArgs& a, int64_t segs, hipStream_t s) {
+  const int shared = Attend<IO, DK, FAST, W>::shared_bytes(a.Hq / a.Hkv);
+  hipLaunchKernelGGL((attend_whole<IO, DK, FAST, W>), dim3(segs), dim3(W * kWave), shared, s, a);
+  return hipGetLastError();
+}
+
 template <typename IO, int DK, bool FAST>
 hipError_t launch(const AttendArgs& a, hipStream_t s) {
+  constexpr int W = kSplitWaves;
   const int blocks = head_blocks(a.Hq, a.Hkv);
   const int64_t segs = a.cache.seqs * blocks;
   const int64_t most = static_cast<int64_t>(a.cache.cols) << a.cache.shift;
-  // units that a segment can have
-  const int64_t units = a.window && a.window < most ? ceil_div(a.window - 1, kUnit) + 1
-                                                    : ceil_div(most, kUnit);
-  const dim3 block(kWaves * kWave);
-  const int shared = Attend<IO, DK, FAST>::shared_bytes(a.Hq / a.Hkv);
+  // tokens and units that a sequence can have
+  const int64_t tokens = a.window && a.window < most ? a.window + W * kStep : most;
+  const int64_t units = ceil_div(tokens, W * kStep);
   const int slices = static_cast<int>(std::min<int64_t>(slices_of(blocks), a.cache.seqs * units));
-  if (slices <= 1 || units <= 2 || (segs >= 512 && units <= 16)) {
-    hipLaunchKernelGGL((attend_whole<IO, DK, FAST>), dim3(segs), block, shared, s, a);
-    return hipGetLastError();
-  }
+  // Two units or fewer: nothing to split.  A window's (17 units at most): whole
+  // ones fill the card from 512 on; from 128 on with sixteen waves for each (32
+  // sequences of 900 or 500 tokens, 8 heads: 24 and 16 us, in slices 34 and 22;
+  // 8 of 900 20, in slices 17).
+  if (slices <= 1 || units <= 2 || (segs >= 512 && units <= 17)) return whole<IO, DK, FAST, W>(a, segs, s);
+  if constexpr (FAST && sizeof(IO) == 2 && DK <= 128)
+    if (segs >= 128 && units <= 17) return whole<IO, DK, FAST, 16>(a, segs, s);
+  const dim3 block(W * kWave);
+  const int shared = Attend<IO, DK, FAST, W>::shared_bytes(a.Hq / a.Hkv);
   Open* open = reinterpret_cast<Open*>(a.part + static_cast<int64_t>(slices_of(blocks)) * blocks *
                                                     2 * part_size(a.D));
   hipLaunchKernelGGL((attend_split<IO, DK, FAST>), dim3(slices * blocks), block, shared, s, a, open,

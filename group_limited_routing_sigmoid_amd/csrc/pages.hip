@@ -5,8 +5,12 @@
 //
 // Everything is decided by integers: references by counts (integer atomics,
 // whose order changes nothing), pages by their rank among the free ones, wants
-// by their place in the rows' order.  The tables' part is bound by its few
-// dependent launches, the copies' by reading and writing the pages once.
+// by their place in the rows' order.  The tables' part is a chain of short steps,
+// each of which needs the one before whole: four launches and the copies', or,
+// for a pool and a batch that one workgroup holds in LDS, one (32 rows of 189 pages,
+// a pool of 1,000: 7 us, where the four launches took 18; 512 rows, a pool of
+// 28,000: 18 us in four, and 24 for copies of 130 MB).  The copies are bound by
+// reading and writing the pages once (2.8 GB in 541 us).
 #include <algorithm>
 #include <climits>
 
@@ -27,6 +31,8 @@ struct Space {  // workspace
   int32_t* counts;    // [blocks] free (or used) pages of a block
   int32_t* begin;     // [rows + 1] a row's first want among all
   int32_t* copied;    // [rows] the page that a row copies, or -1
+  int32_t* list;      // [pages] free pages in order, as many as are wanted
+  int32_t* given;     // [1] how many those are
   int32_t* children;  // [old rows]
   int32_t* over;      // [1] pages wanted past the columns
 };
@@ -60,23 +66,34 @@ __device__ __forceinline__ int open_page(const PageArgs& a, const Row& r) {
   return p >= 0 && p < a.pages ? p : -1;
 }
 
+// ONCE: past the caches' usual order, where many pages move (549 us instead of 563
+// for 2.8 GB; a copied page that is read again soon stays in them).
+template <bool ONCE>
 __device__ __forceinline__ void copy_page(const beam_moe_pools& p, int part, int src, int dst) {
   const int i = part / p.layers, layer = part % p.layers;
   char* base = static_cast<char*>(p.base[i]) + layer * p.layer_stride[i];
   const char* from = base + src * p.page_stride[i];
   char* to = base + dst * p.page_stride[i];
   const int64_t n = p.bytes[i];
+  auto read = [&](int64_t at) {
+    const u32x4* x = reinterpret_cast<const u32x4*>(from + at);
+    return ONCE ? __builtin_nontemporal_load(x) : *x;
+  };
+  auto write = [&](int64_t at, u32x4 v) {
+    u32x4* x = reinterpret_cast<u32x4*>(to + at);
+    if (ONCE) __builtin_nontemporal_store(v, x);
+    else *x = v;
+  };
   int64_t at = static_cast<int64_t>(threadIdx.x) * 16;
   const int64_t step = static_cast<int64_t>(blockDim.x) * 16;
   for (; at + 3 * step < n; at += 4 * step) {
-    const u32x4 v0 = ld16(from + at), v1 = ld16(from + at + step), v2 = ld16(from + at + 2 * step),
-                v3 = ld16(from + at + 3 * step);
-    st16(to + at, v0);
-    st16(to + at + step, v1);
-    st16(to + at + 2 * step, v2);
-    st16(to + at + 3 * step, v3);
+    u32x4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = read(at + u * step);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) write(at + u * step, v[u]);
   }
-  for (; at < n; at += step) st16(to + at, ld16(from + at));
+  for (; at < n; at += step) write(at, read(at));
 }
 
 // Sum over the workgroup's threads before this one; *total the sum over all.
@@ -181,7 +198,6 @@ __global__ __launch_bounds__(kDemand) void update_count(PageArgs a, Space w) {
         if (refs != 1 && !(refs == w.writers[p] && w.lowest[p] == i)) copy = p;
       }
       w.copied[i] = copy;
-      if (copy >= 0) a.tables_out[i * a.cols + r.have - 1] = -1;  // until it has one
       want = (copy >= 0) + min(r.need, most) - r.have;
       over += max(r.need - most, 0);
       const int64_t size = static_cast<int64_t>(r.held) + r.grow;
@@ -198,60 +214,154 @@ __global__ __launch_bounds__(kDemand) void update_count(PageArgs a, Space w) {
   }
 }
 
-// Each free page goes to the want of its rank.  (A copied page keeps at least
-// one reference, so giving one of its references up here frees none.)
-__global__ __launch_bounds__(kThreads) void update_give(PageArgs a, Space w, int blocks) {
+// The free pages in order, as far as they are wanted.  (A copied page keeps at
+// least one reference, so giving one of its references up here frees none.)
+__global__ __launch_bounds__(kThreads) void update_list(PageArgs a, Space w, int blocks) {
   const int rows = static_cast<int>(a.rows), wants = w.begin[rows];
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  for (int64_t i = id; i < rows; i += static_cast<int64_t>(gridDim.x) * kThreads)
-    if (w.copied[i] >= 0) atomicSub(&a.refs_out[w.copied[i]], 1);
-  int n = 0;
-  if (blockIdx.x == 0) {
-    for (int b = threadIdx.x; b < blocks; b += kThreads) n += w.counts[b];
-    n = sum_all(n);
-    if (threadIdx.x == 0) *a.count = max(wants - n, 0) + *w.over;
-  }
-  n = 0;
-  for (int b = threadIdx.x; b < static_cast<int>(blockIdx.x); b += kThreads) n += w.counts[b];
-  const int before = sum_all(n);
-  if (before >= wants) return;
   const int64_t p0 = id * kEach;
-  bool free[kEach];
-  n = 0;
+  int refs[kEach];
 #pragma unroll
-  for (int j = 0; j < kEach; ++j) {
-    free[j] = p0 + j < a.pages && a.refs_out[p0 + j] <= 0;
-    n += free[j];
+  for (int j = 0; j < kEach; ++j) refs[j] = p0 + j < a.pages ? a.refs_out[p0 + j] : 1;
+  int all = 0, mine = 0;  // free pages of every block, of those before this one
+  for (int b = threadIdx.x; b < blocks; b += kThreads) {
+    const int n = w.counts[b];
+    all += n;
+    if (b < static_cast<int>(blockIdx.x)) mine += n;
   }
-  int total;
+  const int before = sum_all(mine);
+  if (blockIdx.x == 0) {
+    all = sum_all(all);
+    if (threadIdx.x == 0) {
+      *a.count = max(wants - all, 0) + *w.over;
+      *w.given = min(wants, all);
+    }
+  }
+  int n = 0, total;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) n += refs[j] <= 0;
   int rank = before + scan<kThreads>(n, &total);
 #pragma unroll
-  for (int j = 0; j < kEach; ++j) {
-    if (!free[j]) continue;
-    if (rank >= wants) break;
-    int lo = 0, hi = rows - 1;  // the last row whose first want is no later
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (w.begin[mid] <= rank) lo = mid;
-      else hi = mid - 1;
+  for (int j = 0; j < kEach; ++j)
+    if (refs[j] <= 0) {
+      if (rank < wants) {
+        w.list[rank] = static_cast<int>(p0 + j);
+        a.refs_out[p0 + j] = 1;
+      }
+      ++rank;
     }
-    const Row r = row_of(a, lo);
-    const int slot = r.have + rank - w.begin[lo] - (w.copied[lo] >= 0);
-    a.tables_out[lo * a.cols + slot] = static_cast<int>(p0 + j);
-    a.refs_out[p0 + j] = 1;
-    ++rank;
+  for (int64_t i = id; i < rows; i += static_cast<int64_t>(gridDim.x) * kThreads)
+    if (w.copied[i] >= 0) atomicSub(&a.refs_out[w.copied[i]], 1);
+}
+
+// A row's new entries (`fill`), and its copy in one layer of one array: a
+// workgroup for each, which take turns.
+__global__ __launch_bounds__(kThreads) void update_copy(PageArgs a, Space w, beam_moe_pools p,
+                                                         bool fill) {
+  const int parts = max(p.count * p.layers, 1);
+  for (int64_t x = blockIdx.x; x < a.rows * parts; x += gridDim.x) {
+    const int i = static_cast<int>(x / parts), part = static_cast<int>(x % parts);
+    const int src = w.copied[i], begin = w.begin[i], given = *w.given;
+    const bool copies = src >= 0;
+    if (fill && part == 0) {
+      const int n = w.begin[i + 1] - begin, have = n > 0 ? row_of(a, i).have : 0;
+      for (int j = threadIdx.x; j < n; j += kThreads)
+        a.tables_out[i * a.cols + have + j - copies] = begin + j < given ? w.list[begin + j] : -1;
+    }
+    if (copies && begin < given && p.count * p.layers > 0) copy_page<false>(p, part, src, w.list[begin]);
   }
 }
 
-// A workgroup takes rows' copies in one layer of one array.
-__global__ __launch_bounds__(kThreads) void update_copy(PageArgs a, Space w, beam_moe_pools p) {
-  const int parts = p.count * p.layers;
-  for (int64_t x = blockIdx.x; x < a.rows * parts; x += gridDim.x) {
-    const int i = static_cast<int>(x / parts), src = w.copied[i];
-    if (src < 0) continue;
-    const int dst = a.tables_out[i * a.cols + row_of(a, i).have - 1];
-    if (dst >= 0) copy_page(p, static_cast<int>(x % parts), src, dst);
+// All of the tables' part in one workgroup: references and who writes where in LDS.
+constexpr int kSmallPages = 8192, kSmallRows = kDemand, kSmallEntries = 1 << 16;
+__global__ __launch_bounds__(kDemand) void update_small(PageArgs a, Space w) {
+  extern __shared__ int32_t lds[];
+  const int pages = static_cast<int>(a.pages), rows = static_cast<int>(a.rows);
+  const int old_rows = static_cast<int>(a.old_rows), cols = static_cast<int>(a.cols);
+  int32_t* const refs = lds;
+  int32_t* const writers = refs + pages;  // later the list of free pages
+  int32_t* const lowest = writers + pages;
+  int32_t* const children = lowest + pages;
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  constexpr int kWaves = kDemand / kWave;
+  // the thread's row
+  const bool mine = tid < rows;
+  Row r = {};
+  if (mine) r = row_of(a, tid);
+  const int open = mine ? open_page(a, r) : -1;
+  for (int p = tid; p < pages; p += kDemand) {
+    refs[p] = a.refs[p];
+    writers[p] = 0;
+    lowest[p] = INT_MAX;
   }
+  if (tid < old_rows) children[tid] = a.parents || rows == 0 ? 0 : 1;
+  __syncthreads();
+  if (a.parents && mine && r.parent >= 0) atomicAdd(&children[r.parent], 1);
+  if (open >= 0) {
+    atomicAdd(&writers[open], 1);
+    atomicMin(&lowest[open], tid);
+  }
+  for (int i = wave; i < rows; i += kWaves) {
+    const Row x = row_of(a, i);
+    const int32_t* from = a.tables + max(x.parent, 0) * cols;
+    for (int c = lane; c < cols; c += kWave) a.tables_out[i * cols + c] = c < x.have ? from[c] : -1;
+  }
+  __syncthreads();
+  for (int i = wave; i < old_rows; i += kWaves) {
+    const int by = children[i] - 1;
+    if (by == 0) continue;
+    const int have = pages_for(a, held_tokens(a, i));
+    for (int c = lane; c < have; c += kWave) {
+      const int p = a.tables[i * cols + c];
+      if (p >= 0 && p < pages) atomicAdd(&refs[p], by);
+    }
+  }
+  __syncthreads();
+  int copy = -1, want = 0, over = 0, wants, overs;
+  if (mine) {
+    if (open >= 0 && refs[open] != 1 && !(refs[open] == writers[open] && lowest[open] == tid)) copy = open;
+    want = (copy >= 0) + min(r.need, cols) - r.have;
+    over = max(r.need - cols, 0);
+    a.lengths_out[tid] =
+        static_cast<int>(min<int64_t>(static_cast<int64_t>(r.held) + r.grow, a.cols << a.shift));
+  }
+  const int begin = scan<kDemand>(want, &wants);
+  scan<kDemand>(over, &overs);
+  // free pages: eight neighbours a thread
+  int n = 0, all;
+  bool free[kEach];
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int p = tid * kEach + j;
+    free[j] = p < pages && refs[p] <= 0;
+    n += free[j];
+  }
+  int rank = scan<kDemand>(n, &all);
+#pragma unroll
+  for (int j = 0; j < kEach; ++j)
+    if (free[j]) {
+      if (rank < wants) {
+        writers[rank] = tid * kEach + j;
+        refs[tid * kEach + j] = 1;
+      }
+      ++rank;
+    }
+  __syncthreads();
+  const int given = min(wants, all);
+  if (copy >= 0) atomicSub(&refs[copy], 1);
+  if (mine) {
+    for (int j = 0; j < want; ++j)
+      a.tables_out[tid * cols + r.have + j - (copy >= 0)] = begin + j < given ? writers[begin + j] : -1;
+    w.copied[tid] = copy;
+    w.begin[tid] = begin;
+    if (copy >= 0 && begin < given) w.list[begin] = writers[begin];
+  }
+  if (tid == 0) {
+    *w.given = given;
+    *a.count = max(wants - all, 0) + overs;
+  }
+  __syncthreads();
+  for (int p = tid; p < pages; p += kDemand) a.refs_out[p] = refs[p];
 }
 
 __global__ __launch_bounds__(kThreads) void copy_list(beam_moe_pools p, int64_t pages, int64_t n,
@@ -259,7 +369,7 @@ __global__ __launch_bounds__(kThreads) void copy_list(beam_moe_pools p, int64_t 
   const int parts = p.count * p.layers;
   for (int64_t x = blockIdx.x; x < n * parts; x += gridDim.x) {
     const int s = src[x / parts], d = dst[x / parts];
-    if (s >= 0 && s < pages && d >= 0 && d < pages) copy_page(p, static_cast<int>(x % parts), s, d);
+    if (s >= 0 && s < pages && d >= 0 && d < pages) copy_page<true>(p, static_cast<int>(x % parts), s, d);
   }
 }
 
@@ -351,7 +461,7 @@ __global__ __launch_bounds__(kThreads) void pack_move(PageArgs a, PackSpace w, b
   const int64_t items = static_cast<int64_t>(moves) * parts;
   for (int64_t x = blockIdx.x; x < items; x += gridDim.x) {
     const int i = static_cast<int>(x / parts);
-    copy_page(p, static_cast<int>(x % parts), w.from[i], w.to[i]);
+    copy_page<true>(p, static_cast<int>(x % parts), w.from[i], w.to[i]);
   }
 }
 
@@ -366,9 +476,9 @@ int32_t* carve(P*& at, int64_t n) {
 
 size_t pages_workspace(int64_t pages, int64_t rows) {
   auto room = [](int64_t n) { return ceil_div(n, 64) * 64; };
-  // from, to and rank of a packing; writers and lowest of an update
+  // from, to and rank of a packing; writers, lowest and list of an update
   return sizeof(int32_t) * static_cast<size_t>(3 * room(pages) + room(ceil_div(pages, kBlock)) +
-                                               2 * room(rows + 1) + room(65536) + room(1));
+                                               2 * room(rows + 1) + room(65536) + 2 * room(1));
 }
 
 hipError_t launch_pages_copy(const beam_moe_pools& p, int64_t pages, int64_t n, const int32_t* src,
@@ -391,16 +501,27 @@ hipError_t launch_pages_update(const PageArgs& a, const beam_moe_pools& p, void*
   w.copied = carve(at, a.rows);
   w.children = carve(at, a.old_rows);
   w.over = carve(at, 1);
+  w.given = carve(at, 1);
+  w.list = carve(at, a.pages);
+  const int64_t copies = std::min(a.rows * p.count * p.layers, kCopyBlocks);
+  if (a.pages <= kSmallPages && std::max(a.rows, a.old_rows) <= kSmallRows &&
+      std::max(a.rows, a.old_rows) * a.cols <= kSmallEntries) {
+    const size_t shared = static_cast<size_t>(3 * a.pages + a.old_rows) * sizeof(int32_t);
+    hipLaunchKernelGGL(update_small, dim3(1), dim3(kDemand), shared, s, a, w);
+    if (copies)
+      hipLaunchKernelGGL(update_copy, dim3(copies), dim3(kThreads), 0, s, a, w, p, false);
+    return hipGetLastError();
+  }
   const int64_t work = std::max(a.pages, a.old_rows * kWave);
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(ceil_div(work, kThreads), 2048));
   hipLaunchKernelGGL(update_prepare, dim3(grid), dim3(kThreads), 0, s, a, w);
   if (a.rows + a.old_rows)
     hipLaunchKernelGGL(update_rows, dim3(a.rows + a.old_rows), dim3(kThreads), 0, s, a, w);
   hipLaunchKernelGGL(update_count, dim3(blocks + 1), dim3(kDemand), 0, s, a, w);
-  hipLaunchKernelGGL(update_give, dim3(std::max(blocks, 1)), dim3(kThreads), 0, s, a, w, blocks);
-  const int64_t copies = std::min(a.rows * p.count * p.layers, kCopyBlocks);
-  if (copies)
-    hipLaunchKernelGGL(update_copy, dim3(copies), dim3(kThreads), 0, s, a, w, p);
+  hipLaunchKernelGGL(update_list, dim3(std::max(blocks, 1)), dim3(kThreads), 0, s, a, w, blocks);
+  if (a.rows)
+    hipLaunchKernelGGL(update_copy, dim3(std::max(copies, std::min(a.rows, kCopyBlocks))),
+                       dim3(kThreads), 0, s, a, w, p, true);
   return hipGetLastError();
 }
 
