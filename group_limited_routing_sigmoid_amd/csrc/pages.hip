@@ -40,14 +40,18 @@ struct Space {  // workspace
 struct Row {  // what a new row has and wants
   int parent;  // or -1
   int held, grow;
-  int have, need;  // pages
+  int have, need;  // pages; need: at most the columns
+  int64_t over;    // pages past those
 };
 
 __device__ __forceinline__ int held_tokens(const PageArgs& a, int r) {
   return min(max(a.lengths[r], 0), static_cast<int>(a.cols << a.shift));
 }
-__device__ __forceinline__ int pages_for(const PageArgs& a, int64_t tokens) {
-  return static_cast<int>((tokens + (int64_t{1} << a.shift) - 1) >> a.shift);
+__device__ __forceinline__ int64_t pages_for(const PageArgs& a, int64_t tokens) {
+  return (tokens + (int64_t{1} << a.shift) - 1) >> a.shift;
+}
+__device__ __forceinline__ int held_pages(const PageArgs& a, int r) {
+  return static_cast<int>(pages_for(a, held_tokens(a, r)));
 }
 __device__ __forceinline__ Row row_of(const PageArgs& a, int i) {
   Row r;
@@ -55,8 +59,10 @@ __device__ __forceinline__ Row row_of(const PageArgs& a, int i) {
   if (r.parent < 0 || r.parent >= a.old_rows) r.parent = -1;
   r.held = r.parent < 0 ? 0 : held_tokens(a, r.parent);
   r.grow = a.grow ? max(a.grow[i], 0) : 0;
-  r.have = pages_for(a, r.held);
-  r.need = pages_for(a, static_cast<int64_t>(r.held) + r.grow);
+  r.have = static_cast<int>(pages_for(a, r.held));
+  const int64_t need = pages_for(a, static_cast<int64_t>(r.held) + r.grow);
+  r.need = static_cast<int>(min<int64_t>(need, a.cols));
+  r.over = need - r.need;
   return r;
 }
 // The unfilled last page that the row is going to write to, or -1.
@@ -119,6 +125,23 @@ __device__ __forceinline__ int scan(int v, int* total) {
   *total = all;
   return before + sum - v;
 }
+// Sum of v over the workgroup, held to an int32.
+template <int kN>
+__device__ __forceinline__ int sum_long(int64_t v) {
+  __shared__ int64_t waves[kN / kWave];
+#pragma unroll
+  for (int i = 1; i < kWave; i *= 2) v += __shfl_xor(v, i);
+  __syncthreads();
+  if (threadIdx.x % kWave == 0) waves[threadIdx.x / kWave] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int i = 0; i < kN / kWave; ++i) v += waves[i];
+  return static_cast<int>(min<int64_t>(v, INT_MAX));
+}
+__device__ __forceinline__ int add_held(int a, int b) {  // of two counts
+  return static_cast<int>(min<int64_t>(static_cast<int64_t>(a) + b, INT_MAX));
+}
 // Sum of v over the workgroup.
 __device__ __forceinline__ int sum_all(int v) {
   int total;
@@ -165,7 +188,7 @@ __global__ __launch_bounds__(kThreads) void update_rows(PageArgs a, Space w) {
   const int r = blockIdx.x - static_cast<int>(a.rows);
   const int by = w.children[r] - 1;
   if (by == 0) return;
-  const int have = pages_for(a, held_tokens(a, r));
+  const int have = held_pages(a, r);
   for (int64_t c = threadIdx.x; c < have; c += kThreads) {
     const int p = a.tables[r * a.cols + c];
     if (p >= 0 && p < a.pages) atomicAdd(&a.refs_out[p], by);
@@ -185,21 +208,22 @@ __global__ __launch_bounds__(kDemand) void update_count(PageArgs a, Space w) {
     if (threadIdx.x == 0) w.counts[blockIdx.x - 1] = total;
     return;
   }
-  int before = 0, over = 0;
+  int before = 0;
+  int64_t over = 0;
   for (int64_t i0 = 0; i0 < a.rows; i0 += kDemand) {
     const int64_t i = i0 + threadIdx.x;
     int want = 0;
     if (i < a.rows) {
       const Row r = row_of(a, static_cast<int>(i));
-      const int p = open_page(a, r), most = static_cast<int>(a.cols);
+      const int p = open_page(a, r);
       int copy = -1;
       if (p >= 0) {
         const int refs = a.refs_out[p];
         if (refs != 1 && !(refs == w.writers[p] && w.lowest[p] == i)) copy = p;
       }
       w.copied[i] = copy;
-      want = (copy >= 0) + min(r.need, most) - r.have;
-      over += max(r.need - most, 0);
+      want = (copy >= 0) + r.need - r.have;
+      over += r.over;
       const int64_t size = static_cast<int64_t>(r.held) + r.grow;
       a.lengths_out[i] = static_cast<int>(min<int64_t>(size, a.cols << a.shift));
     }
@@ -207,10 +231,10 @@ __global__ __launch_bounds__(kDemand) void update_count(PageArgs a, Space w) {
     if (i < a.rows) w.begin[i] = before + first;
     before += total;
   }
-  scan<kDemand>(over, &total);
+  const int overs = sum_long<kDemand>(over);
   if (threadIdx.x == 0) {
     w.begin[a.rows] = before;
-    *w.over = total;
+    *w.over = overs;
   }
 }
 
@@ -233,7 +257,7 @@ __global__ __launch_bounds__(kThreads) void update_list(PageArgs a, Space w, int
   if (blockIdx.x == 0) {
     all = sum_all(all);
     if (threadIdx.x == 0) {
-      *a.count = max(wants - all, 0) + *w.over;
+      *a.count = add_held(max(wants - all, 0), *w.over);
       *w.given = min(wants, all);
     }
   }
@@ -310,23 +334,24 @@ __global__ __launch_bounds__(kDemand) void update_small(PageArgs a, Space w) {
   for (int i = wave; i < old_rows; i += kWaves) {
     const int by = children[i] - 1;
     if (by == 0) continue;
-    const int have = pages_for(a, held_tokens(a, i));
+    const int have = held_pages(a, i);
     for (int c = lane; c < have; c += kWave) {
       const int p = a.tables[i * cols + c];
       if (p >= 0 && p < pages) atomicAdd(&refs[p], by);
     }
   }
   __syncthreads();
-  int copy = -1, want = 0, over = 0, wants, overs;
+  int copy = -1, want = 0, wants;
+  int64_t over = 0;
   if (mine) {
     if (open >= 0 && refs[open] != 1 && !(refs[open] == writers[open] && lowest[open] == tid)) copy = open;
-    want = (copy >= 0) + min(r.need, cols) - r.have;
-    over = max(r.need - cols, 0);
+    want = (copy >= 0) + r.need - r.have;
+    over = r.over;
     a.lengths_out[tid] =
         static_cast<int>(min<int64_t>(static_cast<int64_t>(r.held) + r.grow, a.cols << a.shift));
   }
   const int begin = scan<kDemand>(want, &wants);
-  scan<kDemand>(over, &overs);
+  const int overs = sum_long<kDemand>(over);
   // free pages: eight neighbours a thread
   int n = 0, all;
   bool free[kEach];
@@ -358,7 +383,7 @@ __global__ __launch_bounds__(kDemand) void update_small(PageArgs a, Space w) {
   }
   if (tid == 0) {
     *w.given = given;
-    *a.count = max(wants - all, 0) + overs;
+    *a.count = add_held(max(wants - all, 0), overs);
   }
   __syncthreads();
   for (int p = tid; p < pages; p += kDemand) a.refs_out[p] = refs[p];
@@ -448,7 +473,7 @@ __global__ __launch_bounds__(kThreads) void pack_move(PageArgs a, PackSpace w, b
     a.refs_out[w.to[i]] = a.refs[w.from[i]];
   }
   for (int64_t i = blockIdx.x; i < a.rows; i += gridDim.x) {
-    const int have = pages_for(a, held_tokens(a, static_cast<int>(i)));
+    const int have = held_pages(a, static_cast<int>(i));
     for (int64_t c = threadIdx.x; c < a.cols; c += kThreads) {
       int v = c < have ? a.tables[i * a.cols + c] : -1;
       if (v < 0 || v >= a.pages) v = -1;

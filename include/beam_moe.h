@@ -564,7 +564,7 @@ int beam_moe_pages_workspace_bytes(int64_t pages, int64_t rows, size_t* bytes);
  *             int32: outputs that overlap no input; entries of a table behind its
  *             last page are -1; lengths_out = held + grow, at most cols * page_size
  *   missing   device [1] int32: pages that rows wanted and did not get, for want
- *             of free pages (their entries are -1) or of columns
+ *             of free pages (their entries are -1) or of columns (held to 2^31 - 1)
  * References are first counted for the new rows' held pages.  A page that is the
  * unfilled last page of a row that grows is left to that row if nothing else
  * refers to it, and to the lowest of them if only such rows do; every other such

@@ -185,3 +185,28 @@ def test_empty_batch():
     i = torch.zeros(0, 3, dtype=torch.int32, device=dev)
     out, lse = gl.paged_attention(q, k, k, i, i[:, 0].contiguous(), with_lse=True)
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("page", [8, 16])
+def test_nan_stays_where_it_is_read(page, dtype):
+    # in a query: that head alone; in a cached token: the heads that read it
+    c = make([300, 40, 900, 0], 6, 2, 64, page, dtype, 12)
+    dev = device()
+    for what in ("q", "k_cache", "v_cache"):
+        d = {k: v.clone() for k, v in c.items()}
+        if what == "q":
+            d["q"][2, 4, 9] = math.nan
+            hit = [(2, 4)]
+        else:
+            d[what][int(c["tables"][2, 100 // page]), 100 % page, 1, 3] = math.nan
+            hit = [(2, h) for h in (3, 4, 5)]
+        out, lse = call(d, dev)
+        for b, h in hit:
+            assert torch.isnan(out[b, h]).any()
+            out[b, h], lse[b, h] = 0.0, 0.0
+        assert torch.isfinite(out.float()).all()
+        want, wl = call(c, dev)
+        for b, h in hit:
+            out[b, h], lse[b, h] = want[b, h], wl[b, h]
+        check(c, out, lse)

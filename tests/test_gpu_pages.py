@@ -181,3 +181,25 @@ def test_copies():
         k[:, 40], k[:, 41] = k[:, 3], k[:, 9]
     assert all(torch.equal(a, b) for a, b in zip(pools, kept))
     gl.pages_copy(pools, to_dev([], dev), to_dev([], dev))
+
+
+def test_the_largest_batch_of_one_workgroup():
+    rng = random.Random(8)
+    for rows, cols, pages in ((1024, 64, 8192), (1024, 64, 8193), (1025, 63, 8192), (1000, 66, 8000)):
+        tables, lengths, refs = make(rng, rows, cols, 16, pages, shared=0.8)
+        parents = [rng.randint(-1, rows) for _ in range(rows)]
+        check_update(tables, lengths, refs, 16, parents, [rng.choice([0, 1, 40]) for _ in range(rows)], device(), cols)
+
+
+@pytest.mark.parametrize("rows", [3, 1500])
+def test_growth_of_every_size(rows):
+    # tokens past 2^31, more missing pages than an int32 holds
+    most = (1 << 31) - 1
+    tables, lengths, refs = [[4, 2, 7]] * 2, [3, 2], [0, 0, 2, 0, 2, 0, 0, 1] + [0] * 40
+    for grow in (most, most - 2, 1 << 30, 5):
+        want = ref.pages_update(tables, lengths, refs, 1, [i % 3 for i in range(rows)], [grow] * rows)
+        dev = device()
+        got = gl.pages_update(to_dev(tables, dev), to_dev(lengths, dev), to_dev(refs, dev), 1,
+                              to_dev([i % 3 for i in range(rows)], dev), to_dev([grow] * rows, dev))
+        assert [got[k].tolist() for k in ("tables", "lengths", "refs")] == list(want[:3])
+        assert got["missing"].tolist() == [min(want[3], most)]
