@@ -10,7 +10,7 @@
 // for a pool and a batch that one workgroup holds in LDS, one (32 rows of 189 pages,
 // a pool of 1,000: 7 us, where the four launches took 18; 512 rows, a pool of
 // 28,000: 18 us in four, and 24 for copies of 130 MB).  The copies are bound by
-// reading and writing the pages once (2.8 GB in 541 us).
+// reading and writing the pages once (2.8 GB in 505 us).
 #include <algorithm>
 #include <climits>
 
@@ -73,7 +73,10 @@ __device__ __forceinline__ int open_page(const PageArgs& a, const Row& r) {
 }
 
 // ONCE: past the caches' usual order, where many pages move (549 us instead of 563
-// for 2.8 GB; a copied page that is read again soon stays in them).
+// for 2.8 GB; a copied page that is read again soon stays in them).  A workgroup
+// for each page of a layer, so that it reads the whole of an ordinary one before it
+// writes (511 us; 4,096 workgroups that take turns 546, by fours 549).
+constexpr int kBurst = 8;
 template <bool ONCE>
 __device__ __forceinline__ void copy_page(const beam_moe_pools& p, int part, int src, int dst) {
   const int i = part / p.layers, layer = part % p.layers;
@@ -92,12 +95,12 @@ __device__ __forceinline__ void copy_page(const beam_moe_pools& p, int part, int
   };
   int64_t at = static_cast<int64_t>(threadIdx.x) * 16;
   const int64_t step = static_cast<int64_t>(blockDim.x) * 16;
-  for (; at + 3 * step < n; at += 4 * step) {
-    u32x4 v[4];
+  for (; at + (kBurst - 1) * step < n; at += kBurst * step) {
+    u32x4 v[kBurst];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = read(at + u * step);
+    for (int u = 0; u < kBurst; ++u) v[u] = read(at + u * step);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) write(at + u * step, v[u]);
+    for (int u = 0; u < kBurst; ++u) write(at + u * step, v[u]);
   }
   for (; at < n; at += step) write(at, read(at));
 }
@@ -564,7 +567,7 @@ hipError_t launch_pages_compact(const PageArgs& a, const beam_moe_pools& p, void
   hipLaunchKernelGGL(pack_count, dim3(grid), dim3(kThreads), 0, s, a, w);
   hipLaunchKernelGGL(pack_rank, dim3(grid), dim3(kThreads), 0, s, a, w, blocks);
   const int64_t work = std::max<int64_t>({1, a.rows, a.pages * p.count * p.layers});
-  hipLaunchKernelGGL(pack_move, dim3(std::min<int64_t>(work, 4096)), dim3(kThreads), 0, s, a, w, p);
+  hipLaunchKernelGGL(pack_move, dim3(std::min(work, kCopyBlocks)), dim3(kThreads), 0, s, a, w, p);
   return hipGetLastError();
 }
 
