@@ -323,9 +323,6 @@ struct Attend {
     m = kLowest;
     l = 0.0f;
     if (i < stop) {
-      Place now = place(unit + i, i);
-      load_keys(now);
-      load_values(now);
 #pragma unroll
       for (int j = 0; j < T::kK; ++j) {
         const int col = (4 * j + sub) * T::kPart;
@@ -333,6 +330,9 @@ struct Attend {
                    ? ld16(static_cast<const IO*>(a.q) + (head0 + row) * a.D + col)
                    : u32x4{0, 0, 0, 0};
       }
+      Place now = place(unit + i, i);
+      load_keys(now);
+      load_values(now);
       // the next step's keys are read from when this one's are used up, and its
       // values likewise
       float p[4];
@@ -489,12 +489,14 @@ __global__ __launch_bounds__(kSplitWaves* kWave) void attend_split(AttendArgs a,
   while (unit < stop) {
     g.to = static_cast<int>(min<uint32_t>(at.s.units, g.from + (stop - unit)));
     const bool begins = g.from == 0, ends = g.to == at.s.units;
+    // (the next sequence's length on its way)
+    const int length = a.lengths[min(g.seq + 1, seqs - 1)];
     if (begins && !ends)
       left = Open{g.seq, static_cast<int32_t>((unit + at.s.units - 1) / each)};
     at.run(g, begins && ends ? nullptr : part_of(a, blocks, slice, g.block, begins), sh);
     unit += g.to - g.from;
     g.from = 0;
-    if (++g.seq < seqs) at.s = seq_of<A::kUnit>(a.lengths[g.seq], a.window, most);
+    if (++g.seq < seqs) at.s = seq_of<A::kUnit>(length, a.window, most);
   }
   if (threadIdx.x == 0) open[slice] = left;
 }
@@ -587,13 +589,14 @@ hipError_t launch(const AttendArgs& a, hipStream_t s) {
   const int64_t tokens = a.window && a.window < most ? a.window + W * kStep : most;
   const int64_t units = ceil_div(tokens, W * kStep);
   const int slices = static_cast<int>(std::min<int64_t>(slices_of(blocks), a.cache.seqs * units));
-  // Two units or fewer: nothing to split.  A window's (17 units at most): whole
-  // ones fill the card from 512 on; from 128 on with sixteen waves for each (32
-  // sequences of 900 or 500 tokens, 8 heads: 24 and 16 us, in slices 34 and 22;
-  // 8 of 900 20, in slices 17).
+  // Two units or fewer: nothing to split.  Up to 17 (a window of 1,024): whole
+  // sequences fill the card from 512 on, and with sixteen waves for each from 128
+  // on (32 sequences of 900 or 500 tokens, 8 heads: 24 and 16 us, in slices 34 and
+  // 22; 8 of 900 20, in slices 17).  Up to four units sixteen waves take a step
+  // each, in one launch (250 tokens 8.7 us, in slices 11).
   if (slices <= 1 || units <= 2 || (segs >= 512 && units <= 17)) return whole<IO, DK, FAST, W>(a, segs, s);
   if constexpr (FAST && sizeof(IO) == 2 && DK <= 128)
-    if (segs >= 128 && units <= 17) return whole<IO, DK, FAST, 16>(a, segs, s);
+    if ((segs >= 128 && units <= 17) || units <= 4) return whole<IO, DK, FAST, 16>(a, segs, s);
   const dim3 block(W * kWave);
   const int shared = Attend<IO, DK, FAST, W>::shared_bytes(a.Hq / a.Hkv);
   Open* open = reinterpret_cast<Open*>(a.part + static_cast<int64_t>(slices_of(blocks)) * blocks *

@@ -210,3 +210,39 @@ def test_nan_stays_where_it_is_read(page, dtype):
         for b, h in hit:
             out[b, h], lse[b, h] = want[b, h], wl[b, h]
         check(c, out, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,Hkv,cols,window", [
+    (3, 2, 14, 0), (5, 1, 16, 0), (2, 2, 17, 0),            # tables of a few units
+    (70, 2, 68, 0), (70, 2, 150, 512), (130, 1, 17, 100),   # 128 to 511 heads of sequences
+    (300, 2, 60, 0), (300, 2, 90, 300)])                    # more
+@pytest.mark.parametrize("D", [64, 128])
+def test_whole_sequences(B, Hkv, cols, window, D, dtype):
+    lengths = [(i * 97) % (cols * 16 + 1) for i in range(1, B + 1)]
+    c = make(lengths, 3 * Hkv, Hkv, D, 16, dtype, B + cols, cols=cols)
+    check(c, *call(c, device(), window, True), window, True)
+
+
+def test_graph_of_every_form():
+    # captured calls of each way of dividing the work, replayed with other contents
+    dev = device()
+    cs = [make(n, 6, 2, 128, 16, BF16, i) for i, n in enumerate(([30, 9], [250], [900, 3000], [500] * 70, [40] * 300))]
+    want = [[t.clone() for t in call(c, dev)] for c in cs]
+    held = [(c["q"].to(dev), c["k_cache"].to(dev), c["v_cache"].to(dev), c["tables"].to(dev), c["lengths"].to(dev))
+            for c in cs]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = [gl.paged_attention(*h, with_lse=True) for h in held]
+    for _ in range(3):
+        for o, l in got:
+            o.zero_(), l.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for w, o in zip(want, got):
+            assert torch.equal(w[0], o[0]) and torch.equal(w[1], o[1])
+    # a length that changes between replays is the one that counts
+    held[2][4][1] = 17
+    g.replay()
+    torch.cuda.synchronize()
+    check(dict(cs[2], lengths=held[2][4].cpu()), *got[2])
