@@ -12,11 +12,13 @@
 // exp(z - m), which meet by rescaling; under a cap of ordinary size, whose z
 // binary32's exponentials hold as they are, m is 0.  With alternatives the piece,
 // of at most 16,384 logits, is held in registers (the cap keeps the order, so the
-// raw logits are compared): a wave's best is the largest value at the lowest
-// index, one after another, with each lane's largest of eight kept.  A second
-// kernel joins a row's pieces.  Bound by reading the logits; with the cap by two
-// exponentials and a reciprocal an element as much (4,096 x 100,003
-// bf16: 165 us, 5.0 TB/s; the gradient 308 us, 5.3 TB/s).
+// raw logits are compared): the n-th largest of a wave's lanes' largest is a bar
+// that at least n logits reach and few more, those meet in LDS, and each finds its
+// rank by counting (2,048 x 131,072 bf16 with 16: 204 us, 5: 151; one after
+// another by the wave's largest 562 and 240).  A second kernel joins a row's
+// pieces.  Bound by reading the logits; with the cap by two exponentials and a
+// reciprocal an element as much (4,096 x 100,003 bf16: 165 to 195 us as the clock
+// holds, 4.2 to 5.0 TB/s; the gradient 308, 5.3 TB/s).
 #include <algorithm>
 #include <cfloat>
 
@@ -218,29 +220,48 @@ __device__ __forceinline__ bool behind(float v, int i, const Best& last) {
   return v < last.v || (v == last.v && i > last.i);
 }
 
+// The best `top` of c candidates in LDS, one a lane, by counting those before each;
+// lane i gets the i-th.  One wave's.
+__device__ __forceinline__ Best by_rank(Best* list, int c, int top) {
+  const int lane = threadIdx.x % kWave;
+  const Best mine = lane < c ? list[lane] : kNobody;
+  int rank = 0;
+  for (int j = 0; j < c; ++j) {
+    const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine.v), j));
+    const int i = __builtin_amdgcn_readlane(mine.i, j);
+    rank += v > mine.v || (v == mine.v && i < mine.i);
+  }
+  wave_order();
+  if (lane < c && rank < top) list[rank] = mine;
+  wave_order();
+  return lane < min(top, c) ? list[lane] : kNobody;
+}
+
 struct Shared {
   Sums sums[kWaves];
-  Best best[kWaves][kMaxTop];
+  Best best[kWaves * kMaxTop];
+  Best found[kWaves][kWave];  // a wave's candidates
+  int many[kWaves];
 };
 // The waves' sums and best meet in wave 0, whose lanes i < top get the i-th best.
 __device__ __forceinline__ void join(Shared& sh, int top, Sums& sums, Best& kept) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   sums = wave_meet(sums);
   if (lane == 0) sh.sums[wave] = sums;
-  if (lane < top) sh.best[wave][lane] = kept;
+  if (lane < top) sh.best[wave * top + lane] = kept;
   __syncthreads();
   if (wave) return;
 #pragma unroll
   for (int i = 1; i < kWaves; ++i) sums = meet(sums, sh.sums[i]);
   if (top == 0) return;
-  Best mine = kNobody;
-  if (lane % kMaxTop < top) mine = sh.best[lane / kMaxTop][lane % kMaxTop];
-  kept = kNobody;
-  for (int k = 0; k < top; ++k) {
-    const Best b = wave_best(mine);
-    if (lane == k) kept = b;
-    if (mine.i == b.i) mine = kNobody;
-  }
+  // (a wave's nobodies are no candidates)
+  Best mine = lane < kWaves * top ? sh.best[lane] : kNobody;
+  const uint64_t some = __ballot(mine.i != kNoIndex);
+  const int at = __popcll(some & ((uint64_t{1} << lane) - 1));
+  wave_order();
+  if (mine.i != kNoIndex) sh.best[at] = mine;
+  wave_order();
+  kept = by_rank(sh.best, __popcll(some), top);
 }
 static_assert(kWaves * kMaxTop == kWave, "one lane for each wave's candidate");
 
@@ -409,41 +430,64 @@ __global__ __launch_bounds__(kThreads) void score_top(ScoreArgs a, Cap c, int pi
   const Ref ref = ref_of<F>(c, all);
   float s = 0.0f, w = 0.0f;
 #pragma unroll
-  for (int k = 0; k < STEPS; ++k)
+  for (int k = 0; k < STEPS; ++k) {
+    e[k].repack();
 #pragma unroll
     for (int j = 0; j < 8; ++j) add<F>(c, e[k].get(j), ref, s, w);
-  Best kept = kNobody, last = {INFINITY, -1};
-  for (int x = 0; x < a.top; ++x) {
-    Best b;
-    b.v = wave_max(all);
-    int at = kNoIndex;  // the lane's lowest index of that value, not taken yet
-    if (all == b.v) {
+    e[k].repack();
+  }
+  // The top-th largest of the lanes' largest: at least `top` logits reach it, and
+  // seldom many more.  Those meet in LDS.
+  const int wave = threadIdx.x / kWave;
+  const float highest = wave_max(all);
+  float bar = highest, rest = all;
+  for (int x = 0, reach = 0; x < a.top && reach < a.top; ++x) {
+    if (x) bar = wave_max(rest);
+    reach += __popcll(__ballot(rest == bar));
+    if (rest == bar) rest = -INFINITY;
+  }
+  int found = kWave + 1;
+  if (first + wave * kWave * 8 >= end) {
+    found = 0;  // no logit is the wave's
+  } else if (bar > -INFINITY) {
+    if (lane == 0) sh.many[wave] = 0;
+    wave_order();
 #pragma unroll
-      for (int k = STEPS - 1; k >= 0; --k)
-        if (most[k] == b.v)
+    for (int k = 0; k < STEPS; ++k)
+      if (most[k] >= bar)
 #pragma unroll
-          for (int j = 7; j >= 0; --j) {
-            const int i = base + k * kChunk + j;
-            if (e[k].get(j) == b.v && i < end && behind(b.v, i, last)) at = i;
-          }
-    }
-    b.i = wave_min(at);
-    if (lane == x) kept = b;
-    last = b;
-    if (at == b.i && at != kNoIndex) {  // the lane that held it
-      all = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < STEPS; ++k) {
-        if (most[k] == b.v) {
-          most[k] = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float v = e[k].get(j);
-            if (behind(v, base + k * kChunk + j, b)) most[k] = fmaxf(most[k], v);
+        for (int j = 0; j < 8; ++j) {
+          const float v = e[k].get(j);
+          if (v >= bar) {
+            const int at = atomicAdd(&sh.many[wave], 1);
+            if (at < kWave) sh.found[wave][at] = Best{v, base + k * kChunk + j};
           }
         }
-        all = fmaxf(all, most[k]);
+    wave_order();
+    found = __builtin_amdgcn_readfirstlane(sh.many[wave]);
+  }
+  Best kept = kNobody;
+  if (found <= kWave) {
+    kept = by_rank(sh.found[wave], found, a.top);
+  } else if (highest == -INFINITY) {
+    // all masked: the first ones
+    const int i = first + wave * kWave * 8 + lane;
+    if (lane < a.top && i < end) kept = Best{-INFINITY, i};
+  } else {
+    // logits alike in their hundreds, or masked ones among the best: one after
+    // another, each lane's next by reading its logits again
+    Best last = {INFINITY, -1};
+    for (int x = 0; x < a.top; ++x) {
+      Best mine = kNobody;
+      for (int k = 0; k < STEPS; ++k) {
+        const int i0 = base + k * kChunk;
+        for (int i = i0; i < min(i0 + 8, end); ++i) {
+          const float v = value(row[i]);
+          if (behind(v, i, last) && (v > mine.v || mine.i == kNoIndex)) mine = Best{v, i};
+        }
       }
+      last = wave_best(mine);
+      if (lane == x) kept = last;
     }
   }
   Sums u = sums_of<F>(c, ref, s, w);

@@ -146,6 +146,12 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = u32x4{0, 0, 0, 0};
   }
+  // Makes the compiler forget values it has unpacked (it would rather keep them,
+  // in twice the registers, than unpack again).
+  __device__ __forceinline__ void repack() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[i]));
+  }
   __device__ __forceinline__ float get(int j) const {
     if constexpr (sizeof(IO) == 2)
       return __uint_as_float(j % 2 ? w[0][j / 2] & 0xFFFF0000u : w[0][j / 2] << 16);
