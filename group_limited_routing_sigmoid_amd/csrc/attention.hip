@@ -1,8 +1,8 @@
 // Attention of one new token of every sequence over its cached tokens:
 //   out_h = softmax(scale q_h K^T) V [* sigmoid(gate_h)]
 // for the query heads of a key-value head together, over the last `window`
-// tokens or all ("Reflection Beam", section "Hybrid Attention and Unusual
-// Residuals").
+// tokens or all ("Reflection Releases Beam ...", section "Hybrid Attention and
+// Unusual Residuals").
 //
 // Bound by reading the keys and values once.  The query heads of one key-value
 // head (up to 16; more go in blocks of 16) are the 16 columns of the matrix

@@ -4,8 +4,8 @@
 //   (n_a, n_b) turned by pos * f_i        pairs (i, i + rot/2) or (2i, 2i+1)
 //   q times (1 + (pos + 1) / L)^e
 // (RMSNorm on queries and keys, rotation in the sliding-window layers and the
-// query's temperature in the global ones: "Reflection Beam", section "Hybrid
-// Attention and Unusual Residuals".)
+// query's temperature in the global ones: "Reflection Releases Beam ...",
+// section "Hybrid Attention and Unusual Residuals".)
 //
 // A head is held by a group of lanes, 8 values a lane, so every input is read
 // and every output written once: both directions are bound by those bytes.  A

@@ -3,8 +3,8 @@
 //   z = scale cap tanh(l / cap)      (no cap: scale l)
 //   logp = z - ln S,  S = sum exp(z),  entropy = ln S - sum z exp(z) / S
 //   dl_j = z'(l_j) (g ([j = target] - p_j) - h p_j (logp_j + entropy))
-// (logits capped by tanh at 30: "Reflection Beam", section "Hybrid Attention
-// and Unusual Residuals".)
+// (logits capped by tanh at 30: "Reflection Releases Beam ...", section "Hybrid
+// Attention and Unusual Residuals".)
 //
 // A row is cut into pieces, more of them for few rows, so that they fill the
 // card.  Without alternatives a workgroup runs through its piece with the sums

@@ -436,8 +436,8 @@ int beam_moe_norm_residual_backward(int64_t T, int64_t H, int32_t dtype, const v
 
 /* Norms of query and key heads and their rotation by position, in one pass,
  * and the keys' and values' way into a paged cache ("Hugging Face releases
- * Beam ..."; "Reflection Beam", section "Hybrid Attention and Unusual
- * Residuals": RMSNorm on queries and keys, rotation in the sliding-window
+ * Beam ..."; "Reflection Releases Beam ...", section "Hybrid Attention and
+ * Unusual Residuals": RMSNorm on queries and keys, rotation in the sliding-window
  * layers, none in the global ones, whose queries are scaled by
  * (1 + (pos + 1) / 2048)^0.1).  Per head x of D values of token t:
  *   n = x / sqrt(mean(x^2) + eps) * weight
@@ -501,8 +501,8 @@ int beam_moe_paged_attention_workspace_bytes(int64_t seqs, int32_t Hq, int32_t H
  * one's own key and value among them (beam_moe_qk_norm_rope has put them there):
  *   out = softmax(scale q k^T) v [* sigmoid(gate)]
  * over the last `window` of lengths[s] tokens (window 0: all), query head h
- * reading key-value head h / (Hq / Hkv) ("Reflection Beam", section "Hybrid
- * Attention and Unusual Residuals": a window of 512 or the whole context, 48
+ * reading key-value head h / (Hq / Hkv) ("Reflection Releases Beam ...", section
+ * "Hybrid Attention and Unusual Residuals": a window of 512 or the whole context, 48
  * query and 8 key-value heads, a sigmoid gate for each head's channels).
  *   q        device [seqs, Hq, D] dtype, contiguous
  *   gate     device [seqs, Hq, D] dtype, contiguous, before the sigmoid, or NULL
@@ -606,8 +606,8 @@ int beam_moe_token_logprobs_workspace_bytes(int64_t T, int64_t V, int32_t top, s
  * its best alternatives, in one reading of the logits, per row t:
  *   z = scale * softcap * tanh(l / softcap)   (softcap 0: z = scale * l)
  *   logp = z - ln sum exp(z)
- * ("Reflection Beam", section "Hybrid Attention and Unusual Residuals": logits
- * capped by tanh at 30).
+ * ("Reflection Releases Beam ...", section "Hybrid Attention and Unusual
+ * Residuals": logits capped by tanh at 30).
  *   logits    device [T, V] dtype, rows row_stride >= V elements apart
  *   targets   device [T] int64, or NULL; one outside [0, V) gives logprob 0
  *   logprobs  device [T] fp32, with targets: logp of the target
