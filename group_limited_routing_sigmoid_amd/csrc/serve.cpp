@@ -257,8 +257,11 @@ int beam_moe_paged_attention(int64_t seqs, int32_t Hq, int32_t Hkv, int32_t D, i
                   token_stride, head_stride, pages, page_size, tables, seqs, table_cols, dtype,
                   &a.cache);
   if (st != BEAM_OK) return st;
-  // units of work are counted in 32 bits
-  if (seqs * (table_cols * page_size) >= (int64_t{1} << 36)) return BEAM_ERR_UNSUPPORTED;
+  // tokens are counted in 31 bits up to 64 steps of 256 past a sequence's end, units
+  // of work in 32
+  if (table_cols * page_size > 0x7FFF0000 ||
+      seqs * (table_cols * page_size) >= (int64_t{1} << 36))
+    return BEAM_ERR_UNSUPPORTED;
   if (seqs == 0) return BEAM_OK;
   if (!q || !k_cache || !v_cache || !lengths || !out || (!tables && table_cols > 0))
     return BEAM_ERR_INVALID_ARG;

@@ -514,8 +514,8 @@ int beam_moe_paged_attention_workspace_bytes(int64_t seqs, int32_t Hq, int32_t H
  * and an lse of -infinity.  What pages hold behind a sequence's length or before
  * its window is not read.  Sums and softmax statistics are binary32, and so are
  * the products with the values; one rounding to dtype.
- * scale > 0 and finite, Hq % Hkv == 0, seqs * Hq < 2^24, table_cols * page_size <
- * 2^31, seqs times that < 2^36.  Identical inputs give bitwise identical outputs. */
+ * scale > 0 and finite, Hq % Hkv == 0, seqs * Hq < 2^24, table_cols * page_size <=
+ * 2^31 - 2^16, seqs times that < 2^36.  Identical inputs give bitwise identical outputs. */
 int beam_moe_paged_attention(int64_t seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
                              const void* q, const void* gate, const void* k_cache,
                              const void* v_cache, int64_t page_stride, int64_t token_stride,
