@@ -72,8 +72,11 @@ int check_workspace(const void* ws, size_t have, size_t need) {
   return reinterpret_cast<uintptr_t>(ws) % 256 ? BEAM_ERR_INVALID_ARG : BEAM_OK;
 }
 
+constexpr int32_t kMaxLayers = 65536;  // arrays times layers are counted in 32 bits
+
 int check_pools(const beam_moe_pools* p) {
   if (!p || p->count < 0 || p->count > 8 || p->layers < 0) return BEAM_ERR_INVALID_ARG;
+  if (p->layers > kMaxLayers) return BEAM_ERR_UNSUPPORTED;
   for (int i = 0; i < p->count; ++i) {
     if (p->layers && (!p->base[i] || !aligned16(p->base[i]))) return BEAM_ERR_INVALID_ARG;
     if (p->bytes[i] < 0 || p->bytes[i] % 16 || p->layer_stride[i] % 16 || p->page_stride[i] % 16)

@@ -526,7 +526,7 @@ int beam_moe_paged_attention(int64_t seqs, int32_t Hq, int32_t Hkv, int32_t D, i
 
 /* The arrays whose pages beam_moe_pages_* copy, up to 8 of them: page p of layer
  * l of array i is `bytes[i]` bytes at base[i] + l * layer_stride[i] + p *
- * page_stride[i] (bytes, multiples of 16). */
+ * page_stride[i] (bytes, multiples of 16), layers <= 65536. */
 typedef struct {
   int32_t count;
   int32_t layers;

@@ -14,3 +14,8 @@ def test_attention_holds_the_last_tokens_in_32_bits(size):
     most = ((1 << 31) - (1 << 16)) // size
     assert _attend(size=size, cols=most, **EMPTY) == gl.OK
     assert _attend(size=size, cols=most + 1, **EMPTY) == UNSUPPORTED
+
+
+def test_pools_have_few_layers():
+    # arrays times layers are counted in 32 bits
+    assert _update(pool=_pool(count=8, layers=(1 << 16) + 1)) == UNSUPPORTED
