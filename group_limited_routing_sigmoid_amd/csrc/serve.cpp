@@ -85,6 +85,7 @@ int check_pools(const beam_moe_pools* p) {
   return BEAM_OK;
 }
 
+constexpr float kLog2E = 1.4426950408889634f;
 constexpr int64_t kMaxPages = int64_t{1} << 24, kMaxRows = 65536;
 
 int check_tables(int64_t old_rows, int64_t rows, int64_t cols, int64_t pages, int64_t page_size) {
@@ -100,6 +101,10 @@ int check_score(int64_t T, int64_t V, int32_t dtype, int64_t stride, float softc
   if (T < 0 || V < 1 || !is_dtype(dtype) || (T > 1 && stride < V)) return BEAM_ERR_INVALID_ARG;
   if (!(softcap >= 0.0f) || !isfinite(softcap) || !(scale > 0.0f) || !isfinite(scale))
     return BEAM_ERR_INVALID_ARG;
+  // what the kernels multiply with, in base 2
+  if (!isfinite(kLog2E * scale) ||
+      (softcap > 0.0f && (!isfinite(2.0f * kLog2E * scale * softcap) || !isfinite(2.0f * kLog2E / softcap))))
+    return BEAM_ERR_UNSUPPORTED;
   // 256 threads a piece, fewer than 2^32 in all
   if (V > (1 << 24) || T >= (1 << 23) || score_pieces_count(T, V) >= (1 << 24))
     return BEAM_ERR_UNSUPPORTED;
@@ -263,7 +268,7 @@ int beam_moe_paged_attention(int64_t seqs, int32_t Hq, int32_t Hkv, int32_t D, i
   // tokens are counted in 31 bits up to 64 steps of 256 past a sequence's end, units
   // of work in 32
   if (table_cols * page_size > 0x7FFF0000 ||
-      seqs * (table_cols * page_size) >= (int64_t{1} << 36))
+      seqs * (table_cols * page_size) >= (int64_t{1} << 36) || !isfinite(kLog2E * scale))
     return BEAM_ERR_UNSUPPORTED;
   if (seqs == 0) return BEAM_OK;
   if (!q || !k_cache || !v_cache || !lengths || !out || (!tables && table_cols > 0))

@@ -514,7 +514,7 @@ int beam_moe_paged_attention_workspace_bytes(int64_t seqs, int32_t Hq, int32_t H
  * and an lse of -infinity.  What pages hold behind a sequence's length or before
  * its window is not read.  Sums and softmax statistics are binary32, and so are
  * the products with the values; one rounding to dtype.
- * scale > 0 and finite, Hq % Hkv == 0, seqs * Hq < 2^24, table_cols * page_size <=
+ * 0 < scale <= 2^127, Hq % Hkv == 0, seqs * Hq < 2^24, table_cols * page_size <=
  * 2^31 - 2^16, seqs times that < 2^36.  Identical inputs give bitwise identical outputs. */
 int beam_moe_paged_attention(int64_t seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
                              const void* q, const void* gate, const void* k_cache,
@@ -620,7 +620,10 @@ int beam_moe_token_logprobs_workspace_bytes(int64_t T, int64_t V, int32_t top, s
  * -infinity and entropy 0.  A mask of the type's lowest value is a logit like any
  * other (a row of only those is uniform).  A NaN or +infinity makes its row's
  * results NaN.
- * 0 <= top <= min(16, V); softcap >= 0, scale > 0, finite; V <= 2^24, T < 2^23. */
+ * A capped z is off by at most 16 scale softcap 2^-24, so a cap is meant to be near
+ * the logits' size.
+ * 0 <= top <= min(16, V); softcap >= 0, scale > 0; 3 scale, 3 scale softcap and 3 /
+ * softcap in binary32's range; V <= 2^24, T < 2^23. */
 int beam_moe_token_logprobs(int64_t T, int64_t V, int32_t dtype, const void* logits,
                             int64_t row_stride, const int64_t* targets, float softcap, float scale,
                             int32_t top, float* logprobs, float* entropy, float* lse,
