@@ -29,7 +29,7 @@
 // first unit from the lengths, and leaves sums for the sequences that it did not
 // see whole, which a second kernel joins.
 // 1,000,003 tokens of 8 heads of 128: 690 us, 5.9 TB/s (6.35 is what reading alone
-// reaches); 64 sequences of 100 to 32,000: 257 us, 5.7; 256 windows of 512: 100.
+// reaches); 64 sequences of 100 to 32,000: 257 us, 5.7; 256 windows of 512: 97.
 #include <algorithm>
 
 #include "serve.h"
@@ -398,9 +398,13 @@ struct Attend {
   }
 };
 
-// A workgroup for each block of heads of each sequence.
+// A workgroup for each block of heads of each sequence.  Bound to 128 registers, so
+// that 1,024 workgroups share the card (256 windows of 512: 99 us, with three a
+// compute unit 102; two sequences a workgroup, the second one's first loads before
+// the first one's join, 103).
 template <typename IO, int DK, bool FAST, int W>
-__global__ __launch_bounds__(W* kWave) void attend_whole(AttendArgs a) {
+__global__ __launch_bounds__(W* kWave, W == 4 && DK <= 128 && FAST && sizeof(IO) == 2 ? 4 : 1)
+void attend_whole(AttendArgs a) {
   using A = Attend<IO, DK, FAST, W>;
   extern __shared__ float sh[];
   A at(a);
