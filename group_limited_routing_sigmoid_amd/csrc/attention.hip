@@ -446,10 +446,9 @@ __device__ __forceinline__ float* part_of(const AttendArgs& a, int blocks, int s
   return a.part + ((static_cast<int64_t>(slice) * blocks + block) * 2 + which) * part_size(a.D);
 }
 
-// The units of all sequences in slices of one size, at least `least` units.
+// The units of all sequences in slices of one size.
 template <typename IO, int DK, bool FAST>
-__global__ __launch_bounds__(kSplitWaves* kWave) void attend_split(AttendArgs a, Open* open, int slices,
-                                                               uint32_t least) {
+__global__ __launch_bounds__(kSplitWaves* kWave) void attend_split(AttendArgs a, Open* open, int slices) {
   using A = Attend<IO, DK, FAST, kSplitWaves>;
   extern __shared__ float sh[];
   A at(a);
@@ -463,7 +462,7 @@ __global__ __launch_bounds__(kSplitWaves* kWave) void attend_split(AttendArgs a,
   uint32_t total = 0;
   for (int b = lane; b < seqs; b += kWave) total += units(b);
   total = __builtin_amdgcn_readlane(wave_scan(total), kWave - 1);
-  const uint32_t each = max((total + slices - 1) / slices, least);
+  const uint32_t each = (total + slices - 1) / slices;  // a sequence has at least one
   uint32_t unit = each * slice;
   const uint32_t stop = min(unit + each, total);
   if (unit >= total) {
@@ -596,17 +595,19 @@ hipError_t launch(const AttendArgs& a, hipStream_t s) {
   // Two units or fewer: nothing to split.  Up to 17 (a window of 1,024): whole
   // sequences fill the card from 512 on, and with sixteen waves for each from 128
   // on (32 sequences of 900 or 500 tokens, 8 heads: 24 and 16 us, in slices 34 and
-  // 22; 8 of 900 20, in slices 17).  Up to four units sixteen waves take a step
-  // each, in one launch (250 tokens 8.7 us, in slices 11).
+  // 22; 8 of 900 20, in slices 17).  Up to six units sixteen waves take a step or two
+  // each, in one launch (250 tokens 8.7 us, 300 9.4, in slices 11; 500 tokens 11.6 and
+  // in slices 10).  A slice may be one unit, a step for each wave (2,000 tokens 11.4
+  // us, with two at least 12.7).
   if (slices <= 1 || units <= 2 || (segs >= 512 && units <= 17)) return whole<IO, DK, FAST, W>(a, segs, s);
   if constexpr (FAST && sizeof(IO) == 2 && DK <= 128)
-    if ((segs >= 128 && units <= 17) || units <= 4) return whole<IO, DK, FAST, 16>(a, segs, s);
+    if ((segs >= 128 && units <= 17) || units <= 6) return whole<IO, DK, FAST, 16>(a, segs, s);
   const dim3 block(W * kWave);
   const int shared = Attend<IO, DK, FAST, W>::shared_bytes(a.Hq / a.Hkv);
   Open* open = reinterpret_cast<Open*>(a.part + static_cast<int64_t>(slices_of(blocks)) * blocks *
                                                     2 * part_size(a.D));
   hipLaunchKernelGGL((attend_split<IO, DK, FAST>), dim3(slices * blocks), block, shared, s, a, open,
-                     slices, 2);
+                     slices);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((attend_join<IO>), dim3(slices * a.Hq), dim3(256), 0, s, a, open);
