@@ -121,6 +121,7 @@ __device__ __forceinline__ float value(IO v) {
 struct Cap {
   float a, b;  // no cap: z = b l;  cap: z = a - 2 a r, r of exp2(b l)
   float scale;
+  float unit;  // of Sums::m in base 2
   bool on;
 };
 __host__ __device__ __forceinline__ Cap make_cap(float softcap, float scale) {
@@ -129,6 +130,7 @@ __host__ __device__ __forceinline__ Cap make_cap(float softcap, float scale) {
   c.scale = scale;
   c.a = scale * softcap * kLog2E;
   c.b = c.on ? 2.0f * kLog2E / softcap : scale * kLog2E;
+  c.unit = c.on ? 1.0f : c.b;
   return c;
 }
 // How z is made: without a cap, with one, and with one small enough that 2^z and
@@ -140,25 +142,30 @@ Form form_of(const Cap& c) { return !c.on ? kPlain : c.a <= kSmallCap ? kSmall :
 __device__ __forceinline__ float cap_r(const Cap& c, float l) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(c.b * l));
 }
-// In nats, where the lowest logits still have a z.
-__device__ __forceinline__ float z_of(const Cap& c, float l) {
+// z - m in nats, of a logit and what sums are relative to.  Without a cap the
+// difference of the logits comes first: it has a scaled value where the lowest
+// logit itself has none.
+__device__ __forceinline__ float z_from(const Cap& c, float l, float m) {
   if (l == -INFINITY) return l;  // masked
-  return c.on ? (c.a - 2.0f * c.a * cap_r(c, l)) * kLn2 : c.scale * l;
+  return c.on ? (c.a - 2.0f * c.a * cap_r(c, l) - m) * kLn2 : c.scale * (l - m);
 }
 // Times a logit: at most 5e-7 of a finite one, an infinite one all the same.
 constexpr float kTrace = 0x1p-149f;
 
-// Sums relative to m (in nats): with d = (z - m) / ln 2, s of 2^d, w of d 2^d.
+// Sums relative to m, a logit without a cap, else a z in base 2: with d = z - z(m)
+// in base 2, s of 2^d, w of d 2^d.
 struct Sums {
   float m, s, w;
 };
 // In base 2, and finite, so that it times 0 is 0.
-__device__ __forceinline__ float apart(float m, float to) { return fmaxf((m - to) * kLog2E, -1e30f); }
-__device__ __forceinline__ Sums meet(const Sums& x, const Sums& y) {
+__device__ __forceinline__ float apart(const Cap& c, float m, float to) {
+  return fmaxf((m - to) * c.unit, -1e30f);
+}
+__device__ __forceinline__ Sums meet(const Cap& c, const Sums& x, const Sums& y) {
   Sums o;
   o.m = fmaxf(x.m, y.m);
   // (a side without logits has s and w 0 and any m)
-  const float dx = apart(x.m, o.m), dy = apart(y.m, o.m);
+  const float dx = apart(c, x.m, o.m), dy = apart(c, y.m, o.m);
   const float fx = __builtin_amdgcn_exp2f(dx), fy = __builtin_amdgcn_exp2f(dy);
   o.s = x.s * fx + y.s * fy;
   o.w = (x.w + dx * x.s) * fx + (y.w + dy * y.s) * fy;
@@ -192,10 +199,10 @@ __device__ __forceinline__ float wave_sum(float v) {
 __device__ __forceinline__ int wave_min(int v) {
   return static_cast<int>(-wave_max(-static_cast<float>(v)));
 }
-__device__ __forceinline__ Sums wave_meet(const Sums& v) {
+__device__ __forceinline__ Sums wave_meet(const Cap& c, const Sums& v) {
   Sums o;
   o.m = wave_max(v.m);
-  const float d = apart(v.m, o.m), f = __builtin_amdgcn_exp2f(d);
+  const float d = apart(c, v.m, o.m), f = __builtin_amdgcn_exp2f(d);
   o.s = wave_sum(v.s * f);
   o.w = wave_sum((v.w + d * v.s) * f);
   return o;
@@ -244,15 +251,15 @@ struct Shared {
   int many[kWaves];
 };
 // The waves' sums and best meet in wave 0, whose lanes i < top get the i-th best.
-__device__ __forceinline__ void join(Shared& sh, int top, Sums& sums, Best& kept) {
+__device__ __forceinline__ void join(Shared& sh, const Cap& c, int top, Sums& sums, Best& kept) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  sums = wave_meet(sums);
+  sums = wave_meet(c, sums);
   if (lane == 0) sh.sums[wave] = sums;
   if (lane < top) sh.best[wave * top + lane] = kept;
   __syncthreads();
   if (wave) return;
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) sums = meet(sums, sh.sums[i]);
+  for (int i = 1; i < kWaves; ++i) sums = meet(c, sums, sh.sums[i]);
   if (top == 0) return;
   // (a wave's nobodies are no candidates)
   Best mine = lane < kWaves * top ? sh.best[lane] : kNobody;
@@ -288,11 +295,12 @@ __device__ __forceinline__ void finish(const ScoreArgs& a, const Cap& c, int64_t
   const bool bad = !(u.s <= FLT_MAX);  // a NaN or +infinity among them
   const float log2s = bad ? NAN : __log2f(u.s), lns = log2s * kLn2;
   auto logp = [&](float l) {
-    const float z = z_of(c, l);
-    return z == -INFINITY && !bad ? z : (z - u.m) - lns;
+    const float d = z_from(c, l, u.m);
+    return d == -INFINITY && !bad ? d : d - lns;
   };
   if (lane == 0) {
-    a.lse[t] = none ? -INFINITY : u.m + lns;
+    const float most = c.on ? u.m * kLn2 : fminf(fmaxf(c.scale * u.m, -FLT_MAX), FLT_MAX);
+    a.lse[t] = none ? -INFINITY : most + lns;
     a.entropy[t] = none ? 0.0f : (log2s - u.w / u.s) * kLn2;
     if (a.logprobs) a.logprobs[t] = g.counts ? logp(g.l) : 0.0f;
   }
@@ -337,8 +345,8 @@ __device__ __forceinline__ void add(const Cap& c, float l, const Ref& ref, float
 }
 template <Form F>
 __device__ __forceinline__ Sums sums_of(const Cap& c, const Ref& ref, float s, float w) {
-  if constexpr (F == kPlain) return Sums{fmaxf(c.scale * ref.l, -FLT_MAX), s, w};
-  else if constexpr (F == kCapped) return Sums{ref.z * kLn2, s, w};
+  if constexpr (F == kPlain) return Sums{ref.l, s, w};
+  else if constexpr (F == kCapped) return Sums{ref.z, s, w};
   else return Sums{0.0f, s, c.a * s - 2.0f * c.a * w};
 }
 
@@ -400,7 +408,7 @@ __global__ __launch_bounds__(kThreads) void score_sums(ScoreArgs a, Cap c, int p
   while (i < end) step();
   Sums u = sums_of<F>(c, ref, s, w);
   Best kept = kNobody;
-  join(sh, 0, u, kept);
+  join(sh, c, 0, u, kept);
   if (threadIdx.x >= kWave) return;
   if (pieces == 1) finish<IO>(a, c, t, u, kept, target_of<IO>(a, t));
   else if (threadIdx.x == 0) put_sums(part, blockIdx.x, u);
@@ -491,7 +499,7 @@ __global__ __launch_bounds__(kThreads) void score_top(ScoreArgs a, Cap c, int pi
     }
   }
   Sums u = sums_of<F>(c, ref, s, w);
-  join(sh, a.top, u, kept);
+  join(sh, c, a.top, u, kept);
   if (threadIdx.x >= kWave) return;
   if (pieces == 1) {
     finish<IO>(a, c, t, u, kept, target_of<IO>(a, t));
@@ -517,7 +525,7 @@ __global__ __launch_bounds__(kThreads) void score_join(ScoreArgs a, Cap c, int p
   Sums u = {-FLT_MAX, 0.0f, 0.0f};
   for (int i = threadIdx.x; i < pieces; i += kThreads) {
     const f32x4 p = *reinterpret_cast<const f32x4*>(part + 4 * (t * pieces + i));
-    u = meet(u, Sums{p[0], p[1], p[2]});
+    u = meet(c, u, Sums{p[0], p[1], p[2]});
   }
   const Target g = target_of<IO>(a, t);
   Best kept = kNobody;
@@ -550,7 +558,7 @@ __global__ __launch_bounds__(kThreads) void score_join(ScoreArgs a, Cap c, int p
     }
   }
   // with pieces in one wave alone, its best are the row's
-  join(sh, pieces > kWave ? a.top : 0, u, kept);
+  join(sh, c, pieces > kWave ? a.top : 0, u, kept);
   if (threadIdx.x < kWave) finish<IO>(a, c, t, u, kept, g);
 }
 

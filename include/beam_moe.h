@@ -612,14 +612,14 @@ int beam_moe_token_logprobs_workspace_bytes(int64_t T, int64_t V, int32_t top, s
  *   targets   device [T] int64, or NULL; one outside [0, V) gives logprob 0
  *   logprobs  device [T] fp32, with targets: logp of the target
  *   entropy   device [T] fp32: -sum p logp
- *   lse       device [T] fp32: ln sum exp(z)
+ *   lse       device [T] fp32: ln sum exp(z), held to binary32's range
  *   top_ids, top_logprobs  device [T, top] int32 and fp32, top > 0: the tokens of
  *             the highest logits in order, equal ones by their index
  * A logit of -infinity is masked: it has probability 0, logp -infinity and
  * gradient 0, also under the cap.  A row of only those has lse and logp
  * -infinity and entropy 0.  A mask of the type's lowest value is a logit like any
- * other (a row of only those is uniform).  A NaN or +infinity makes its row's
- * results NaN.
+ * other (a row of only those is uniform, at any scale); a logp past binary32's
+ * range is -infinity.  A NaN or +infinity makes its row's results NaN.
  * A capped z is off by at most 16 scale softcap 2^-24, so a cap is meant to be near
  * the logits' size.
  * 0 <= top <= min(16, V); softcap >= 0, scale > 0; 3 scale, 3 scale softcap and 3 /
