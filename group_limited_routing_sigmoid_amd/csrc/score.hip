@@ -119,9 +119,10 @@ __device__ __forceinline__ float value(IO v) {
 // z in base 2, and with the cap r = 1 / (1 + e^(2 l / cap)): z = a (1 - 2 r),
 // dz/dl = 4 r (1 - r) scale.
 struct Cap {
-  float a, b;  // no cap: z = b l;  cap: z = a - 2 a r, r of exp2(b l)
+  float a, b;  // no cap: z = b l;  cap: r of exp2(b l)
   float scale;
   float unit;  // of Sums::m in base 2
+  float near;  // logits below it have a series (tanh_series)
   bool on;
 };
 __host__ __device__ __forceinline__ Cap make_cap(float softcap, float scale) {
@@ -131,23 +132,62 @@ __host__ __device__ __forceinline__ Cap make_cap(float softcap, float scale) {
   c.a = scale * softcap * kLog2E;
   c.b = c.on ? 2.0f * kLog2E / softcap : scale * kLog2E;
   c.unit = c.on ? 1.0f : c.b;
+  c.near = 1.0f / c.b;
   return c;
 }
 // How z is made: without a cap, with one, and with one small enough that 2^z and
-// its sums need no maximum.
+// its sums need no maximum (a z of 2^24 logits, 96 2^96 2^24 at most) and that 1 - 2 r
+// has bits enough.
 enum Form { kPlain, kCapped, kSmall };
-constexpr float kSmallCap = 50.0f;
+constexpr float kSmallCap = 96.0f;
 Form form_of(const Cap& c) { return !c.on ? kPlain : c.a <= kSmallCap ? kSmall : kCapped; }
 
-__device__ __forceinline__ float cap_r(const Cap& c, float l) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(c.b * l));
+__device__ __forceinline__ float r_of(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x));
+}
+// tanh(u) by its series to u^11 where |u| <= 0.35 (2^-26 of itself is left out), u = x
+// ln 2 / 2 of an exponent |x| < 1 in base 2.
+__device__ __forceinline__ float tanh_series(float x) {
+  const float u = x * (0.5f * kLn2), q = u * u;
+  float p = __builtin_fmaf(q, -1382.0f / 155925.0f, 62.0f / 2835.0f);
+  p = __builtin_fmaf(q, p, -17.0f / 315.0f);
+  p = __builtin_fmaf(q, p, 2.0f / 15.0f);
+  p = __builtin_fmaf(q, p, -1.0f / 3.0f);
+  return __builtin_fmaf(q * u, p, u);
+}
+// A capped z in base 2.  1 - 2 r cancels where r is near a half, which leaves 16 2^-24
+// of the cap: under a small one less than the sums' own errors.  Past it logits below
+// 0.35 caps take the series, the others r of |l|: 20 2^-24 of z itself.  Where a wave
+// has only the former, as under a cap far above its logits, the latter is not
+// worked out (NEAR).  4,096 x 100,003 bf16 of deviation 4: caps of 30 and 50 178 and
+// 161 us, of 80 and 1,000 238 and 233 (a small one's way 196), a z of 2.5 times a cap
+// of 30, in whose every wave some need r, 361; gradients 311, 310, 325, 329 and 435.
+template <Form F, bool NEAR = false>
+__device__ __forceinline__ float capped(const Cap& c, float l) {
+  const float x = c.b * l;
+  if constexpr (F == kSmall) return c.a - 2.0f * c.a * r_of(x);
+  const float near = c.a * tanh_series(x);
+  if constexpr (NEAR) return near;
+  const float far = __builtin_copysignf(c.a - 2.0f * c.a * r_of(fabsf(x)), x);
+  return fabsf(l) < c.near ? near : far;
+}
+// Whether none of the wave's logits needs more than the series (masked ones, infinite
+// ones and NaNs need no z).
+template <typename IO>
+__device__ __forceinline__ bool all_near(const Cap& c, const Eight<IO>& e) {
+  const uint32_t from = __float_as_uint(c.near);
+  uint32_t least = 0xFFFFFFFFu;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) least = min(least, (__float_as_uint(e.get(j)) & 0x7FFFFFFFu) - from);
+  return !__any(least < 0x7F800000u - from);
 }
 // z - m in nats, of a logit and what sums are relative to.  Without a cap the
 // difference of the logits comes first: it has a scaled value where the lowest
 // logit itself has none.
 __device__ __forceinline__ float z_from(const Cap& c, float l, float m) {
   if (l == -INFINITY) return l;  // masked
-  return c.on ? (c.a - 2.0f * c.a * cap_r(c, l) - m) * kLn2 : c.scale * (l - m);
+  if (!c.on) return c.scale * (l - m);
+  return ((c.a <= kSmallCap ? capped<kSmall>(c, l) : capped<kCapped>(c, l)) - m) * kLn2;
 }
 // Times a logit: at most 5e-7 of a finite one, an infinite one all the same.
 constexpr float kTrace = 0x1p-149f;
@@ -321,10 +361,10 @@ struct Ref {
 template <Form F>
 __device__ __forceinline__ Ref ref_of(const Cap& c, float l) {
   Ref r = {fmaxf(l, -FLT_MAX), 0.0f};
-  if constexpr (F == kCapped) r.z = c.a - 2.0f * c.a * cap_r(c, r.l);
+  if constexpr (F == kCapped) r.z = capped<kCapped>(c, r.l);
   return r;
 }
-template <Form F>
+template <Form F, bool NEAR>
 __device__ __forceinline__ void add(const Cap& c, float l, const Ref& ref, float& s, float& w) {
   if constexpr (F == kPlain) {
     // the difference first: exact for logits alike, however large
@@ -332,15 +372,27 @@ __device__ __forceinline__ void add(const Cap& c, float l, const Ref& ref, float
     s += p;
     w += p * fmaxf(d, -160.0f);  // 0, not NaN, where p is 0
   } else if constexpr (F == kCapped) {
-    const float d = c.a - 2.0f * c.a * cap_r(c, l) - ref.z;
+    // (not past the largest logit's by its rounding, which 2^d would not hold under a
+    // very large cap; 0 for the NaN of an infinity's series)
+    const float d = fminf(capped<F, NEAR>(c, l) - ref.z, 0.0f);
     const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(l, kTrace, d));
     s += p;
     w += p * d;
   } else {
-    const float r = cap_r(c, l);
+    const float r = r_of(c.b * l);
     const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(-2.0f * c.a, r, __builtin_fmaf(l, kTrace, c.a)));
     s += p;
     w += p * r;
+  }
+}
+template <Form F, typename IO>
+__device__ __forceinline__ void add8(const Cap& c, const Eight<IO>& e, const Ref& ref, float& s, float& w) {
+  if (F == kCapped && all_near(c, e)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) add<F, true>(c, e.get(j), ref, s, w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) add<F, false>(c, e.get(j), ref, s, w);
   }
 }
 template <Form F>
@@ -384,8 +436,7 @@ __global__ __launch_bounds__(kThreads) void score_sums(ScoreArgs a, Cap c, int p
         ref = to;
       }
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) add<F>(c, e.get(j), ref, s, w);
+    add8<F>(c, e, ref, s, w);
   };
   // the step over the row's start; whole ones, four at a time; what is left
   const int in = static_cast<int>(threadIdx.x) * 8;
@@ -440,8 +491,7 @@ __global__ __launch_bounds__(kThreads) void score_top(ScoreArgs a, Cap c, int pi
 #pragma unroll
   for (int k = 0; k < STEPS; ++k) {
     e[k].repack();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) add<F>(c, e[k].get(j), ref, s, w);
+    add8<F>(c, e[k], ref, s, w);
     e[k].repack();
   }
   // The top-th largest of the lanes' largest: at least `top` logits reach it, and
@@ -562,7 +612,7 @@ __global__ __launch_bounds__(kThreads) void score_join(ScoreArgs a, Cap c, int p
   if (threadIdx.x < kWave) finish<IO>(a, c, t, u, kept, g);
 }
 
-template <typename IO, bool CAP>
+template <typename IO, Form F>
 __global__ __launch_bounds__(kThreads) void score_backward(ScoreGradArgs a, Cap c, int pieces,
                                                             int len) {
   const int64_t t = blockIdx.x / pieces;
@@ -579,12 +629,28 @@ __global__ __launch_bounds__(kThreads) void score_backward(ScoreGradArgs a, Cap 
   const float both = -(g + h * a.entropy[t]), h2 = -h * kLn2;
   const int at = counts ? static_cast<int>(target) : -1;
   // a logit's gradient, in which the target's own g is missing; q: z'
-  auto gradient = [&](float l, float& q) {
-    if constexpr (CAP) {
-      const float r = cap_r(c, l), r4 = 4.0f * r;
+  auto gradient = [&](auto near, float l, float& q) {
+    if constexpr (F == kSmall) {
+      const float r = r_of(c.b * l), r4 = 4.0f * r;
       const float logp = __builtin_fmaf(-2.0f * c.a, r, c.a - lse2);
       const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(l, kTrace, logp));
       q = __builtin_fmaf(-r4, r, r4);
+      return p * __builtin_fmaf(h2, logp, both) * q;
+    } else if constexpr (F == kCapped) {
+      // as capped, with z' of the same terms
+      const float x = c.b * l, t = tanh_series(x);
+      float z = c.a * t;
+      q = __builtin_fmaf(-t, t, 1.0f);
+      if constexpr (!decltype(near)::value) {
+        const float r = r_of(fabsf(x)), r4 = 4.0f * r;
+        const float far = __builtin_copysignf(c.a - 2.0f * c.a * r, x), far_q = __builtin_fmaf(-r4, r, r4);
+        const bool low = fabsf(l) < c.near;
+        z = low ? z : far;
+        q = low ? q : far_q;
+      }
+      const float logp = fminf(z - lse2, 0.0f);
+      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(l, kTrace, logp));
+      q = l == -INFINITY ? 0.0f : q;
       return p * __builtin_fmaf(h2, logp, both) * q;
     } else {
       q = 1.0f;
@@ -594,13 +660,18 @@ __global__ __launch_bounds__(kThreads) void score_backward(ScoreGradArgs a, Cap 
   };
   auto use = [&](Eight<IO>& e, int i) {
     float d[8], q;
+    if (F == kCapped && all_near(c, e)) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) d[j] = gradient(e.get(j), q);
+      for (int j = 0; j < 8; ++j) d[j] = gradient(std::true_type(), e.get(j), q);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = gradient(std::false_type(), e.get(j), q);
+    }
     if (at >= i && at < i + 8) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (at == i + j && e.get(j) != -INFINITY) {
-          gradient(e.get(j), q);
+          gradient(std::false_type(), e.get(j), q);
           d[j] += g * q;
         }
     }
@@ -688,10 +759,16 @@ hipError_t backward(const ScoreGradArgs& a, hipStream_t s) {
   const Cap c = make_cap(a.softcap, a.scale);
   const Cut k = cut(a.V, steps_for(a.T, a.V, kMaxSteps), 7);
   const dim3 grid(a.T * k.pieces), block(kThreads);
-  if (c.on)
-    hipLaunchKernelGGL((score_backward<IO, true>), grid, block, 0, s, a, c, k.pieces, k.len);
-  else
-    hipLaunchKernelGGL((score_backward<IO, false>), grid, block, 0, s, a, c, k.pieces, k.len);
+  switch (form_of(c)) {
+    case kPlain:
+      hipLaunchKernelGGL((score_backward<IO, kPlain>), grid, block, 0, s, a, c, k.pieces, k.len);
+      break;
+    case kCapped:
+      hipLaunchKernelGGL((score_backward<IO, kCapped>), grid, block, 0, s, a, c, k.pieces, k.len);
+      break;
+    default:
+      hipLaunchKernelGGL((score_backward<IO, kSmall>), grid, block, 0, s, a, c, k.pieces, k.len);
+  }
   return hipGetLastError();
 }
 

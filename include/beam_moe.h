@@ -620,8 +620,8 @@ int beam_moe_token_logprobs_workspace_bytes(int64_t T, int64_t V, int32_t top, s
  * -infinity and entropy 0.  A mask of the type's lowest value is a logit like any
  * other (a row of only those is uniform, at any scale); a logp past binary32's
  * range is -infinity.  A NaN or +infinity makes its row's results NaN.
- * A capped z is off by at most 16 scale softcap 2^-24, so a cap is meant to be near
- * the logits' size.
+ * A capped z is off by at most 16 scale softcap 2^-24 where scale softcap is up to
+ * 66, past it by 20 |z| 2^-24.
  * 0 <= top <= min(16, V); softcap >= 0, scale > 0; 3 scale, 3 scale softcap and 3 /
  * softcap in binary32's range; V <= 2^24, T < 2^23. */
 int beam_moe_token_logprobs(int64_t T, int64_t V, int32_t dtype, const void* logits,

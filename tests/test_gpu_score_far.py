@@ -5,7 +5,7 @@ logits.
 Tolerances count roundings of u = 2^-24, in nats.  Without a cap a word's
 distance to its row's largest logit is one difference and two products (3 u of
 it; past 104 nats a probability is 0), its exponential 4 u; a capped z past a cap
-of 34 is off by 20 u of itself.  A thread adds V / 256 terms one by one, and the
+of 66 is off by 20 u of itself.  A thread adds V / 256 terms one by one, and the
 joining of threads and pieces 64 more, u each, all of one sign.  The logarithm of
 a sum adds 4 u of itself."""
 import math
