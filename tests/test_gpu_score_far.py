@@ -105,3 +105,89 @@ def test_masks_of_the_lowest_value_under_a_scale(V, scale, dtype):
     got = gl.token_logprobs(x.to(dev), torch.tensor([0, 4, 0], device=dev), scale=scale)["logprobs"].cpu().double()
     far = low * scale if abs(low * scale) <= MOST else -math.inf
     assert all(v == far or abs(v - far) <= 4 * U * abs(far) for v in got[:2].tolist())
+
+
+# the sums of rows of 3 words or fewer pieces, of pieces, and of one piece a row
+SIZES = [(6, 7), (5, 40003), (1100, 517)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("scale", [1.0, 1.25])
+@pytest.mark.parametrize("T,V", SIZES)
+def test_gradient_of_rows_of_one_value(T, V, scale, dtype):
+    info, dev = torch.finfo(dtype), device()
+    g = torch.Generator().manual_seed(T)
+    x = (torch.randn(T, V, generator=g) * 4).to(dtype)
+    x[0], x[1], x[2, :] = info.min, info.max, -1e30
+    x[3, ::2] = info.min
+    t = torch.randint(-1, V, (T,), generator=g)
+    t[:3] = torch.tensor([1, V - 1, 0])
+    d_l, d_h = torch.randn(T, generator=g), torch.randn(T, generator=g)
+    got = gl.token_logprobs(x.to(dev), t.to(dev), scale=scale)
+    for a, b in ((d_l, None), (None, d_h), (d_l, d_h)):
+        d = gl.token_logprobs_backward(x.to(dev), got["lse"], got["entropy"], t.to(dev), None if a is None else a.to(dev),
+                                       None if b is None else b.to(dev), scale=scale)
+        check_gradient(x, t, a, b, d, 0.0, scale)
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.7])
+@pytest.mark.parametrize("offset", [300.0, 1e4, -1e4, 1e6])
+@pytest.mark.parametrize("T,V", SIZES)
+def test_gradient_of_logits_with_an_offset(T, V, offset, scale):
+    dev, g = device(), torch.Generator().manual_seed(V)
+    x = torch.randn(T, V, generator=g) * 4
+    x[::3] += offset               # beside rows without one
+    t = torch.randint(0, V, (T,), generator=g)
+    d_l, d_h = torch.randn(T, generator=g), torch.randn(T, generator=g)
+    dx, dt, da, db = x.to(dev), t.to(dev), d_l.to(dev), d_h.to(dev)
+    got = gl.token_logprobs(dx, dt, scale=scale)
+    d = gl.token_logprobs_backward(dx, got["lse"], got["entropy"], dt, da, db, scale=scale)
+    check_gradient(x, t, d_l, d_h, d, 0.0, scale)
+    # in the logits' place, and into rows that start elsewhere
+    wide = torch.full((T, V + 5), 9.0, device=dev)
+    gl.token_logprobs_backward(dx, got["lse"], got["entropy"], dt, da, db, scale=scale, out=wide[:, :V])
+    assert torch.equal(wide[:, :V], d) and (wide[:, V:] == 9.0).all()
+    gl.token_logprobs_backward(dx, got["lse"], got["entropy"], dt, da, db, scale=scale, out=dx)
+    assert torch.equal(dx, d)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,V", SIZES)
+def test_gradient_under_a_cap_past_every_sum(T, V, dtype):
+    # words that lie further apart than any sum reaches, beside ordinary ones
+    dev, g = device(), torch.Generator().manual_seed(V)
+    x = (torch.randn(T, V, generator=g) * 4).to(dtype)
+    x[2] = (torch.randn(V, generator=g) * 3e29).clamp(max=1.5e30).to(dtype)
+    x[2, 5] = 2e30        # (the next one's tanh is 0.06 less: far from a tie in binary32)
+    t = torch.randint(0, V, (T,), generator=g)
+    t[2] = 5
+    d_l, d_h = torch.randn(T, generator=g), torch.randn(T, generator=g)
+    got = gl.token_logprobs(x.to(dev), t.to(dev), softcap=1e30)
+    d = gl.token_logprobs_backward(x.to(dev), got["lse"], got["entropy"], t.to(dev), d_l.to(dev), d_h.to(dev), softcap=1e30)
+    keep = torch.arange(T) != 2
+    check_gradient(x[keep], t[keep], d_l[keep], d_h[keep], d[keep.to(dev)], 1e30, 1.0)
+    # p is 1 for the largest word, and the gradient 0 but for a product's rounding
+    assert got["logprobs"][2] == 0 and got["entropy"][2] == 0 and (d[2].abs() <= 4 * U * d_l[2].abs().item()).all()
+
+
+def test_far_rows_in_a_graph():
+    # captured once, replayed over rows that are near and far in turn
+    dev, g = device(), torch.Generator().manual_seed(8)
+    T, V = 5, 40003
+    x = torch.randn(T, V, generator=g).to(dev) * 4
+    t, d_l, d_h = (v.to(dev) for v in (torch.randint(0, V, (T,), generator=g), torch.randn(T, generator=g),
+                                       torch.randn(T, generator=g)))
+
+    def step(y):
+        got = gl.token_logprobs(y, t)
+        return gl.token_logprobs_backward(y, got["lse"], got["entropy"], t, d_l, d_h)
+
+    held, graph = x.clone(), torch.cuda.CUDAGraph()
+    step(held)
+    with torch.cuda.graph(graph):
+        out = step(held)
+    for offsets in ([0] * 5, [1e4, 0, -1e5, 0, 300], [0, 1e6, 0, 0, 0], [0] * 5):
+        held.copy_(x + torch.tensor(offsets, device=dev)[:, None])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, step(held))
