@@ -142,8 +142,9 @@ struct Shared {
 // Lane groups of LPH lanes hold a head; a wave takes 64 / LPH heads at a step:
 // first the queries', then the keys', then the values' (which are copied).
 // `parts` waves share a token.  Loads are never masked (a lane without a head
-// reads its step's last one), so that the next step's are on their way while one
-// is worked on; stores are.
+// reads its step's last one, one past D the head's first values, which stay out of
+// the head's sums), so that the next step's are on their way while one is worked
+// on; stores are.
 template <typename IO, int LPH>
 __global__ __launch_bounds__(kRopeWaves* kWave) void rope_forward(RopeArgs a, int parts) {
   constexpr int kHeads = kWave / LPH;
@@ -173,7 +174,7 @@ __global__ __launch_bounds__(kRopeWaves* kWave) void rope_forward(RopeArgs a, in
   const int64_t at = a.cache.k ? place(a, t, pos) : -1;
   Turn tn;
   make_turn<LPH>(a, pos, sh.freq, sh.pairs[wave], lane, tn);
-  const float per = in ? 1.0f / static_cast<float>(a.D) : 0.0f;
+  const float per = 1.0f / static_cast<float>(a.D);
   // y = inv (c v + s o) with the weights and the scale in c and s
   float c[8], s[8];
   auto factors = [&](const float* w, float scale) {
@@ -192,7 +193,7 @@ __global__ __launch_bounds__(kRopeWaves* kWave) void rope_forward(RopeArgs a, in
       x[j] = e.get(j);
       ss += x[j] * x[j];
     }
-    const float inv = __builtin_amdgcn_rsqf(head_sum<LPH>(ss * per) + a.eps);
+    const float inv = __builtin_amdgcn_rsqf(head_sum<LPH>(in ? ss * per : 0.0f) + a.eps);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = (x[j] * c[j] + o[j] * s[j]) * inv;
     e.set(x);
@@ -252,7 +253,7 @@ __global__ __launch_bounds__(kRopeWaves* kWave) void rope_backward(RopeGradArgs 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const bool in = lane % LPH * 8 < a.D;
   const int col = in ? lane % LPH * 8 : 0, sub = lane / LPH;
-  const float per = in ? 1.0f / static_cast<float>(a.D) : 0.0f;
+  const float per = 1.0f / static_cast<float>(a.D);
   sh.stage(a);
   float acc[2][8] = {};
   const int64_t every = static_cast<int64_t>(gridDim.x) * kRopeWaves;
@@ -292,7 +293,7 @@ __global__ __launch_bounds__(kRopeWaves* kWave) void rope_backward(RopeGradArgs 
           ss += v[j] * v[j];
           d[j] = (nd.get(j) * tn.c[j] - o[j] * tn.s[j]) * scale;
         }
-        const float inv = __builtin_amdgcn_rsqf(head_sum<LPH>(ss * per) + a.eps);
+        const float inv = __builtin_amdgcn_rsqf(head_sum<LPH>(in ? ss * per : 0.0f) + a.eps);
         const bool live = in && i * kHeads + sub < H;
         float dot = 0.0f;
 #pragma unroll
@@ -302,7 +303,7 @@ __global__ __launch_bounds__(kRopeWaves* kWave) void rope_backward(RopeGradArgs 
           d[j] *= w[j];
           dot += d[j] * v[j];
         }
-        const float mean = head_sum<LPH>(dot * per);
+        const float mean = head_sum<LPH>(in ? dot * per : 0.0f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] = inv * (d[j] - v[j] * mean);
         if (live) {
