@@ -1,5 +1,6 @@
 // C ABI of the operators around a paged key-value cache: host-side checks, then
 // the launches.  See include/beam_moe.h for the contract of every entry point.
+#include <float.h>
 #include <math.h>
 
 #include "serve.h"
@@ -37,6 +38,9 @@ int check_rope(int64_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype, int
   if (!(eps > 0.0f) || !isfinite(eps) || !(temp_length >= 0.0f) || !isfinite(temp_length) ||
       !isfinite(temp_exponent))
     return BEAM_ERR_INVALID_ARG;
+  // the inverse root of a number below binary32's normal ones is infinite, and NaN times
+  // a head of zeros
+  if (eps < FLT_MIN) return BEAM_ERR_UNSUPPORTED;
   // a launch holds fewer than 2^32 threads, 64 a token
   if (rot % 16 || T >= (int64_t{1} << 25) || T * (Hq + 2 * Hkv) >= (int64_t{1} << 31))
     return BEAM_ERR_UNSUPPORTED;

@@ -462,7 +462,8 @@ int beam_moe_norm_residual_backward(int64_t T, int64_t H, int32_t dtype, const v
  *               tokens may name one place.
  * Squares are binary32: a head whose sum of them passes its range gives zeros and no
  * gradients (NaN where a weighted value passes the range as well).
- * Outputs do not overlap inputs.  T * (Hq + 2 Hkv) < 2^31, Hq, Hkv <= 4096.
+ * Outputs do not overlap inputs.  T * (Hq + 2 Hkv) < 2^31, Hq, Hkv <= 4096, eps >=
+ * 2^-126.
  * No workspace. */
 int beam_moe_qk_norm_rope(int64_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t dtype,
                           const void* q, int64_t q_stride, const void* k, int64_t k_stride,
