@@ -760,6 +760,19 @@ def _dtype_code(name: str, dtype: torch.dtype) -> int:
     raise ValueError(f"{name}: dtype {dtype}, expected torch.bfloat16 or torch.float32")
 
 
+def _values(keep: list, on, name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple) -> int:
+    """Address of indices, lengths or scalars, as _arg.  The library wants every
+    array to begin on 16 bytes; a view that begins between (tokens[1:], the rows of
+    a batch from n on) is copied on the call's stream first, into `keep`, which
+    the caller holds until its call is queued."""
+    p = _arg(name, t, dev, dtype, shape)
+    if p % 16 == 0:
+        return p
+    with _alloc_on(None if on is True else on):
+        keep.append(t.clone())
+    return keep[-1].data_ptr()
+
+
 def _heads(name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple):
     """Address and token stride of heads [T, H, D] whose heads and values are
     contiguous (a view of a projection's output)."""
@@ -781,7 +794,7 @@ def _empty_like(on, device, dtype: torch.dtype, *shape) -> torch.Tensor:
         return torch.empty(*shape, dtype=dtype, device=device)
 
 
-def _cache_args(k_cache, v_cache, tables, dev: int, dtype: torch.dtype, Hkv: int, D: int):
+def _cache_args(keep: list, on, k_cache, v_cache, tables, dev: int, dtype: torch.dtype, Hkv: int, D: int):
     """Checked arguments of a cache: (k, v, page, token and head stride, pages,
     page size, tables, seqs, table columns)."""
     if k_cache.dim() != 4 or tables is None or tables.dim() != 2:
@@ -797,32 +810,32 @@ def _cache_args(k_cache, v_cache, tables, dev: int, dtype: torch.dtype, Hkv: int
         raise ValueError(f"strides of k_cache {stride} and v_cache {v_cache.stride()}: expected the "
                          "same, values contiguous")
     return (k_cache.data_ptr(), v_cache.data_ptr(), stride[0], stride[1], stride[2], shape[0], shape[1],
-            _arg("tables", tables, dev, torch.int32, cols), *cols)
+            _values(keep, on, "tables", tables, dev, torch.int32, cols), *cols)
 
 
-def _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq, temperature):
+def _rope_inputs(keep: list, stream, q, k, q_weight, k_weight, positions, inv_freq, temperature):
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError(f"shapes {tuple(q.shape)} and {tuple(k.shape)}, expected [T, heads, D]")
     T, Hq, D = q.shape
     Hkv, dev, dtype = k.shape[1], q.get_device(), q.dtype
-    code = _dtype_code("q", dtype)
+    code, on = _dtype_code("q", dtype), _on(stream, dev)
     pq, sq = _heads("q", q, dev, dtype, (T, Hq, D))
     pk, sk = _heads("k", k, dev, dtype, (T, Hkv, D))
-    wq = _arg("q_weight", q_weight, dev, torch.float32, (D,))
-    wk = _arg("k_weight", k_weight, dev, torch.float32, (D,))
+    wq = _values(keep, on, "q_weight", q_weight, dev, torch.float32, (D,))
+    wk = _values(keep, on, "k_weight", k_weight, dev, torch.float32, (D,))
     pp = pf = None
     rot = 0
     if positions is not None:
-        pp = _arg("positions", positions, dev, torch.int32, (T,))
+        pp = _values(keep, on, "positions", positions, dev, torch.int32, (T,))
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        pf = _arg("inv_freq", inv_freq, dev, torch.float64, (rot // 2,))
+        pf = _values(keep, on, "inv_freq", inv_freq, dev, torch.float64, (rot // 2,))
     length, exponent = (0.0, 0.0) if temperature is None else temperature
     if temperature is not None and not length > 0:
         raise ValueError(f"temperature {temperature}: its length has to be positive")
     if positions is None and (rot or temperature is not None) and T:
         raise ValueError("rotation and temperature need positions")
-    return T, Hq, Hkv, D, dev, dtype, code, pq, sq, pk, sk, wq, wk, pp, pf, rot, length, exponent
+    return T, Hq, Hkv, D, dev, on, dtype, code, pq, sq, pk, sk, wq, wk, pp, pf, rot, length, exponent
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
@@ -840,9 +853,10 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_wei
     v [T,Hkv,D] go to their places: positions in sequence rows [T] int32 (None:
     token t in sequence t).  Returns (q_out, k_out); k_out is None with a cache
     but where with_k asks for it."""
-    (T, Hq, Hkv, D, dev, dtype, code, pq, sq, pk, sk, wq, wk, pp, pf, rot, length,
-     exponent) = _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq, temperature)
-    device, on = q.device, _on(stream, dev)
+    keep = []
+    (T, Hq, Hkv, D, dev, on, dtype, code, pq, sq, pk, sk, wq, wk, pp, pf, rot, length,
+     exponent) = _rope_inputs(keep, stream, q, k, q_weight, k_weight, positions, inv_freq, temperature)
+    device = q.device
     pv, sv, pr = None, 0, None
     cache = (None, None, 0, 0, 0, 0, 0, None, 0, 0)
     if k_cache is not None or v_cache is not None:
@@ -850,10 +864,10 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_wei
             raise ValueError("a cache is k_cache and v_cache, and takes v")
         if positions is None:
             raise ValueError("a cache needs positions")
-        cache = _cache_args(k_cache, v_cache, tables, dev, dtype, Hkv, D)
+        cache = _cache_args(keep, on, k_cache, v_cache, tables, dev, dtype, Hkv, D)
         pv, sv = _heads("v", v, dev, dtype, (T, Hkv, D))
         if rows is not None:
-            pr = _arg("rows", rows, dev, torch.int32, (T,))
+            pr = _values(keep, on, "rows", rows, dev, torch.int32, (T,))
         elif cache[8] != T:
             raise ValueError(f"{cache[8]} sequences for {T} tokens: rows says which is whose")
     elif v is not None or tables is not None or rows is not None or with_k is False:
@@ -879,9 +893,10 @@ def qk_norm_rope_backward(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: torch
     """beam_moe_qk_norm_rope_backward: from the gradients of q_out and k_out
     (contiguous) a dict: d_q and d_k in q's dtype, d_q_weight and d_k_weight [D]
     fp32.  The other arguments are the forward's."""
-    (T, Hq, Hkv, D, dev, dtype, code, pq, sq, pk, sk, wq, wk, pp, pf, rot, length,
-     exponent) = _rope_inputs(q, k, q_weight, k_weight, positions, inv_freq, temperature)
-    device, on = q.device, _on(stream, dev)
+    keep = []
+    (T, Hq, Hkv, D, dev, on, dtype, code, pq, sq, pk, sk, wq, wk, pp, pf, rot, length,
+     exponent) = _rope_inputs(keep, stream, q, k, q_weight, k_weight, positions, inv_freq, temperature)
+    device = q.device
     pdq = _arg("d_q_out", d_q_out, dev, dtype, (T, Hq, D))
     pdk = _arg("d_k_out", d_k_out, dev, dtype, (T, Hkv, D))
     need = _size_of("beam_moe_qk_norm_rope_workspace_bytes", T, Hq, Hkv, D)
@@ -916,10 +931,11 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     code = _dtype_code("q", dtype)
     device, on = q.device, _on(stream, dev)
     pq = _arg("q", q, dev, dtype, shape)
-    cache = _cache_args(k_cache, v_cache, tables, dev, dtype, Hkv, D)
+    keep = []
+    cache = _cache_args(keep, on, k_cache, v_cache, tables, dev, dtype, Hkv, D)
     if cache[8] != B:
         raise ValueError(f"tables of {cache[8]} sequences for {B} queries")
-    pl = _arg("lengths", lengths, dev, torch.int32, (B,))
+    pl = _values(keep, on, "lengths", lengths, dev, torch.int32, (B,))
     pg = None if gate is None else _arg("gate", gate, dev, dtype, shape)
     need = _size_of("beam_moe_paged_attention_workspace_bytes", B, Hq, Hkv, D)
     if out is None:
@@ -963,15 +979,16 @@ def _pools(pools, pages: int, dev: int) -> bytes:
     return _pack_pools(len(pools), layers, *base, *size, *by_layer, *by_page)
 
 
-def _pages_inputs(tables, lengths, refs, page_size: int):
+def _pages_inputs(keep: list, stream, tables, lengths, refs):
     if tables.dim() != 2 or refs.dim() != 1:
         raise ValueError(f"tables {tuple(tables.shape)} and refs {tuple(refs.shape)}, expected [rows, "
                          "columns] and [pages]")
     rows, cols = tables.shape
-    pages, dev = refs.shape[0], refs.get_device()
-    return (rows, cols, pages, dev, _arg("tables", tables, dev, torch.int32, (rows, cols)),
-            _arg("lengths", lengths, dev, torch.int32, (rows,)),
-            _arg("refs", refs, dev, torch.int32, (pages,)))
+    pages, dev, i32 = refs.shape[0], refs.get_device(), torch.int32
+    on = _on(stream, dev)
+    return (rows, cols, pages, dev, on, _values(keep, on, "tables", tables, dev, i32, (rows, cols)),
+            _values(keep, on, "lengths", lengths, dev, i32, (rows,)),
+            _values(keep, on, "refs", refs, dev, i32, (pages,)))
 
 
 def _pages_scratch(pages: int, rows: int, workspace, device, stream):
@@ -990,11 +1007,12 @@ def pages_update(tables: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor
     arrays [layers,pages,...] whose shared last pages are copied before they are
     written.  All int32.  Returns a dict: tables, lengths (with the growth), refs,
     and missing [1], the pages that were wanted and not to be had."""
-    old, cols, pages, dev, pt, pl, pr = _pages_inputs(tables, lengths, refs, page_size)
+    keep, i32 = [], torch.int32
+    old, cols, pages, dev, on, pt, pl, pr = _pages_inputs(keep, stream, tables, lengths, refs)
     rows = old if parents is None else parents.shape[0]
-    pp = None if parents is None else _arg("parents", parents, dev, torch.int32, (rows,))
-    pg = None if grow is None else _arg("grow", grow, dev, torch.int32, (rows,))
-    device, on, i32 = refs.device, _on(stream, dev), torch.int32
+    pp = None if parents is None else _values(keep, on, "parents", parents, dev, i32, (rows,))
+    pg = None if grow is None else _values(keep, on, "grow", grow, dev, i32, (rows,))
+    device = refs.device
     p = _pools(pools, pages, dev)
     out = {"tables": _empty(on, device, i32, rows, cols), "lengths": _empty(on, device, i32, rows),
            "refs": _empty(on, device, i32, pages), "missing": _empty(on, device, i32, 1)}
@@ -1010,8 +1028,9 @@ def pages_compact(tables: torch.Tensor, lengths: torch.Tensor, refs: torch.Tenso
     """beam_moe_pages_compact: the used pages (refs > 0) moved to the pool's
     front, in the arrays of pools too.  Returns a dict: tables and refs with the
     new ids, new_id [pages] (-1: free) and live [1], how many there are."""
-    rows, cols, pages, dev, pt, pl, pr = _pages_inputs(tables, lengths, refs, page_size)
-    device, on, i32 = refs.device, _on(stream, dev), torch.int32
+    keep, i32 = [], torch.int32
+    rows, cols, pages, dev, on, pt, pl, pr = _pages_inputs(keep, stream, tables, lengths, refs)
+    device = refs.device
     p = _pools(pools, pages, dev)
     out = {"tables": _empty(on, device, i32, rows, cols), "refs": _empty(on, device, i32, pages),
            "new_id": _empty(on, device, i32, pages), "live": _empty(on, device, i32, 1)}
@@ -1028,11 +1047,11 @@ def pages_copy(pools, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None
     if not pools or pools[0].dim() < 2:
         raise ValueError("pools: at least one array [layers, pages, ...]")
     n, dev, pages = src.shape[0], src.get_device(), pools[0].shape[1]
-    ps = _arg("src", src, dev, torch.int32, (n,))
-    pd = _arg("dst", dst, dev, torch.int32, (n,))
+    keep, on = [], _on(stream, dev)
+    ps = _values(keep, on, "src", src, dev, torch.int32, (n,))
+    pd = _values(keep, on, "dst", dst, dev, torch.int32, (n,))
     p = _pools(pools, pages, dev)
-    _run(lib().beam_moe_pages_copy, "beam_moe_pages_copy", _on(stream, dev), dev, (src, dst, *pools),
-         p, pages, n, ps, pd)
+    _run(lib().beam_moe_pages_copy, "beam_moe_pages_copy", on, dev, (src, dst, *pools), p, pages, n, ps, pd)
 
 
 def _logits(name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple):
@@ -1046,7 +1065,8 @@ def _logits(name: str, t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tup
 def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, softcap: float = 0.0,
                    scale: float = 1.0, top: int = 0, workspace: Optional[Workspace] = None,
                    stream=None) -> dict:
-    """beam_moe_token_logprobs of logits [T,V] (bf16 or fp32, rows any stride):
+    """beam_moe_token_logprobs of logits [T,V] (bf16 or fp32, rows any stride, the
+    first on 16 bytes):
     z = scale * softcap * tanh(l / softcap) (softcap 0: scale * l).  Returns a
     dict of fp32 [T]: lse, entropy, with targets [T] int64 logprobs (0 where the
     target is outside [0, V)); with top > 0 also top_ids [T,top] int32 and
@@ -1056,8 +1076,8 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     (T, V), dev = logits.shape, logits.get_device()
     code = _dtype_code("logits", logits.dtype)
     pl, stride = _logits("logits", logits, dev, logits.dtype, (T, V))
-    pt = None if targets is None else _arg("targets", targets, dev, torch.int64, (T,))
-    device, on, f32 = logits.device, _on(stream, dev), torch.float32
+    device, on, f32, keep = logits.device, _on(stream, dev), torch.float32, []
+    pt = None if targets is None else _values(keep, on, "targets", targets, dev, torch.int64, (T,))
     need = _size_of("beam_moe_token_logprobs_workspace_bytes", T, V, top)
     out = {"lse": _empty(on, device, f32, T), "entropy": _empty(on, device, f32, T)}
     lp = ids = tl = None
@@ -1093,11 +1113,13 @@ def token_logprobs_backward(logits: torch.Tensor, lse: torch.Tensor, entropy: to
     (T, V), dev, f32 = logits.shape, logits.get_device(), torch.float32
     code = _dtype_code("logits", logits.dtype)
     pl, stride = _logits("logits", logits, dev, logits.dtype, (T, V))
-    ps, pe = _arg("lse", lse, dev, f32, (T,)), _arg("entropy", entropy, dev, f32, (T,))
-    pt = None if targets is None else _arg("targets", targets, dev, torch.int64, (T,))
-    pdl = None if d_logprobs is None else _arg("d_logprobs", d_logprobs, dev, f32, (T,))
-    pde = None if d_entropy is None else _arg("d_entropy", d_entropy, dev, f32, (T,))
-    on = _on(stream, dev)
+    on, keep = _on(stream, dev), []
+
+    def row_values(name, t, dtype=f32):
+        return None if t is None else _values(keep, on, name, t, dev, dtype, (T,))
+    ps, pe = row_values("lse", lse), row_values("entropy", entropy)
+    pt = row_values("targets", targets, torch.int64)
+    pdl, pde = row_values("d_logprobs", d_logprobs), row_values("d_entropy", d_entropy)
     if out is None:
         out = _empty(on, logits.device, logits.dtype, T, V)
     po, so = _logits("out", out, dev, logits.dtype, (T, V))
