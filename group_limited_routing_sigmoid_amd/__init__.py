@@ -765,9 +765,11 @@ def _values(keep: list, on, name: str, t: torch.Tensor, dev: int, dtype: torch.d
     array to begin on 16 bytes; a view that begins between (tokens[1:], the rows of
     a batch from n on) is copied on the call's stream first, into `keep`, which
     the caller holds until its call is queued."""
-    p = _arg(name, t, dev, dtype, shape)
-    if p % 16 == 0:
-        return p
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0 and t.is_contiguous():
+        p = t.data_ptr()
+        if not p & 15:
+            return p
+    _arg(name, t, dev, dtype, shape)  # raises for all but where the view begins
     with _alloc_on(None if on is True else on):
         keep.append(t.clone())
     return keep[-1].data_ptr()
