@@ -142,10 +142,6 @@ struct Eight {
     for (int i = 0; i < kWords; ++i)
       __builtin_nontemporal_store(w[i], reinterpret_cast<u32x4*>(p + i * (8 / kWords)));
   }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = u32x4{0, 0, 0, 0};
-  }
   // Makes the compiler forget values it has unpacked (it would rather keep them,
   // in twice the registers, than unpack again).
   __device__ __forceinline__ void repack() {
