@@ -642,7 +642,9 @@ int beam_moe_token_logprobs(int64_t T, int64_t V, int32_t dtype, const void* log
  * A target outside [0, V) has no gradient of its logprob.  Probabilities come from
  * z and the binary32 lse, off by 2^-18 for its rounding; where |lse| is 128 or more,
  * from the row's largest logit and the sum beside it, formed again by one workgroup a
- * row, so that rows far from 0 have the gradients of rows near it.  No workspace. */
+ * row, so that rows far from 0 have the gradients of rows near it (unless they do not
+ * make the given lse, as where the row is a shard of a vocabulary and lse the whole's:
+ * then p has lse's rounding).  No workspace. */
 int beam_moe_token_logprobs_backward(int64_t T, int64_t V, int32_t dtype, const void* logits,
                                      int64_t row_stride, const int64_t* targets, float softcap,
                                      float scale, const float* lse, const float* entropy,

@@ -191,3 +191,23 @@ def test_far_rows_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, step(held))
+
+
+@pytest.mark.parametrize("offset", [0.0, 300.0, -2000.0])
+def test_entropy_gradient_of_a_shard(offset):
+    # half of a vocabulary each, with the whole's lse and entropy (a target outside the
+    # half has no gradient of its logprob, so that the entropy's is what can be cut)
+    dev, g = device(), torch.Generator().manual_seed(9)
+    T, V = 40, 9000
+    x = torch.randn(T, V, generator=g) * 4 + offset
+    d_h = torch.randn(T, generator=g)
+    whole = gl.token_logprobs(x.to(dev))
+    got = torch.cat([gl.token_logprobs_backward(h.contiguous().to(dev), whole["lse"], whole["entropy"], d_entropy=d_h.to(dev))
+                     for h in x.split(V // 2, 1)], 1).cpu().double()
+    want, size = (ref.score_grad(level(x), None, None, d_h, absolute=a) for a in (False, True))
+    r = ref.score(level(x))
+    dp, ls, dh = parts(r, 0.0, 1.0)
+    dp = dp + U * ref.score(x)["lse"].abs()          # lse's own rounding
+    tol = (2 * (dp + ls) + 8 * U)[:, None] * size
+    tol = tol + d_h.abs().double()[:, None] * torch.exp(r["logp"]) * 2 * (dp + ls + dh)[:, None]
+    assert ((got - want).abs() <= tol + U * want.abs() + 2.0 ** -120).all()
