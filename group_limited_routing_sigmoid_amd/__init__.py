@@ -738,7 +738,8 @@ def norm_residual_backward(residual_out: torch.Tensor,
 
 def rope_frequencies(rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """Radians a position of each of rot / 2 pairs, base^(-2 i / rot), in binary64
-    as qk_norm_rope takes them."""
+    as qk_norm_rope takes them.  Made on the host and copied, which waits for the
+    GPU: once, not in every step."""
     if rot < 0 or rot % 2:
         raise ValueError(f"rot {rot}: pairs of channels turn")
     return base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1)).to(device)

@@ -11,11 +11,12 @@
 // and every output written once: both directions are bound by those bytes.  A
 // wave stays with one token: each lane takes the sine and cosine of one pair
 // (two at D > 128) and all heads of the token take theirs from LDS.  An angle
-// is reduced in binary64, in quarter turns, so that what is left is exact to
-// 2^-26 of a quarter turn at any position.  One token a wave and the next step's
-// loads ahead of the work: 16,381 tokens of 48 + 8 heads of 128 into a cache take
-// 101 us (5.3 TB/s); waves that stay for several tokens, with loads ahead across
-// them, took 139, and two to eight waves a token 119 to 173.
+// is reduced in binary64, in quarter turns: what is left is off by 2^-26 of a quarter
+// turn and by 2^-52 of the turns taken off (two roundings of them, 2^-22 near position
+// 2^30 at a radian each).  One token a wave and the next step's loads ahead of the
+// work: 16,381 tokens of 48 + 8 heads of 128 into a cache take 101 us (5.3 TB/s; fp32
+// 231, 4.6); waves that stay for several tokens, with loads ahead across them, took
+// 139, and two to eight waves a token 119 to 173.
 #include <algorithm>
 
 #include "serve.h"

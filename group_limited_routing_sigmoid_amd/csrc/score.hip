@@ -1,5 +1,6 @@
 // Log probabilities of given tokens with the entropy of the distribution and
-// its best alternatives, in one reading of the logits, and their gradient:
+// its best alternatives, in one reading of the logits (ordinary ones), and their
+// gradient:
 //   z = scale cap tanh(l / cap)      (no cap: scale l)
 //   logp = z - ln S,  S = sum exp(z),  entropy = ln S - sum z exp(z) / S
 //   dl_j = z'(l_j) (g ([j = target] - p_j) - h p_j (logp_j + entropy))
@@ -14,11 +15,15 @@
 // of at most 16,384 logits, is held in registers (the cap keeps the order, so the
 // raw logits are compared): the n-th largest of a wave's lanes' largest is a bar
 // that at least n logits reach and few more, those meet in LDS, and each finds its
-// rank by counting (2,048 x 131,072 bf16 with 16: 204 us, 5: 151; one after
-// another by the wave's largest 562 and 240).  A second kernel joins a row's
-// pieces.  Bound by reading the logits; with the cap by two exponentials and a
-// reciprocal an element as much (4,096 x 100,003 bf16: 165 to 195 us as the clock
-// holds, 4.2 to 5.0 TB/s; the gradient 308, 5.3 TB/s).
+// rank by counting (2,048 x 131,072 bf16 with 16: 201 us, 5: 142, none: 100; one
+// after another by the wave's largest 562 and 240).  A wave whose lanes with any
+// unmasked logit are fewer than the alternatives has no bar, and one with more than
+// 64 equal logits at it no room: those read their logits again for each alternative
+// (50 scattered words a row of the same shape, 16 alternatives: 3.6 ms).  A second
+// kernel joins a row's pieces.  Bound by reading the logits; with the cap by two
+// exponentials and a reciprocal an element as much (4,096 x 100,003 bf16: 165 us among
+// many calls, 5.0 TB/s, 195 to 238 among the first few, as the clock holds; without a
+// cap 148; the gradient 311, 5.3 TB/s).
 #include <algorithm>
 #include <cfloat>
 
@@ -77,9 +82,9 @@ __device__ __forceinline__ void store8(const Eight<IO>& e, IO* p, int64_t n) {
     }
 }
 // Rows start anywhere.  What runs through them steps in whole 16 bytes of memory
-// (4,096 x 100,003 bf16, capped: 161 us, as for 100,000; from the row's start
-// 208), so that its first and last eight may lie over the row's ends: `skew` is
-// how many values the row starts behind such a place.
+// (4,096 x 100,003 bf16, capped: 166 us, 100,000 164), so that its first and last
+// eight may lie over the row's ends: `skew` is how many values the row starts behind
+// such a place.
 template <typename IO>
 __device__ __forceinline__ int skew_of(const IO* row) {
   return static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(IO));

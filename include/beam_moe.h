@@ -606,7 +606,9 @@ int beam_moe_pages_compact(int64_t rows, int64_t cols, int64_t pages, int64_t pa
 int beam_moe_token_logprobs_workspace_bytes(int64_t T, int64_t V, int32_t top, size_t* bytes);
 
 /* Log probabilities of given tokens with the entropy of the distribution and
- * its best alternatives, in one reading of the logits, per row t:
+ * its best alternatives, in one reading of the logits (with alternatives, rows with
+ * few unmasked logits or hundreds of equal ones in parts up to `top` times more), per
+ * row t:
  *   z = scale * softcap * tanh(l / softcap)   (softcap 0: z = scale * l)
  *   logp = z - ln sum exp(z)
  * ("Reflection Releases Beam ...", section "Hybrid Attention and Unusual
